@@ -1,0 +1,353 @@
+"""The operators around the adapters' delta when the base model is held in
+microscaled formats: what a serving step calls next to ``lora_add_linear``.
+
+    norm       residual sum and root-mean-square norm; the normalised rows leave once in
+               the data's own type (the adapters' shrink reads them) and, where the base
+               product is microscaled, once as MXFP8
+    quantize   rows to MXFP8 (e4m3) or MXFP4 (e2m1): blocks of 32 along a row, one
+               power-of-two scale each; read back, since what is held in 8 or 4 bits is
+               compared by the values it stands for
+    dequantize microscaled rows back to bf16 or fp32 (a base weight before an adapter is
+               merged into it)
+    linear     y = x W^T with W in MXFP4 and x in MXFP8 or MXFP4: the base product that
+               lora_add_linear's y arrives with
+
+Storage of a microscaled matrix [rows][cols]: cols padded to a multiple of 128 with
+zeros; MXFP8 one byte an element, MXFP4 two elements a byte (the even one in the low
+nibble).  Scales: one byte e per block for 2^(e-127), in tiles of 128 rows x 4 blocks =
+512 bytes; inside a tile row r, block b sits at (r % 32) * 16 + (r // 32) * 4 + b; tiles
+run along a row of tiles first.  A block's e is the exponent of its largest magnitude
+less the format's own largest exponent (8 for e4m3, 2 for e2m1), at least 0.
+"""
+import math
+
+import torch
+
+own = False
+
+BITS = {"mxfp8": 8, "mxfp4": 4}
+DTYPE = {"bf16": torch.bfloat16, "fp32": torch.float32}
+EPS = 1e-5
+
+
+# ------------------------------------------------------------------------ cases
+def listed():
+    return [
+        # one token's hidden state ahead of a microscaled base product: latency
+        {"name": "norm 1 x 4096", "op": "norm", "T": 1, "d": 4096, "dtype": "bf16", "residual": True, "out": "mxfp8"},
+        # a ragged fp32 batch, odd width, no residual, no 8-bit output (adapters alone)
+        {"name": "norm 333 x 1003 fp32", "op": "norm", "T": 333, "d": 1003, "dtype": "fp32", "residual": False,
+         "out": "none"},
+        # the mixed 70B-shaped batch's rows: 8192 tokens of 8192
+        {"name": "norm 8192 x 8192", "op": "norm", "T": 8192, "d": 8192, "dtype": "bf16", "residual": True,
+         "out": "mxfp8"},
+        # a decode batch's input of the down projection
+        {"name": "quantize 256 x 14336 mxfp8", "op": "quantize", "T": 256, "d": 14336, "dtype": "bf16", "out": "mxfp8"},
+        # a base weight at load time (8192 -> 28672 up projection)
+        {"name": "quantize 28672 x 8192 mxfp4", "op": "quantize", "T": 28672, "d": 8192, "dtype": "bf16",
+         "out": "mxfp4"},
+        # ragged fp32 rows: the last block of a row is cut, rows are not 16-byte aligned
+        {"name": "quantize 777 x 1003 fp32", "op": "quantize", "T": 777, "d": 1003, "dtype": "fp32", "out": "mxfp4"},
+        # a gate projection read back before an adapter is merged into it
+        {"name": "dequantize 14336 x 4096 mxfp4", "op": "dequantize", "T": 14336, "d": 4096, "dtype": "bf16",
+         "out": "mxfp4"},
+        # odd sizes, fp32 rows
+        {"name": "dequantize 1003 x 999 mxfp8", "op": "dequantize", "T": 1003, "d": 999, "dtype": "fp32",
+         "out": "mxfp8"},
+        # one token through a q projection: latency, and the weight's bytes
+        {"name": "linear 1 x 4096 x 4096", "op": "linear", "T": 1, "d": 4096, "d_out": 4096, "dtype": "bf16",
+         "out": "mxfp8"},
+        # a decode batch through gate and up: the weight's bytes
+        {"name": "linear 64 x 4096 x 28672", "op": "linear", "T": 64, "d": 4096, "d_out": 28672, "dtype": "bf16",
+         "out": "mxfp8"},
+        # a short prompt, an odd number of rows, the down projection's long sums
+        {"name": "linear 257 x 14336 x 4096", "op": "linear", "T": 257, "d": 14336, "d_out": 4096, "dtype": "bf16",
+         "out": "mxfp8"},
+        # the mixed batch's up projection, both operands in 4 bits: the tensor cores' rate
+        {"name": "linear 8192 x 8192 x 28672", "op": "linear", "T": 8192, "d": 8192, "d_out": 28672, "dtype": "bf16",
+         "out": "mxfp4"},
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return min(hi, max(lo, int(math.exp(rng.uniform(math.log(lo), math.log(hi + 1))))))
+
+
+def _width(rng, lo, hi):
+    """A width: any integer one time in three, else a multiple of 8 or of 128."""
+    n = _log_int(rng, lo, hi)
+    step = rng.choice([1, 8, 128])
+    return max(step, n // step * step)
+
+
+def draw(rng):
+    op = rng.choice(["norm", "quantize", "dequantize", "linear", "linear"])
+    case = {"op": op, "dtype": rng.choice(["bf16", "bf16", "fp32"])}
+    if op == "linear":
+        case["dtype"] = "bf16"
+        case["d"], case["d_out"] = _width(rng, 64, 28672), _width(rng, 64, 28672)
+        most = 8192 * 8192 * 28672 // (case["d"] * case["d_out"])
+        case["T"] = _log_int(rng, 1, min(8192, most))
+        case["out"] = rng.choice(["mxfp8", "mxfp4"])
+        return case
+    case["d"] = _width(rng, 64, 28672)
+    case["T"] = _log_int(rng, 1, min(28672, 8192 * 8192 // case["d"]))
+    if op == "norm":
+        case["residual"] = rng.random() < 0.7
+        case["out"] = rng.choice(["mxfp8", "mxfp8", "none"])
+    else:
+        case["out"] = rng.choice(["mxfp8", "mxfp4"])
+    return case
+
+
+# ------------------------------------------------- microscaled formats, plain form
+def _padded(cols):
+    return -(-cols // 128) * 128
+
+
+def _quantize(x, fmt):
+    """(values q on the format's grid, scale exponents e): x ~ q * 2^(e - 127), fp32 x."""
+    x = torch.nn.functional.pad(x, (0, _padded(x.shape[1]) - x.shape[1]))
+    b = x.view(x.shape[0], -1, 32)
+    most = b.abs().amax(2)
+    e = ((most.view(torch.int32) >> 23) - (8 if fmt == "mxfp8" else 2)).clamp_(min=0)
+    s = torch.ldexp(b, (127 - e)[:, :, None])   # a power of two: exact
+    if fmt == "mxfp8":
+        s = s.clamp_(-448, 448)
+        _, k = torch.frexp(s)
+        step = torch.ldexp(torch.ones_like(s), (k - 4).clamp_(min=-9))   # 3 mantissa bits, subnormals below 2^-6
+        q = torch.round(s / step) * step
+    else:
+        s = s.clamp_(-6, 6)
+        a = s.abs()
+        step = torch.where(a < 2, 0.5, torch.where(a < 4, 1.0, 2.0))
+        q = torch.round(s / step) * step
+    return q, e
+
+
+def _values(q, e, cols):
+    """q * 2^(e - 127) in fp32, without the padding."""
+    return torch.ldexp(q, (e - 127)[:, :, None]).flatten(1)[:, :cols]
+
+
+def _pack(q, e, fmt):
+    """A quantised matrix in its storage: (bytes, scale bytes)."""
+    rows, kb = e.shape
+    if fmt == "mxfp8":
+        data = q.flatten(1).to(torch.float8_e4m3fn).view(torch.uint8)
+    else:
+        grid = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0], device=q.device)
+        code = torch.bucketize(q.flatten(1).abs(), grid).to(torch.uint8)
+        code |= (torch.signbit(q.flatten(1)).to(torch.uint8) << 3)
+        data = code[:, 0::2] | (code[:, 1::2] << 4)
+    s = torch.zeros(-(-rows // 128) * 128, kb, dtype=torch.uint8, device=q.device)
+    s[:rows] = e.to(torch.uint8)
+    s = s.view(-1, 4, 32, kb // 4, 4).permute(0, 3, 2, 1, 4).contiguous().view(-1)
+    return data.contiguous(), s
+
+
+def _unpack(data, scales, rows, cols, fmt):
+    """The values of a stored matrix, fp32."""
+    kb = _padded(cols) // 32
+    e = scales.view(-1, kb // 4, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(-1, kb)[:rows].to(torch.int32)
+    if fmt == "mxfp8":
+        q = data.view(torch.float8_e4m3fn).to(torch.float32)
+    else:
+        table = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], device=data.device)
+        table = torch.cat([table, -table])
+        q = torch.stack([table[(data & 15).int()], table[(data >> 4).int()]], 2)
+    return _values(q.reshape(rows, kb, 32), e, cols)
+
+
+# ------------------------------------------------------------------------ inputs
+def _activations(T, d, g):
+    """Rows as a transformer has them: unit scale, channels of uneven size."""
+    channel = torch.exp(0.5 * torch.randn(d, generator=g, device="cuda"))
+    return torch.randn(T, d, generator=g, device="cuda") * channel
+
+
+def _stored(rows, cols, fmt, make):
+    """A microscaled matrix as a program holds it, from the rows that make() gives, and the same as the
+    framework's handle where the framework runs."""
+    data, scales = _pack(*_quantize(make(rows, cols), fmt), fmt)
+    s = {"data": data, "scales": scales}
+    if own:
+        import lora_adapter_application_b200 as lora
+        s["mx"] = lora.MxTensor(rows, cols, {"mxfp8": lora.LORA_MXFP8, "mxfp4": lora.LORA_MXFP4}[fmt], q=data,
+                                scales=scales)
+    return s
+
+
+def _empty_mx(rows, cols, fmt):
+    if not own or fmt == "none":
+        return None
+    import lora_adapter_application_b200 as lora
+    return lora.MxTensor(rows, cols, {"mxfp8": lora.LORA_MXFP8, "mxfp4": lora.LORA_MXFP4}[fmt])
+
+
+def prepare(case, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    T, d, dt, op = case["T"], case["d"], DTYPE[case["dtype"]], case["op"]
+    s = {"case": case, "op": op}
+    if op == "norm":
+        s["x"] = _activations(T, d, g).to(dt)
+        s["residual"] = (4 * _activations(T, d, g)).to(dt) if case["residual"] else None
+        s["weight"] = (1 + 0.1 * torch.randn(d, generator=g, device="cuda")).to(dt)
+        s["h"] = torch.empty(T, d, dtype=dt, device="cuda")
+        s["sum"] = torch.empty_like(s["h"]) if case["residual"] else None
+        s["mx"] = _empty_mx(T, d, case["out"])
+        s["values"] = torch.empty(T, d, dtype=torch.bfloat16, device="cuda") if case["out"] != "none" else None
+    elif op == "quantize":
+        s["x"] = _activations(T, d, g).to(dt)
+        s["mx"] = _empty_mx(T, d, case["out"])
+        s["values"] = torch.empty(T, d, dtype=dt, device="cuda")
+    elif op == "dequantize":
+        s["w"] = _stored(T, d, case["out"], lambda n, k: torch.randn(n, k, generator=g, device="cuda") / d ** 0.5)
+        s["values"] = torch.empty(T, d, dtype=dt, device="cuda")
+    else:
+        n = case["d_out"]
+        s["x"] = _stored(T, d, case["out"], lambda m, k: _activations(m, k, g))
+        s["w"] = _stored(n, d, "mxfp4", lambda m, k: torch.randn(m, k, generator=g, device="cuda") / d ** 0.5)
+        s["y"] = torch.empty(T, n, dtype=dt, device="cuda")
+        s["status"] = torch.zeros(1, dtype=torch.int32, device="cuda")
+    return s
+
+
+# ------------------------------------------------------------------------ one pass
+def run(s):
+    return _run_own(s) if own else _run_plain(s)
+
+
+def _run_own(s):
+    import lora_adapter_application_b200 as lora
+    if s["op"] == "norm":
+        lora.lora_rms_norm(s["h"], s["x"], s["weight"], EPS, residual=s["residual"], residual_out=s["sum"], q=s["mx"])
+        out = {"h": s["h"]}
+        if s["sum"] is not None:
+            out["sum"] = s["sum"]
+        if s["mx"] is not None:
+            lora.lora_mx_dequantize(s["values"], s["mx"])
+            out["values"] = s["values"]
+        return out
+    if s["op"] == "quantize":
+        lora.lora_mx_quantize(s["mx"], s["x"])
+        lora.lora_mx_dequantize(s["values"], s["mx"])
+        return {"values": s["values"]}
+    if s["op"] == "dequantize":
+        lora.lora_mx_dequantize(s["values"], s["w"]["mx"])
+        return {"values": s["values"]}
+    lora.lora_mx_linear(s["y"], s["x"]["mx"], s["w"]["mx"], s["status"])
+    return {"y": s["y"]}
+
+
+def _run_plain(s):
+    c = s["case"]
+    T, d, dt, op = c["T"], c["d"], DTYPE[c["dtype"]], c["op"]
+    if op == "norm":
+        r = s["x"].float()
+        out = {}
+        if s["residual"] is not None:
+            out["sum"] = (r + s["residual"].float()).to(dt)
+            r = out["sum"].float()
+        h = r * torch.rsqrt(r.square().mean(1, keepdim=True) + EPS) * s["weight"].float()
+        out["h"] = h.to(dt)
+        if c["out"] != "none":   # of the rounded rows: what the adapters read
+            out["values"] = _values(*_quantize(out["h"].float(), c["out"]), d).to(torch.bfloat16)
+        return out
+    if op == "quantize":
+        return {"values": _values(*_quantize(s["x"].float(), c["out"]), d).to(dt)}
+    if op == "dequantize":
+        return {"values": _unpack(s["w"]["data"], s["w"]["scales"], T, d, c["out"]).to(dt)}
+    x = _unpack(s["x"]["data"], s["x"]["scales"], T, d, c["out"])
+    w = _unpack(s["w"]["data"], s["w"]["scales"], c["d_out"], d, "mxfp4")
+    return {"y": (x @ w.t()).to(dt)}
+
+
+# ------------------------------------------------------------------------ accounting
+def work(case):
+    """Each input read once, each output written once; a multiply and an add count two."""
+    T, d = case["T"], case["d"]
+    es = DTYPE[case["dtype"]].itemsize
+    mx = 0 if case["out"] == "none" else d * BITS[case["out"]] / 8 + -(-d // 32)   # bytes of a microscaled row
+    if case["op"] == "norm":
+        arrays = 4 if case["residual"] else 2
+        values = 2 * d if mx else 0
+        return {"bytes": T * (arrays * d * es + mx + values) + d * es, "flops": 4.0 * T * d}
+    if case["op"] == "quantize":
+        return {"bytes": T * (2 * d * es + mx), "flops": 2.0 * T * d}
+    if case["op"] == "dequantize":
+        return {"bytes": T * (d * es + mx), "flops": 1.0 * T * d}
+    n = case["d_out"]
+    return {"bytes": T * (mx + n * es) + n * (d / 2 + -(-d // 32)), "flops": 2.0 * T * d * n}
+
+
+# ------------------------------------------------------------------- 64-bit values
+def _mx_exact(v, fmt):
+    """The microscaled values of v (fp64 rows) by the formats' definition: nearest element of the table
+    of the format's magnitudes, ties to the even code."""
+    if fmt == "mxfp4":
+        mags, emax = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], 2
+    else:
+        mags = [m / 8 * 2.0 ** -6 for m in range(8)]
+        mags += [(1 + m / 8) * 2.0 ** (k - 7) for k in range(1, 16) for m in range(8)][:-1]
+        emax = 8
+    mags = torch.tensor(mags, dtype=torch.float64, device=v.device)
+    rows, cols = v.shape
+    out = torch.empty_like(v)
+    for lo in range(0, rows, max(1, (1 << 25) // cols)):
+        a = v[lo:lo + max(1, (1 << 25) // cols)]
+        b = torch.cat([a, a.new_zeros(a.shape[0], -cols % 32)], 1).unflatten(1, (-1, 32))
+        top = b.abs().max(2, keepdim=True).values
+        k = torch.floor(torch.log2(top.clamp(min=2.0 ** -140)))
+        k = torch.where(2.0 ** (k + 1) <= top, k + 1, torch.where(2.0 ** k > top, k - 1, k))   # log2 at a border
+        scale = 2.0 ** (k - emax).clamp(min=-127)
+        m = b.abs() / scale
+        hi = torch.searchsorted(mags, m.contiguous()).clamp(max=mags.numel() - 1)
+        lo_i = (hi - 1).clamp(min=0)
+        up, down = mags[hi] - m, m - mags[lo_i]
+        take_hi = (up < down) | ((up == down) & (hi % 2 == 0))
+        q = torch.where(take_hi, mags[hi], mags[lo_i])
+        out[lo:lo + a.shape[0]] = (torch.copysign(q, b) * scale).flatten(1)[:, :cols]
+    return out
+
+
+def _stored_exact(m, rows, cols, fmt):
+    """The fp64 values of a stored matrix, decoded from its bits."""
+    data, pad = m["data"], _padded(cols)
+    if fmt == "mxfp4":
+        code = torch.empty(rows, pad, dtype=torch.uint8, device=data.device)
+        code[:, 0::2], code[:, 1::2] = data % 16, data // 16
+        sign, ex, man, bias, bits = code // 8, code // 2 % 4, code % 2, 1, 1
+    else:
+        sign, ex, man, bias, bits = data // 128, data // 8 % 16, data % 8, 7, 3
+    ex, man = ex.double(), man.double() / 2 ** bits
+    q = torch.where(ex > 0, (1 + man) * 2.0 ** (ex - bias), man * 2.0 ** (1 - bias))
+    q = torch.where(sign > 0, -q, q)
+    r = torch.arange(rows, device=data.device)[:, None]
+    b = torch.arange(pad // 32, device=data.device)[None, :]
+    at = (r // 128 * (pad // 128) + b // 4) * 512 + r % 32 * 16 + r // 32 % 4 * 4 + b % 4
+    e = m["scales"][at].double() - 127
+    return (q.unflatten(1, (-1, 32)) * (2.0 ** e)[:, :, None]).flatten(1)[:, :cols]
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    T, d, dt, op = case["T"], case["d"], DTYPE[case["dtype"]], case["op"]
+    if op == "norm":
+        r = s["x"].double()
+        out = {}
+        if s["residual"] is not None:
+            out["sum"] = r + s["residual"].double()
+            r = out["sum"].to(dt).double()   # the operator norms the sum as it is stored
+        ms = (r * r).sum(1, keepdim=True) / d
+        out["h"] = r / torch.sqrt(ms + EPS) * s["weight"].double()
+        if case["out"] != "none":
+            out["values"] = _mx_exact(out["h"].to(dt).double(), case["out"])
+        return out
+    if op == "quantize":
+        return {"values": _mx_exact(s["x"].double(), case["out"])}
+    if op == "dequantize":
+        return {"values": _stored_exact(s["w"], T, d, case["out"])}
+    x = _stored_exact(s["x"], T, d, case["out"])
+    w = _stored_exact(s["w"], case["d_out"], d, "mxfp4")
+    return {"y": torch.mm(x, w.t())}
