@@ -60,8 +60,8 @@ def listed():
         # a decode batch through gate and up: the weight's bytes
         {"name": "linear 64 x 4096 x 28672", "op": "linear", "T": 64, "d": 4096, "d_out": 28672, "dtype": "bf16",
          "out": "mxfp8"},
-        # a short prompt, an odd number of rows, the down projection's long sums
-        {"name": "linear 257 x 14336 x 4096", "op": "linear", "T": 257, "d": 14336, "d_out": 4096, "dtype": "bf16",
+        # a short prompt, an odd number of rows, the down projection's long sums into fp32 rows
+        {"name": "linear 257 x 14336 x 4096", "op": "linear", "T": 257, "d": 14336, "d_out": 4096, "dtype": "fp32",
          "out": "mxfp8"},
         # the mixed batch's up projection, both operands in 4 bits: the tensor cores' rate
         {"name": "linear 8192 x 8192 x 28672", "op": "linear", "T": 8192, "d": 8192, "d_out": 28672, "dtype": "bf16",
@@ -84,7 +84,6 @@ def draw(rng):
     op = rng.choice(["norm", "quantize", "dequantize", "linear", "linear"])
     case = {"op": op, "dtype": rng.choice(["bf16", "bf16", "fp32"])}
     if op == "linear":
-        case["dtype"] = "bf16"
         case["d"], case["d_out"] = _width(rng, 64, 28672), _width(rng, 64, 28672)
         most = 8192 * 8192 * 28672 // (case["d"] * case["d_out"])
         case["T"] = _log_int(rng, 1, min(8192, most))
