@@ -105,7 +105,7 @@ typedef enum {
     LORA_ERR_DTYPE = -2,      /* unknown element type */
     LORA_ERR_SHAPE = -3,      /* a size or stride is out of range or inconsistent */
     LORA_ERR_RANK = -4,       /* r_max outside [1, LORA_MAX_RANK] */
-    LORA_ERR_ALIGN = -5,      /* reserved: misaligned data takes a slower path instead */
+    LORA_ERR_ALIGN = -5,      /* a microscaled matrix off its alignment (other data takes a slower path) */
     LORA_ERR_WORKSPACE = -6,  /* scratch or workspace smaller than required */
     LORA_ERR_CAPACITY = -7,   /* a tile-list capacity below lora_meta_capacity() */
     LORA_ERR_CUDA = -8        /* a CUDA launch failed (cudaGetLastError) */
@@ -432,6 +432,91 @@ LORA_API int lora_merge_adapter(void *W, int64_t ld_w, int32_t d_out, int32_t d_
                                 const void *B, int32_t N, int32_t r_max, int32_t n,
                                 const int32_t *ranks, const float *alphas, int32_t sign,
                                 lora_dtype dtype, int32_t *status, void *stream);
+
+/*
+ * A microscaled base around the deltas.  Holding the base weights in 4 bits is
+ * what leaves the memory for adapters; the calls below are the base product of
+ * such a server (the W x that lora_add_linear's y arrives with; page
+ * "Multi-LoRA Serving", section 2 flowchart: one shared base product for every
+ * row), the norm that feeds both it and the adapters' shrink, and the conversions.
+ *
+ * Microscaled matrix (OCP Microscaling v1.0): blocks of 32 consecutive elements
+ * of a row share one scale 2^(e-127), held as the byte e (255: NaN).
+ *   LORA_MXFP8   elements e4m3, one byte each
+ *   LORA_MXFP4   elements e2m1, two in a byte, the even column in the low four bits
+ * The struct lives in host memory; q and scales are device memory of the caller.
+ *   q       [rows][lora_mx_row_bytes(format, cols)]: a row is padded with zeros
+ *           to a multiple of 128 columns
+ *   scales  lora_mx_scale_bytes(rows, cols) bytes, in tiles of 128 rows x 4
+ *           blocks = 512 bytes, the tiles of one band of 128 rows one after the other: row r,
+ *           block b is byte ((r / 128) * ceil(cols / 128) + b / 4) * 512 +
+ *           (r % 32) * 16 + (r / 32 % 4) * 4 + b % 4.  Blocks of the padding
+ *           columns have e = 0; bytes of rows past the last one are not used.
+ * Both are aligned to LORA_MX_ALIGN bytes (LORA_ERR_ALIGN otherwise).  Where a call takes a
+ * row count T beside a matrix, it uses its rows 0..T-1 and leaves the others as they were.
+ */
+typedef enum { LORA_MXFP8 = 0, LORA_MXFP4 = 1 } lora_mx_format;
+
+#define LORA_MX_MAX   1048576  /* rows, columns */
+#define LORA_MX_ALIGN     128  /* bytes */
+
+typedef struct {
+    void *q;
+    uint8_t *scales;
+    int32_t rows;
+    int32_t cols;
+    int32_t format;     /* lora_mx_format */
+} lora_mx;
+
+/* Bytes of one row of q; 0 for an unknown format or cols outside [1, LORA_MX_MAX]. */
+LORA_API int64_t lora_mx_row_bytes(int32_t format, int32_t cols);
+
+/* Bytes of scales; 0 for rows outside [0, LORA_MX_MAX] or cols outside [1, LORA_MX_MAX]. */
+LORA_API int64_t lora_mx_scale_bytes(int32_t rows, int32_t cols);
+
+/*
+ * Rows 0..T-1 of x ([T][ld_x], dtype bf16 or fp32, q->cols columns used) to
+ * microscaled form.  Per block: e = max(0, E - emax), E the biased fp32 exponent
+ * of the block's largest magnitude and emax 8 (MXFP8) or 2 (MXFP4); an element
+ * is x * 2^(127-e) rounded to nearest, ties to even, saturating at the format's largest
+ * (448, 6).  A block that holds an infinity or a NaN gets e = 255 and zero
+ * elements: it reads back as NaN as a whole.  A row's last block may be short; its
+ * missing elements count as zeros.
+ */
+LORA_API int lora_mx_quantize(const lora_mx *q, const void *x, int64_t ld_x, int32_t T,
+                              lora_dtype dtype, void *stream);
+
+/* Rows 0..T-1 of q back to values: out[i][j] = element * 2^(e-127), rounded once where
+ * dtype cannot hold it.  out: [T][ld_out], columns 0..q->cols-1 written. */
+LORA_API int lora_mx_dequantize(void *out, int64_t ld_out, const lora_mx *q, int32_t T,
+                                lora_dtype dtype, void *stream);
+
+/*
+ * Root-mean-square norm of T rows of d columns, with the residual's sum before it:
+ *     r = x + residual              rounded to dtype, written to residual_out
+ *     h = r / sqrt(mean_j r_j^2 + eps) * weight        rounded to dtype
+ *     q = lora_mx_quantize(h)
+ * residual and residual_out are both NULL (r = x) or both given, and may be the
+ * same array.  h (the x of lora_add_linear) or q (the x of lora_mx_linear; q->cols = d) may
+ * be NULL, not both; q is what lora_mx_quantize gives for h, whether h is stored or not.
+ * h may be x itself; other outputs overlap nothing.  Sums in fp32.  weight: [d],
+ * eps >= 0.
+ */
+LORA_API int lora_rms_norm(void *h, int64_t ld_h, const void *x, int64_t ld_x,
+                           const void *residual, int64_t ld_r, void *residual_out, int64_t ld_ro,
+                           const void *weight, float eps, int32_t T, int32_t d, const lora_mx *q,
+                           lora_dtype dtype, void *stream);
+
+/*
+ * Base product y = x W^T over T rows: y[i][o] = sum_j x[i][j] w[o][j] for i < T,
+ * o < w->rows, from the stored values of x (LORA_MXFP8 or LORA_MXFP4) and w
+ * (LORA_MXFP4; x->cols = w->cols), fp32 accumulation in a fixed order, one
+ * rounding into y ([T][ld_y], dtype bf16 or fp32).  A NaN block of x or w makes
+ * the elements of y that it enters NaN.  status: device int32, receives LORA_DEV_TIMEOUT if
+ * a bounded wait ran out (the call's results are then unreliable).
+ */
+LORA_API int lora_mx_linear(void *y, int64_t ld_y, const lora_mx *x, const lora_mx *w, int32_t T,
+                            lora_dtype dtype, int32_t *status, void *stream);
 
 #ifdef __cplusplus
 }

@@ -31,12 +31,15 @@ __all__ = [
     "lora_add_linear", "alphas_full", "lora_load_adapter", "SlotCache", "lora_slot_cache_create",
     "lora_slot_cache_destroy", "lora_slot_cache_acquire", "lora_slot_cache_release",
     "lora_slot_cache_key", "lora_slot_cache_evict", "lora_merge_adapter", "lora_segment_plan",
+    "LORA_MXFP8", "LORA_MXFP4", "MxTensor", "lora_mx_row_bytes", "lora_mx_scale_bytes",
+    "lora_mx_quantize", "lora_mx_dequantize", "lora_rms_norm", "lora_mx_linear",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblora_delta.so")
 
 LORA_BF16, LORA_FP32 = 0, 1
+LORA_MXFP8, LORA_MXFP4 = 0, 1
 DEV_BAD_ID, DEV_TILE_OVERFLOW, DEV_BAD_RANK, DEV_TIMEOUT = 1, 2, 4, 8
 ERR_CUDA = -8   # LORA_ERR_CUDA
 MAX_ROWS, MAX_ADAPTERS, MAX_RANK, MAX_SLICES, LONG_TILE = 131072, 4096, 128, 8, 128
@@ -54,6 +57,10 @@ class lora_meta(ctypes.Structure):
 
 class lora_slice(ctypes.Structure):
     _fields_ = [("A", _P), ("B", _P), ("d_out", _I32), ("col_off", _I32)]
+
+
+class lora_mx(ctypes.Structure):
+    _fields_ = [("q", _P), ("scales", _P), ("rows", _I32), ("cols", _I32), ("format", _I32)]
 
 
 class LoraError(RuntimeError):
@@ -91,6 +98,13 @@ _SIGS = {
                                          ctypes.c_float, _P, _P, ctypes.c_int, _P]),
     "lora_merge_adapter": (ctypes.c_int, [_P, _I64, _I32, _I32, _P, _P, _I32, _I32, _I32, _P, _P,
                                           _I32, ctypes.c_int, _P, _P]),
+    "lora_mx_row_bytes": (_I64, [_I32, _I32]),
+    "lora_mx_scale_bytes": (_I64, [_I32, _I32]),
+    "lora_mx_quantize": (ctypes.c_int, [_P, _P, _I64, _I32, ctypes.c_int, _P]),
+    "lora_mx_dequantize": (ctypes.c_int, [_P, _I64, _P, _I32, ctypes.c_int, _P]),
+    "lora_rms_norm": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, ctypes.c_float, _I32,
+                                     _I32, _P, ctypes.c_int, _P]),
+    "lora_mx_linear": (ctypes.c_int, [_P, _I64, _P, _P, _I32, ctypes.c_int, _P, _P]),
     "lora_slot_cache_create": (_P, [_I32]),
     "lora_slot_cache_destroy": (None, [_P]),
     "lora_slot_cache_acquire": (ctypes.c_int, [_P, _I64, ctypes.POINTER(_I32), ctypes.POINTER(_I32)]),
@@ -503,3 +517,154 @@ def lora_merge_adapter(W, A, B, n, ranks, alphas, status, sign=1, stream=None):
                                      _ptr(_dev(ranks, "ranks")), _ptr(_dev(alphas, "alphas")),
                                      int(sign), _dtype_code(W), _ptr(_dev(status, "status")),
                                      _stream(stream)))
+
+
+# ---------------------------------------------------------------- microscaled base
+def lora_mx_row_bytes(fmt, cols):
+    return int(load().lora_mx_row_bytes(fmt, cols))
+
+
+def lora_mx_scale_bytes(rows, cols):
+    return int(load().lora_mx_scale_bytes(rows, cols))
+
+
+class MxTensor:
+    """A microscaled matrix [rows][cols] (lora_mx): ``q`` uint8 [rows, row bytes] and
+    ``scales`` uint8, allocated zero-filled or given by the caller in the layout of
+    include/lora_delta.h.  ``fmt``: LORA_MXFP8 or LORA_MXFP4.  Calls that take fewer
+    rows use the first ones."""
+
+    __slots__ = ("rows", "cols", "fmt", "q", "scales", "device", "c", "ref")
+
+    def __init__(self, rows, cols, fmt, q=None, scales=None, device=None):
+        row_bytes, n_scales = lora_mx_row_bytes(fmt, cols), lora_mx_scale_bytes(rows, cols)
+        if row_bytes == 0 or rows < 0 or (rows > 0 and n_scales == 0):
+            raise LoraError("fmt is LORA_MXFP8 or LORA_MXFP4, rows and cols at most 1048576, cols at least 1")
+        if device is None:
+            device = q.device if q is not None else "cuda"
+        if q is None:
+            q = torch.zeros(rows, row_bytes, dtype=torch.uint8, device=device)
+        if scales is None:
+            scales = torch.zeros(n_scales, dtype=torch.uint8, device=device)
+        for t, what, n in ((q, "q", rows * row_bytes), (scales, "scales", n_scales)):
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or not t.is_contiguous() or t.numel() < n:
+                raise LoraError(f"{what} must be a contiguous uint8 tensor of at least {n} entries")
+        if q.device != scales.device:
+            raise LoraError("q and scales must be on one device")
+        self.rows, self.cols, self.fmt, self.q, self.scales, self.device = rows, cols, fmt, q, scales, q.device
+        self.c = lora_mx(q.data_ptr(), scales.data_ptr(), rows, cols, fmt)
+        self.ref = ctypes.addressof(self.c)
+
+
+def _mx(t, what):
+    if not isinstance(t, MxTensor):
+        raise LoraError(f"{what} must be an MxTensor")
+    if t.device.type != "cuda":
+        raise LoraError(f"{what} must be on a CUDA device")
+    return t
+
+
+def _matrix(t, what, rows=None, cols=None):
+    """(rows, columns, row stride) of a 2-D operand with unit column stride."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise LoraError(f"{what} must be 2-D with unit column stride")
+    n, d = t.shape
+    if (rows is not None and n != rows) or (cols is not None and d != cols):
+        raise LoraError(f"{what} must be [{'rows' if rows is None else rows}, {'columns' if cols is None else cols}]")
+    ld = t.stride(0) if n > 1 else d
+    if ld < d:
+        raise LoraError(f"{what}'s rows overlap")
+    return n, d, ld
+
+
+def _on_one_device(device, stream, *operands):
+    """The device and stream of a call: every operand on `device`, which becomes the
+    current one for the launch; the stream defaults to that device's current one."""
+    for t, what in operands:
+        if t is not None and t.device != device:
+            raise LoraError(f"{what} must be on {device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    return torch.cuda.device(device), _stream(stream)
+
+
+def lora_mx_quantize(q, x, stream=None):
+    """Rows of x (bf16 or fp32, [T <= q.rows, q.cols]) into the first T rows of q."""
+    _mx(q, "q")
+    T, d, ld = _matrix(x, "x", cols=q.cols)
+    _dev(x, "x")
+    if T > q.rows:
+        raise LoraError(f"q holds {q.rows} rows, x has {T}")
+    dev, st = _on_one_device(q.device, stream, (x, "x"))
+    with dev:
+        _check(load().lora_mx_quantize(q.ref, _ptr(x), ld, T, _dtype_code(x), st))
+
+
+def lora_mx_dequantize(out, q, stream=None):
+    """The values of q's first out.shape[0] rows into out (bf16 or fp32, [T <= q.rows, q.cols])."""
+    _mx(q, "q")
+    T, d, ld = _matrix(out, "out", cols=q.cols)
+    _dev(out, "out")
+    if T > q.rows:
+        raise LoraError(f"q holds {q.rows} rows, out has {T}")
+    dev, st = _on_one_device(q.device, stream, (out, "out"))
+    with dev:
+        _check(load().lora_mx_dequantize(_ptr(out), ld, q.ref, T, _dtype_code(out), st))
+
+
+def lora_rms_norm(h, x, weight, eps, residual=None, residual_out=None, q=None, stream=None):
+    """h = r / sqrt(mean(r^2) + eps) * weight per row, r = x + residual (stored to
+    residual_out, by default in place) or x; q (MxTensor, optional): the rows of h
+    microscaled as well.  h may be None when q is given."""
+    T, d, ld_x = _matrix(x, "x")
+    _dev(x, "x")
+    code = _dtype_code(x)
+    if h is None and q is None:
+        raise LoraError("at least one of h and q")
+    if residual is None and residual_out is not None:
+        raise LoraError("residual_out without residual")
+    if residual is not None and residual_out is None:
+        residual_out = residual
+    ld_h = ld_r = ld_ro = 0
+    if h is not None:
+        ld_h = _matrix(h, "h", T, d)[2]
+    if residual is not None:
+        ld_r = _matrix(residual, "residual", T, d)[2]
+        ld_ro = _matrix(residual_out, "residual_out", T, d)[2]
+    if not isinstance(weight, torch.Tensor) or weight.dim() != 1 or weight.numel() != d or \
+            not weight.is_contiguous():
+        raise LoraError("weight must be contiguous [d]")
+    for t in (h, residual, residual_out, weight):
+        if t is not None and t.dtype != x.dtype:
+            raise LoraError("x, h, residual and weight share one dtype")
+    if q is not None:
+        _mx(q, "q")
+        if q.cols != d or q.rows < T:
+            raise LoraError("q must hold at least T rows of d columns")
+    dev, st = _on_one_device(x.device, stream, (h, "h"), (weight, "weight"), (residual, "residual"),
+                             (residual_out, "residual_out"), (q, "q"))
+    with dev:
+        _check(load().lora_rms_norm(_ptr(h), ld_h, _ptr(x), ld_x, _ptr(residual), ld_r, _ptr(residual_out),
+                                    ld_ro, _ptr(weight), float(eps), T, d, None if q is None else q.ref, code,
+                                    st))
+
+
+def lora_mx_linear(y, x, w, status, stream=None):
+    """y[T, w.rows] = x[:T] w^T from microscaled operands (x MXFP8 or MXFP4, w MXFP4);
+    y bf16 or fp32, T = y.shape[0] <= x.rows."""
+    _mx(x, "x")
+    _mx(w, "w")
+    T, n, ld = _matrix(y, "y", cols=w.rows)
+    _dev(y, "y")
+    if x.cols != w.cols:
+        raise LoraError(f"x has {x.cols} columns, w {w.cols}")
+    if T > x.rows:
+        raise LoraError(f"x holds {x.rows} rows, y has {T}")
+    if w.fmt != LORA_MXFP4:
+        raise LoraError("w must be MXFP4")
+    _dev(status, "status")
+    if status.dtype != torch.int32 or status.numel() < 1:
+        raise LoraError("status must be an int32 tensor")
+    dev, st = _on_one_device(x.device, stream, (y, "y"), (w, "w"), (status, "status"))
+    with dev:
+        _check(load().lora_mx_linear(_ptr(y), ld, x.ref, w.ref, T, _dtype_code(y), _ptr(status), st))

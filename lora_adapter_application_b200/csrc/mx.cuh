@@ -1,0 +1,195 @@
+// Microscaled storage (lora_mx): element and scale conversions, scale
+// addressing and the argument checks shared by the kernels that read or write
+// it.  Formats: OCP Microscaling v1.0, MXFP8 (e4m3) and MXFP4 (e2m1), blocks of
+// 32 elements along a row with one e8m0 scale.
+#pragma once
+
+#include "kernels.cuh"
+
+#include <cuda_fp16.h>
+
+namespace lora {
+
+constexpr int MX_BLOCK = 32;         // elements of one scale
+constexpr int MX_TILE_ROWS = 128;    // rows of one scale tile
+constexpr int MX_TILE_COLS = 128;    // columns (4 blocks) of one scale tile
+constexpr int MX_TILE_BYTES = 512;
+
+// columns of a stored row, padding included
+__host__ __device__ constexpr int64_t mx_padded(int64_t cols) {
+    return (cols + MX_TILE_COLS - 1) / MX_TILE_COLS * MX_TILE_COLS;
+}
+__host__ __device__ constexpr int64_t mx_row_bytes(int format, int64_t cols) {
+    return format == LORA_MXFP4 ? mx_padded(cols) / 2 : mx_padded(cols);
+}
+
+// Byte of the first of a row's four scales in tile column kt (the 4 blocks of
+// columns 128 kt .. 128 kt + 127); tiles of one 128-row band run along k.
+__host__ __device__ constexpr int64_t mx_scale_word(int64_t row, int64_t kt, int64_t n_kt) {
+    return ((row / MX_TILE_ROWS) * n_kt + kt) * MX_TILE_BYTES + (row % 32) * 16 + (row / 32 % 4) * 4;
+}
+
+// The scale code of a block from the bits of its largest magnitude: the
+// exponent of that magnitude less the format's own largest exponent, not below
+// 2^-127.  The bit patterns of magnitudes order as the magnitudes do, with infinity and NaN on
+// top: such a block gets the e8m0 NaN (255) and reads back as NaN as a whole.
+template <bool FP4>
+__device__ __forceinline__ uint32_t mx_code(uint32_t amax_bits) {
+    if (amax_bits >= 0x7f800000u) return 255u;
+    const int e = (int)(amax_bits >> 23) - (FP4 ? 2 : 8);
+    return (uint32_t)max(e, 0);
+}
+// 2^(127 - code): the factor that brings a block onto its format's grid.  Codes
+// of finite blocks end at 252, so the factor is a normal number and the product exact.
+// 0 for the NaN code (its elements are stored as zeros).
+__device__ __forceinline__ float mx_inverse(uint32_t code) {
+    return code == 255u ? 0.f : __uint_as_float((254u - code) << 23);
+}
+// 2^(code - 127), NaN for 255
+__device__ __forceinline__ float mx_scale(uint32_t code) {
+    return __uint_as_float(code == 255u ? 0x7fffffffu : code ? code << 23 : 0x00400000u);
+}
+
+// 8 scaled elements to storage, round-to-nearest-even, saturating
+__device__ __forceinline__ uint2 mx_pack_e4m3(const float *v) {
+    uint2 r;
+    asm("{\n\t.reg .b16 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 a, %3, %2;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %5, %4;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 c, %7, %6;\n\tcvt.rn.satfinite.e4m3x2.f32 d, %9, %8;\n\t"
+        "mov.b32 %0, {a, b};\n\tmov.b32 %1, {c, d};\n\t}\n"
+        : "=r"(r.x), "=r"(r.y)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+__device__ __forceinline__ uint32_t mx_pack_e2m1(const float *v) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}\n"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+__device__ __forceinline__ void mx_half2(uint32_t h, float *v) {
+    const __half2 x = *reinterpret_cast<__half2 *>(&h);
+    v[0] = __low2float(x);
+    v[1] = __high2float(x);
+}
+// 8 stored elements to fp32 (exact), without their scale
+__device__ __forceinline__ void mx_unpack_e4m3(uint2 q, float *v) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b16 a, b, c, d;\n\tmov.b32 {a, b}, %4;\n\tmov.b32 {c, d}, %5;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %2, c;\n\tcvt.rn.f16x2.e4m3x2 %3, d;\n\t}\n"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(q.x), "r"(q.y));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx_half2(h[i], v + 2 * i);
+}
+__device__ __forceinline__ void mx_unpack_e2m1(uint32_t q, float *v) {
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}\n"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(q));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx_half2(h[i], v + 2 * i);
+}
+
+// A warp holds 256 consecutive columns of one row, 8 per lane (v: fp32, zeros
+// past the row's end).  Returns the lane's four-block scale word (the same for
+// its 16 lanes) and leaves the elements scaled in v.
+template <bool FP4>
+__device__ __forceinline__ uint32_t mx_scale_warp(float *v) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    m = max(m, __shfl_xor_sync(FULL, m, 1));
+    m = max(m, __shfl_xor_sync(FULL, m, 2));
+    const uint32_t code = mx_code<FP4>(m);
+    const float inv = mx_inverse(code);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = code == 255u ? 0.f : v[i] * inv;
+    uint32_t word = code << (8 * ((threadIdx.x >> 2) & 3));
+    word |= __shfl_xor_sync(FULL, word, 4);
+    word |= __shfl_xor_sync(FULL, word, 8);
+    return word;
+}
+// the lane's 8 scaled elements to column col of a stored row
+template <bool FP4>
+__device__ __forceinline__ void mx_store8(unsigned char *row, int64_t col, const float *v) {
+    if (FP4) *reinterpret_cast<uint32_t *>(row + (col >> 1)) = mx_pack_e2m1(v);
+    else *reinterpret_cast<uint2 *>(row + col) = mx_pack_e4m3(v);
+}
+
+// 8 consecutive elements as fp32; VEC: 16-byte loads (n is then 8 or <= 0)
+template <bool VEC>
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, int64_t n, float *v) {
+    if (VEC) {
+        const uint4 u = n > 0 ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
+        v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
+        v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? load_elem(p + i) : 0.f;
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void load8(const float *p, int64_t n, float *v) {
+    if (VEC) {
+        const float4 z = make_float4(0, 0, 0, 0);
+        const float4 a = n > 0 ? *reinterpret_cast<const float4 *>(p) : z;
+        const float4 b = n > 0 ? *reinterpret_cast<const float4 *>(p + 4) : z;
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? load_elem(p + i) : 0.f;
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, int64_t n, const float *v) {
+    if (VEC) {
+        if (n > 0)
+            *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                       pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) store_elem(p + i, v[i]);
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(float *p, int64_t n, const float *v) {
+    if (VEC) {
+        if (n > 0) {
+            *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) store_elem(p + i, v[i]);
+    }
+}
+// v as the type E holds it
+__device__ __forceinline__ float round_to(const __nv_bfloat16 *, float v) {
+    return __bfloat162float(__float2bfloat16_rn(v));
+}
+__device__ __forceinline__ float round_to(const float *, float v) { return v; }
+
+// tmaps.cu: a map over the bytes of a microscaled matrix's q
+int tensor_map_mx(CUtensorMap *out, const void *base, uint64_t inner, uint64_t rows, uint64_t pitch,
+                  uint32_t box_rows, bool packed4);
+
+// mx_rows.cu: LORA_OK, or what is wrong with a microscaled matrix of at least `rows` rows
+int check_mx(const lora_mx *m, int64_t rows);
+
+inline bool mx_aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+// rows of ld elements of es bytes at p allow 16-byte accesses to 8-column groups of `cols` columns
+inline bool mx_vec(const void *p, int64_t ld, int64_t cols, int es) {
+    return mx_aligned(p, 16) && (cols & 7) == 0 && (ld * es) % 16 == 0;
+}
+
+}  // namespace lora
