@@ -183,7 +183,6 @@ __device__ __forceinline__ float round_to(const float *, float v) { return v; }
 int tensor_map_mx(CUtensorMap *out, const void *base, uint64_t inner, uint64_t rows, uint64_t pitch,
                   uint32_t box_rows, bool packed4);
 
-int tensor_map_mx_scales(CUtensorMap *out, const void *base, uint64_t tiles, uint32_t box_tiles);
 
 // mx_rows.cu: LORA_OK, or what is wrong with a microscaled matrix of at least `rows` rows
 int check_mx(const lora_mx *m, int64_t rows);

@@ -156,19 +156,4 @@ int tensor_map_mx(CUtensorMap *out, const void *base, uint64_t inner, uint64_t r
     return r == CUDA_SUCCESS ? LORA_OK : cuda_fail("cuTensorMapEncodeTiled failed");
 }
 
-// The scales of a microscaled matrix as [tiles][512 bytes]: boxes of box_tiles
-// consecutive tiles, as they lie.
-int tensor_map_mx_scales(CUtensorMap *out, const void *base, uint64_t tiles, uint32_t box_tiles) {
-    auto fn = encoder();
-    if (!fn) return cuda_fail("cuTensorMapEncodeTiled: driver entry point not found");
-    const cuuint64_t dims[2] = {128, tiles};
-    const cuuint64_t strides[1] = {512};
-    const cuuint32_t box[2] = {128, box_tiles};
-    const cuuint32_t estr[2] = {1, 1};
-    const CUresult r = fn(out, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(base), dims, strides, box, estr,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? LORA_OK : cuda_fail("cuTensorMapEncodeTiled failed");
-}
-
 }  // namespace lora

@@ -49,7 +49,8 @@ def _run(T, xm, wm, dtype, ld=None):
 SHAPES = [(1, 1, 1), (1, 32, 128), (1, 128, 128), (16, 256, 128), (17, 384, 100), (3, 1000, 260), (33, 512, 130),
           (64, 2048, 1024), (65, 640, 257), (128, 1003, 300), (129, 4096, 129), (200, 8192, 64), (300, 264, 520),
           (1000, 1152, 1000), (2, 14336, 640), (1, 4096, 4096), (256, 28672, 96), (513, 1, 1), (2049, 128, 33),
-          (700, 640, 257), (1024, 8192, 2304), (5000, 300, 3000), (6000, 1920, 4500)]
+          (257, 1408, 384), (193, 128, 128), (400, 4224, 260), (500, 3000, 700), (16, 16384, 128), (31, 896, 9000),
+          (7, 2176, 20000), (700, 640, 257), (1024, 8192, 2304), (5000, 300, 3000), (6000, 1920, 4500)]
 
 
 @pytest.mark.parametrize("fmt", FMT)
