@@ -67,14 +67,25 @@ __device__ __forceinline__ void mx_mma(uint32_t d, uint64_t a, uint64_t b, uint3
     if (KIND == MX_A4 && PAIR) MX_MMA("2", "mxf4.block_scale.scale_vec::2X");
 }
 #undef MX_MMA
-// One lane of a full warp, the same at every call.  The tensor-core and copy instructions want
-// warp-uniform operands: behind this test the compiler knows that one lane runs and
-// issues them in a few cycles; behind `lane == 0` each takes about 60 (measured: 59 against 38
-// clocks an MMA of N = 16, 49 against 3 a commit).
+// One lane of a full warp, the same at every call.  The tensor-core and copy instructions take
+// their operands from uniform registers.  So the copying and issuing warps run their loops and
+// waits as whole warps, whose counters the compiler then keeps there, and elect a lane around
+// the instructions alone.  Measured: an MMA of N = 16 issued every 59 clocks behind `lane == 0`, every 38 (its
+// own time) behind an election; with the loop inside the elected branch each stage of four still cost
+// about 470 clocks of register moves.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
     return p != 0;
+}
+
+// Bounded wait of a whole warp, uniform for all its lanes.
+__device__ __forceinline__ bool uniform_wait(uint32_t bar, unsigned parity, int32_t *status, bool &failed) {
+    for (unsigned it = 0; it < WAIT_LIMIT; ++it)
+        if (__all_sync(FULL, mbar_try<false>(bar, parity))) return true;
+    if (elect_one()) atomicOr(status, LORA_DEV_TIMEOUT);
+    failed = true;
+    return false;
 }
 
 // 16 bytes to four columns of this thread's tensor-memory lane
@@ -84,35 +95,10 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint4 v) {
                  : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-// 8 bytes into the shared memory of a block of the cluster, counted on its barrier (see st_async_f4)
-__device__ __forceinline__ void st_async_f2(uint32_t addr, float a, float b, uint32_t bar) {
-    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1,%2}, [%3];\n" ::"r"(addr), "f"(a),
-                 "f"(b), "r"(bar)
-                 : "memory");
-}
 // arrival on a barrier of a block of the cluster (address mapped with map_rank); it orders tensor
 // memory only (through the tcgen05 fences), so it needs no release
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
-}
-
-// This thread's 16 columns of its feature f to the blocks that own them (block r: 16 / S columns from
-// r * 16 / S), at [source][feature][column] of their buffer, counted on their barrier.
-__device__ __forceinline__ void send_chunk(const float *d, uint32_t buf, uint32_t bar, int S, int rank, int f) {
-    if (S == 8) {
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            const uint32_t to = map_rank(buf + (uint32_t)((rank * 128 + f) * 8), (uint32_t)r), tb = map_rank(bar, (uint32_t)r);
-            st_async_f2(to, d[2 * r], d[2 * r + 1], tb);
-        }
-    } else {
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {   // four columns at a time: all of one owner
-            const int share = 16 / S, r = 4 * g / share;
-            const uint32_t to = map_rank(buf + (uint32_t)((rank * 128 + f) * share + 4 * g - r * share) * 4u, (uint32_t)r);
-            st_async_f4(to, d[4 * g], d[4 * g + 1], d[4 * g + 2], d[4 * g + 3], map_rank(bar, (uint32_t)r));
-        }
-    }
 }
 
 // The MMAs of one ring stage: n_tiles scale tiles (128 columns of K each) of operands
@@ -140,24 +126,18 @@ __device__ __forceinline__ void y_store(void *y, int64_t at, float v) {
     if (BF16) static_cast<__nv_bfloat16 *>(y)[at] = __float2bfloat16_rn(v);
     else static_cast<float *>(y)[at] = v;
 }
-template <class Args>
-__device__ __forceinline__ void y_store(const Args &a, int64_t row, int64_t col, float v) {
-    if (a.y_bf16) y_store<true>(a.y, row * a.ld_y + col, v);
-    else y_store<false>(a.y, row * a.ld_y + col, v);
-}
 
-// A place in a ring of n slots: the slot and the parity of its current use.  Kept by counting: a
-// single thread's integer division costs as much as the MMAs of a stage.
+// A place in a ring of n slots: the slot and the parity of its current use.  Kept by counting: an
+// integer division costs as much as the MMAs of a stage.
 struct Ring {
-    int slot = 0, n;
+    int slot = 0, n, left;   // left: uses until every slot has been used once
     unsigned parity = 0;
-    int64_t count = 0;   // uses so far
-    __device__ explicit Ring(int n_) : n(n_) {}
+    __device__ explicit Ring(int n_) : n(n_), left(n_) {}
     __device__ void next() {
-        ++count;
+        left = max(left - 1, 0);
         if (++slot == n) slot = 0, parity ^= 1u;
     }
-    __device__ bool reused() const { return count >= n; }
+    __device__ bool reused() const { return left == 0; }
 };
 
 // after a failed wait: the copies that a thread has under way into a ring land before its block goes
@@ -170,20 +150,21 @@ __device__ __forceinline__ void drain_ring(Ring r, uint32_t full) {
 // A cluster takes 128 output features (the MMA's M side: W's rows, which a small
 // batch reads once) x BN rows of x (its N side, any multiple of 16 up to 192), each of its S
 // blocks over 1 / S of k; persistent, cluster c takes tiles c, c + clusters, ....
-// k goes in blocks of 256 columns (two scale tiles).  Roles: one thread copies W into a ring of up to
-// FEW_STAGES slots, one copies x into it and scales into FEW_SF slots, one issues MMAs,
-// four warps move scales from shared to tensor memory, four take the finished
-// accumulator (two of them, so the next tile's products overlap) and add the S
-// partial sums, in block order, through distributed shared memory: 16 columns at a
-// time, block r owning 16 / S of them, sent as st.async counted on the receiver's barrier
-// (four buffers: a block sends chunk i + 1 after reading chunk i - 1, which every block sent
-// after reading chunk i - 3; so a buffer's last chunk has been read everywhere when its next is sent).
+// A ring slot holds KT scale tiles of k (128 columns each): two, or one where wide x tiles would leave too few
+// slots.  Roles: one warp copies W, one x and scales, one issues MMAs, four move scales from
+// shared to tensor memory, four take the finished
+// accumulator (two of them, so the next tile's products overlap).  S > 1 only where every cluster has one tile:
+// its blocks then add their partial sums, in block order, through distributed shared memory: each owns
+// 1 / S of the rows, and gets the others' sums by plain stores between cluster barriers (st.async, which counts every
+// 16 bytes on a barrier, took 1.4 us per 16 rows).  They land behind the ring (few rows) or, once every
+// block's products are done, in it.
 //
-// Bound: W's bytes from HBM (64 rows, 4096 -> 28672: 66 MB), or, per SM, filling shared memory.
-constexpr int FEW_THREADS = 352;      // warp 0 copies W, 1 MMAs, 2-5 scales, 6-9 sums and stores, 10 copies x and scales
+// Bound: W's bytes from HBM (64 rows, 4096 -> 28672: 66 MB), or, per SM, filling shared memory.  What
+// a warp does per slot counts as much: a stage of the MMA warp with a barrier for each 128
+// columns and one for its scales took 1200 clocks per 256 columns, the products 320.
+// warp 0 copies W, 1 MMAs, 2-5 scales, 6-9 and 11-14 sums and stores (every other 16 rows), 10 copies x and scales
+constexpr int FEW_THREADS = 480;
 constexpr int FEW_STAGES = 12;
-constexpr int FEW_SF = 8;
-constexpr int FEW_XCH = 4;            // exchange buffers of 8 KB
 constexpr int FEW_ROWS = 192;         // widest BN
 constexpr size_t MX_MAX_SMEM = 226 * 1024;
 
@@ -192,54 +173,63 @@ struct MxFewArgs {
     const uint8_t *sw, *sx;
     void *y;
     int64_t ld_y;
-    int T, d_out, n_kt, n_kb;   // k in scale tiles (128) and in blocks of two
+    int T, d_out, n_kt, n_ks;   // k in scale tiles and in ring slots
     int bn, nt, tiles;          // rows of a tile, row tiles, all tiles
     int bands, x_bands;         // 128-row bands of x scales one tile may touch; that x has
-    int stages, sf_slots, split;
-    int y_bf16;
+    int stages, split;
+    int own_red;                // the partial sums' place is behind the ring
     int32_t *status;
 };
 
+// A slot: W (16 KB a box: a scale tile of MXFP8's k, two of MXFP4's), x, then the scales of W and of
+// x's bands (KT tiles each)
 template <int KIND>
+__host__ __device__ constexpr int mx_boxes(int kt) { return KIND == MX_A8 ? kt : kt / 2; }
+template <int KIND>
+__host__ __device__ constexpr uint32_t few_x_at(int kt) { return 16384u * mx_boxes<KIND>(kt); }
+template <int KIND>
+__host__ __device__ constexpr uint32_t few_sf_at(int kt, int bn) { return (16384u + 128u * bn) * mx_boxes<KIND>(kt); }
+template <int KIND>
+__host__ __device__ constexpr uint32_t few_slot_bytes(int kt, int bn, int bands) {
+    return (few_sf_at<KIND>(kt, bn) + (1 + bands) * kt * MX_TILE_BYTES + 1023u) & ~1023u;
+}
+__host__ __device__ constexpr uint32_t few_sf_cols(int kt, int bn) { return kt * (bn > 128 ? 12 : 8); }
+
+template <int KIND, int KT, typename Y>
 __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __grid_constant__ MxFewArgs a) {
     extern __shared__ __align__(1024) unsigned char mx_sm[];
     __shared__ uint32_t tmem_sm;
-    __shared__ __align__(8) uint64_t bars[2 * FEW_STAGES + 3 * FEW_SF + 4 + FEW_XCH];
-    constexpr int SUBS = KIND == MX_A8 ? 2 : 1;   // ring stages of a k block
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t slot_bytes = 16384u + (uint32_t)a.bn * 128u, sf_bytes = (uint32_t)(1 + a.bands) * 2 * MX_TILE_BYTES;
-    const uint32_t base = (smem_u32(mx_sm) + 1023u) & ~1023u;
-    const uint32_t sf_base = base + (uint32_t)a.stages * slot_bytes, red = sf_base + (uint32_t)a.sf_slots * sf_bytes;
+    __shared__ __align__(8) uint64_t bars[3 * FEW_STAGES + 4];
+    constexpr int BOXES = mx_boxes<KIND>(KT);
+    const int warp = __shfl_sync(FULL, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t slot_bytes = few_slot_bytes<KIND>(KT, a.bn, a.bands), sf_at = few_sf_at<KIND>(KT, a.bn);
+    const uint32_t base = (smem_u32(mx_sm) + 1023u) & ~1023u, red = base + (a.own_red ? (uint32_t)a.stages * slot_bytes : 0u);
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     auto full = [&](int s) { return bar(s); };
     auto empty = [&](int s) { return bar(FEW_STAGES + s); };
     auto sf_full = [&](int s) { return bar(2 * FEW_STAGES + s); };
-    auto sf_ready = [&](int s) { return bar(2 * FEW_STAGES + FEW_SF + s); };
-    auto sf_empty = [&](int s) { return bar(2 * FEW_STAGES + 2 * FEW_SF + s); };
-    auto acc_full = [&](int b) { return bar(2 * FEW_STAGES + 3 * FEW_SF + b); };
-    auto acc_empty = [&](int b) { return bar(2 * FEW_STAGES + 3 * FEW_SF + 2 + b); };
-    auto xch = [&](int b) { return bar(2 * FEW_STAGES + 3 * FEW_SF + 4 + b); };
+    auto acc_full = [&](int b) { return bar(3 * FEW_STAGES + b); };
+    auto acc_empty = [&](int b) { return bar(3 * FEW_STAGES + 2 + b); };
     const int S = a.split, rank = S > 1 ? (int)cluster_rank() : 0;
     const int c0 = (int)blockIdx.x / S, clusters = (int)gridDim.x / S;
-    const int kb_lo = (int)((int64_t)a.n_kb * rank / S), kb_hi = (int)((int64_t)a.n_kb * (rank + 1) / S);
-    const uint32_t acc_cols = ((uint32_t)a.bn + 31u) & ~31u, xc = a.bn > 128 ? 8u : 4u, sf_cols = 8u + 2u * xc;
-    const uint32_t tmem_cols = pow2_cols(2 * acc_cols + (uint32_t)a.sf_slots * sf_cols);
+    const int k_lo = (int)((int64_t)a.n_ks * rank / S), k_hi = (int)((int64_t)a.n_ks * (rank + 1) / S);
+    const uint32_t acc_cols = ((uint32_t)a.bn + 31u) & ~31u, xc = a.bn > 128 ? 8u : 4u;
+    const uint32_t sf_cols = few_sf_cols(KT, a.bn), tmem_cols = pow2_cols(2 * acc_cols + (uint32_t)a.stages * sf_cols);
     bool failed = false;
 
-    // a warp's place: tile t (m0, n0: its first feature and row), k block kb, stage sub of the block
-    int t = c0, m0 = c0 / a.nt * 128, n0 = c0 % a.nt * a.bn, kb = kb_lo, sub = 0;
-    Ring ring(a.stages), sfr(a.sf_slots);
+    // a warp's place: tile t (m0, n0: its first feature and row)
+    int t = c0, m0 = c0 / a.nt * 128, n0 = c0 % a.nt * a.bn;
+    Ring ring(a.stages);
     auto next_tile = [&]() {
         t += clusters;
         m0 = t / a.nt * 128, n0 = t % a.nt * a.bn;
     };
 
     if (warp == 0) {
-        for (int i = lane; i < 2 * FEW_STAGES + 3 * FEW_SF + 4 + FEW_XCH; i += 32) {
-            const bool two = i < FEW_STAGES;                                                // full: both copying warps
-            const bool four = (i >= 2 * FEW_STAGES + FEW_SF && i < 2 * FEW_STAGES + 2 * FEW_SF) ||      // sf_ready
-                              (i >= 2 * FEW_STAGES + 3 * FEW_SF + 2 && i < 2 * FEW_STAGES + 3 * FEW_SF + 4);   // acc_empty
-            mbar_init(bar(i), two ? 2 : four ? 4 : 1);
+        for (int i = lane; i < 3 * FEW_STAGES + 4; i += 32) {
+            // full: both copying warps and the four scale warps; acc_empty: eight warps
+            const bool six = i < FEW_STAGES, eight = i >= 3 * FEW_STAGES + 2;
+            mbar_init(bar(i), six ? 6 : eight ? 8 : 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         if (lane == 0) prefetch_tmap(&a.tmW);
@@ -255,152 +245,150 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
     __syncthreads();
     tc_fence_after();
     if (S > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");   // this block's barriers are set
-    const uint32_t tmem = tmem_sm, sf = tmem + 2 * acc_cols;
+    const uint32_t tmem = __shfl_sync(FULL, tmem_sm, 0), sf = tmem + 2 * acc_cols;
 
     if (warp == 0) {
-        if (elect_one()) {
-            for (; t < a.tiles && !failed; next_tile())
-                for (kb = kb_lo; kb < kb_hi && !failed; ++kb)
-                    for (sub = 0; sub < min(SUBS, a.n_kt - 2 * kb); ++sub, ring.next()) {
-                        const int s = ring.slot;
-                        if (ring.reused() && !mbar_wait(empty(s), ring.parity ^ 1u, a.status, failed)) break;
-                        mbar_expect_tx(full(s), KIND == MX_A8 ? 8192u : 16384u);   // packed4 boxes count packed bytes
-                        tma_2d(base + (uint32_t)s * slot_bytes, &a.tmW, (SUBS * kb + sub) * 128, m0, full(s));
-                    }
-            if (failed) drain_ring(ring, full(0));
-        }
-        __syncwarp();
+        for (; t < a.tiles && !failed; next_tile())
+            for (int k = k_lo; k < k_hi; ++k, ring.next()) {
+                const uint32_t b = full(ring.slot), slot = base + (uint32_t)ring.slot * slot_bytes;
+                if (ring.reused() && !uniform_wait(empty(ring.slot), ring.parity ^ 1u, a.status, failed)) break;
+                if (elect_one()) {
+                    // packed4 boxes count packed bytes; a box past k's end arrives as zeros that no MMA reads
+                    mbar_expect_tx(b, (KIND == MX_A8 ? 8192u : 16384u) * BOXES);
+#pragma unroll
+                    for (int x = 0; x < BOXES; ++x) tma_2d(slot + 16384u * x, &a.tmW, (BOXES * k + x) * 128, m0, b);
+                }
+            }
+        if (failed) drain_ring(ring, full(0));
     } else if (warp == 10) {
-        if (elect_one()) {
-            for (; t < a.tiles && !failed; next_tile()) {
-                const int xb = n0 / 128, nb = min(a.bands, a.x_bands - xb);
-                for (kb = kb_lo; kb < kb_hi && !failed; ++kb, sfr.next()) {
-                    const int l = sfr.slot, tiles = min(2, a.n_kt - 2 * kb);
-                    if (sfr.reused() && !mbar_wait(sf_empty(l), sfr.parity ^ 1u, a.status, failed)) break;
-                    const uint32_t dst = sf_base + (uint32_t)l * sf_bytes, n = (uint32_t)tiles * MX_TILE_BYTES;
-                    mbar_expect_tx(sf_full(l), (uint32_t)(1 + nb) * n);
-                    bulk_g2s(dst, a.sw + ((int64_t)(m0 / 128) * a.n_kt + 2 * kb) * MX_TILE_BYTES, n, sf_full(l));
-                    for (int b = 0; b < nb; ++b)
-                        bulk_g2s(dst + (uint32_t)(1 + b) * 2 * MX_TILE_BYTES,
-                                 a.sx + ((int64_t)(xb + b) * a.n_kt + 2 * kb) * MX_TILE_BYTES, n, sf_full(l));
-                    for (sub = 0; sub < min(SUBS, tiles); ++sub, ring.next()) {
-                        const int s = ring.slot;
-                        if (ring.reused() && !mbar_wait(empty(s), ring.parity ^ 1u, a.status, failed)) break;
-                        mbar_expect_tx(full(s), (uint32_t)a.bn * 128u);
-                        tma_2d(base + (uint32_t)s * slot_bytes + 16384u, &a.tmX, (SUBS * kb + sub) * 128, n0, full(s));
-                    }
+        const uint32_t x_bytes = (uint32_t)a.bn * 128u;
+        for (; t < a.tiles && !failed; next_tile()) {
+            const int xb = n0 / 128, nb = min(a.bands, a.x_bands - xb);
+            const uint8_t *sw = a.sw + (int64_t)(m0 / 128) * a.n_kt * MX_TILE_BYTES;
+            const uint8_t *sx = a.sx + (int64_t)xb * a.n_kt * MX_TILE_BYTES;
+            for (int k = k_lo; k < k_hi; ++k, ring.next()) {
+                const uint32_t b = full(ring.slot), slot = base + (uint32_t)ring.slot * slot_bytes;
+                if (ring.reused() && !uniform_wait(empty(ring.slot), ring.parity ^ 1u, a.status, failed)) break;
+                if (elect_one()) {
+                    const uint32_t sb = sf_full(ring.slot), n = (uint32_t)min(KT, a.n_kt - KT * k) * MX_TILE_BYTES;
+                    const int64_t off = (int64_t)k * KT * MX_TILE_BYTES;
+                    mbar_expect_tx(sb, (uint32_t)(1 + nb) * n);
+                    bulk_g2s(slot + sf_at, sw + off, n, sb);
+                    for (int i = 0; i < nb; ++i)
+                        bulk_g2s(slot + sf_at + (uint32_t)((1 + i) * KT) * MX_TILE_BYTES,
+                                 sx + off + (int64_t)i * a.n_kt * MX_TILE_BYTES, n, sb);
+                    mbar_expect_tx(b, x_bytes * BOXES);
+#pragma unroll
+                    for (int x = 0; x < BOXES; ++x)
+                        tma_2d(slot + few_x_at<KIND>(KT) + x_bytes * x, &a.tmX, (BOXES * k + x) * 128, n0, b);
                 }
             }
-            if (failed) drain_ring(sfr, sf_full(0)), drain_ring(ring, full(0));
         }
-        __syncwarp();
+        if (failed) drain_ring(ring, sf_full(0)), drain_ring(ring, full(0));
     } else if (warp == 1) {
-        if (elect_one()) {
-            const uint32_t idesc = KIND == MX_A8 ? mx_idesc(5, 0, 128, a.bn) : mx_idesc(1, 1, 128, a.bn);
-            int n = 0;
-            for (; t < a.tiles && !failed; next_tile(), ++n) {
-                const int b = n & 1;
-                if (n >= 2 && !mbar_wait(acc_empty(b), (unsigned)(n / 2 - 1) & 1u, a.status, failed)) break;
-                const uint32_t d = tmem + (uint32_t)b * acc_cols;
-                for (kb = kb_lo; kb < kb_hi && !failed; ++kb, sfr.next()) {
-                    const int l = sfr.slot, tiles = min(2, a.n_kt - 2 * kb);
-                    if (!mbar_wait(sf_ready(l), sfr.parity, a.status, failed)) break;
-                    const uint32_t ta = sf + sf_cols * (uint32_t)l, tb = ta + 8;
-                    for (sub = 0; sub < min(SUBS, tiles); ++sub, ring.next()) {
-                        const int s = ring.slot;
-                        if (!mbar_wait(full(s), ring.parity, a.status, failed)) break;
-                        tc_fence_after();
-                        const uint32_t slot = base + (uint32_t)s * slot_bytes;
-                        mx_stage_mmas<KIND, false>(d, slot, slot + 16384u, ta + 4 * sub, tb + xc * sub, (int)xc, tiles, idesc,
-                                                   kb == kb_lo && sub == 0);
-                        tc_commit(empty(s));
-                    }
-                    tc_commit(sf_empty(l));
+        const uint32_t idesc = KIND == MX_A8 ? mx_idesc(5, 0, 128, a.bn) : mx_idesc(1, 1, 128, a.bn);
+        const uint32_t x_bytes = (uint32_t)a.bn * 128u;
+        int n = 0;
+        for (; t < a.tiles && !failed; next_tile(), ++n) {
+            const int b = n & 1;
+            if (n >= 2 && !uniform_wait(acc_empty(b), (unsigned)(n / 2 - 1) & 1u, a.status, failed)) break;
+            const uint32_t d = tmem + (uint32_t)b * acc_cols;
+            for (int k = k_lo; k < k_hi; ++k, ring.next()) {
+                const uint32_t slot = base + (uint32_t)ring.slot * slot_bytes, ta = sf + sf_cols * (uint32_t)ring.slot;
+                const int tiles = min(KT, a.n_kt - KT * k);
+                if (!uniform_wait(full(ring.slot), ring.parity, a.status, failed)) break;
+                tc_fence_after();
+                if (elect_one()) {
+#pragma unroll
+                    for (int x = 0; x < BOXES; ++x)
+                        if (KIND == MX_A4 || x < tiles)
+                            mx_stage_mmas<KIND, false>(d, slot + 16384u * x, slot + few_x_at<KIND>(KT) + x_bytes * x, ta + 4 * x,
+                                                       ta + 4 * KT + xc * x, (int)xc, tiles, idesc, k == k_lo && x == 0);
+                    tc_commit(empty(ring.slot));
                 }
-                tc_commit(acc_full(b));
             }
+            if (elect_one()) tc_commit(acc_full(b));
         }
-        __syncwarp();
     } else if (warp < 6) {
         const uint32_t dst = sf + ((uint32_t)(32 * (warp & 3)) << 16);
         for (; t < a.tiles && !failed; next_tile()) {
+            // W: lane r gets the 16 bytes of rows r, r + 32, r + 64, r + 96.  x: the tile's rows may start
+            // anywhere in a band; column g, lane r: row n0 + 32 g + r
             const int xb = n0 / 128, last = min(a.bands, a.x_bands - xb) - 1;
-            for (kb = kb_lo; kb < kb_hi; ++kb, sfr.next()) {
-                const int l = sfr.slot;
-                if (!warp_wait(sf_full(l), sfr.parity, a.status, failed)) break;
-                const uint32_t src = sf_base + (uint32_t)l * sf_bytes, to = dst + sf_cols * (uint32_t)l;
+            uint32_t at[8];   // where column g's scales of k tile 0 lie in a slot
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {   // a tile past k's end is old data that no MMA reads
-                    // W: lane r gets the 16 bytes of rows r, r + 32, r + 64, r + 96
-                    tmem_st4(to + 4 * k, lds128(src + k * MX_TILE_BYTES + 16 * lane));
-                    // x: the tile's rows start anywhere in a band; column g, lane r: row n0 + 32 g + r
-                    for (uint32_t g = 0; g < xc; g += 4) {
-                        uint32_t w[4];
+            for (int g = 0; g < 8; ++g) {
+                const int row = n0 + 32 * g + lane, band = min(row / 128 - xb, last);
+                at[g] = sf_at + (uint32_t)((1 + band) * KT) * MX_TILE_BYTES + (uint32_t)(row % 32 * 16 + row / 32 % 4 * 4);
+            }
+            for (int k = k_lo; k < k_hi; ++k, ring.next()) {
+                if (!uniform_wait(sf_full(ring.slot), ring.parity, a.status, failed)) break;
+                const uint32_t slot = base + (uint32_t)ring.slot * slot_bytes, to = dst + sf_cols * (uint32_t)ring.slot;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int row = n0 + 32 * (int)(g + i) + lane, band = min(row / 128 - xb, last);
-                            w[i] = lds32(src + (uint32_t)(1 + band) * 2 * MX_TILE_BYTES + k * MX_TILE_BYTES +
-                                         (uint32_t)(row % 32 * 16 + row / 32 % 4 * 4));
-                        }
-                        tmem_st4(to + 8 + xc * k + g, make_uint4(w[0], w[1], w[2], w[3]));
-                    }
+                for (int i = 0; i < KT; ++i) {   // a tile past k's end is old data that no MMA reads
+                    const uint32_t src = slot + i * MX_TILE_BYTES;
+                    tmem_st4(to + 4 * i, lds128(src + sf_at + 16 * lane));
+                    tmem_st4(to + 4 * KT + xc * i, make_uint4(lds32(src + at[0]), lds32(src + at[1]), lds32(src + at[2]),
+                                                              lds32(src + at[3])));
+                    if (xc == 8)
+                        tmem_st4(to + 4 * KT + xc * i + 4, make_uint4(lds32(src + at[4]), lds32(src + at[5]),
+                                                                      lds32(src + at[6]), lds32(src + at[7])));
                 }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(sf_ready(l));
+                if (elect_one()) mbar_arrive(full(ring.slot));
             }
         }
     } else {
         const int q = warp & 3, f = 32 * q + lane;   // this thread's output feature of the tile
+        const int half = 16 * (warp > 10);           // its first row; then every other 16
         const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
         if (S > 1) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");   // every block's barriers are set
-        const int share = 16 / S;
         int n = 0;
-        uint32_t chunk = 0, sent = 0;
         for (; t < a.tiles && !failed; next_tile(), ++n) {
-            const int b = n & 1;
-            const int64_t m = m0 + f;
-            if (!warp_wait(acc_full(b), (unsigned)(n / 2) & 1u, a.status, failed)) break;
-            tc_fence_after();
-            const int rows = min(a.bn, a.T - n0);
+            const int b = n & 1, rows = min(a.bn, a.T - n0);
             const uint32_t src_acc = acc + (uint32_t)b * acc_cols;
+            const bool there = m0 + f < a.d_out;
+            Y *y = static_cast<Y *>(a.y) + (int64_t)n0 * a.ld_y + m0 + f;
+            if (!warp_wait(acc_full(b), (unsigned)(n / 2) & 1u, a.status, failed) && S == 1) break;
+            tc_fence_after();
             if (S == 1) {
-                for (int c = 0; c < rows; c += 16) {
+                for (int c = half; c < rows; c += 32) {
                     float d[16];
                     tc_ld16(src_acc + c, d);
                     tc_wait_ld();
-                    if (m < a.d_out)
+                    Y *p = y + c * a.ld_y;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (c + j < rows) y_store(a, n0 + c + j, m, d[j]);
+                    for (int j = 0; j < 16; ++j, p += a.ld_y)
+                        if (there && c + j < rows) store_elem(p, d[j]);
                 }
             } else {
-                auto send = [&](int c) {
+                const int own = (rows + S - 1) / S;   // rows of a block
+                if (!a.own_red) cluster_sync_all();   // every block's products are done with its ring
+                const uint32_t mine = red + (uint32_t)(rank * own * 128 + f) * 4u;   // [source][row][feature]
+                for (int c = half; c < rows; c += 32) {
                     float d[16];
                     tc_ld16(src_acc + c, d);
+                    int to = c / own, left = own - (c - to * own);
+                    uint32_t at = map_rank(mine, (uint32_t)to) + (uint32_t)(own - left) * 512u;
                     tc_wait_ld();
-                    const uint32_t p = sent++ & (FEW_XCH - 1);
-                    if (threadIdx.x == 192) mbar_expect_tx(xch((int)p), 8192);
-                    send_chunk(d, red + p * 8192u, xch((int)p), S, rank, f);
-                };
-                send(0);
-                for (int c = 0; c < rows; c += 16) {
-                    if (c + 16 < rows) send(c + 16);
-                    const uint32_t p = chunk & (FEW_XCH - 1), buf = red + p * 8192u;
-                    if (!warp_wait(xch((int)p), chunk / FEW_XCH & 1u, a.status, failed)) break;
-                    ++chunk;
-                    if (m < a.d_out)
-                        for (int j = 0; j < share; ++j) {
-                            const int row = c + rank * share + j;
-                            if (row >= rows) break;
-                            float v = 0.f;
-                            for (int src = 0; src < S; ++src)
-                                v += __uint_as_float(lds32(buf + (uint32_t)(((src * 128 + f) * share + j) * 4)));
-                            y_store(a, n0 + row, m, v);
-                        }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        if (c + j >= rows) break;
+                        asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(at), "f"(d[j]) : "memory");
+                        at += 512;
+                        if (--left == 0) left = own, at = map_rank(mine, (uint32_t)min(++to, S - 1));
+                    }
                 }
-                if (failed) break;
+                cluster_sync_all();
+                Y *p = y + (int64_t)(rank * own + (half >> 4)) * a.ld_y;
+                for (int j = half >> 4; there && j < min(own, rows - rank * own); j += 2, p += 2 * a.ld_y) {
+                    const uint32_t at = red + (uint32_t)(j * 128 + f) * 4u;
+                    float v = 0.f;
+                    for (int src = 0; src < S; ++src) v += __uint_as_float(lds32(at + (uint32_t)(src * own) * 512u));
+                    store_elem(p, v);
+                }
             }
             tc_fence_before();
             __syncwarp();
@@ -408,36 +396,34 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
         }
     }
     // ---------------------------------------------------------------- teardown
-    // A block may go once it has all its chunks: nothing more is sent to it.  After a failed wait that
-    // is not known: the block stays until what is under way has landed and its peers have left or failed too.
     __syncwarp();
-    tc_fence_before();
-    if (__syncthreads_or(failed) && S > 1) {
-        for (int i = 0; i < 100; ++i) __nanosleep(1000);
-        __syncwarp();
-        if (warp < 6 || warp == 10) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    if (S > 1 && (warp < 6 || warp == 10)) {   // the barriers that the other warps wait at
+        asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+        if (!a.own_red) cluster_sync_all();
         cluster_sync_all();
     }
+    tc_fence_before();
+    __syncthreads();
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(tmem_cols) : "memory");
     }
 }
 
-// Blocks along k, clusters of them that fit the device at once, and the time they would take (in k blocks
+// Blocks along k, clusters of them that fit the device at once, and the time they would take (in ring slots
 // a block goes through, a tile's fixed cost counted as TILE_COST of them).
 struct FewPlan {
     int split = 1, clusters = 1;
 };
-template <int KIND>
-int few_plan(int tiles, int n_kb, int dev, FewPlan *out) {
+template <int KIND, int KT, typename Y>
+int few_plan(int tiles, int n_ks, int dev, FewPlan *out) {
     // clusters resident at once: a property of the device and the kernel, asked for once
     static std::mutex mu;
     static int fit[64][4] = {};
     constexpr int TILE_COST = 3;
     std::lock_guard<std::mutex> lock(mu);
     int *f = fit[dev & 63];
-    auto kernel = mx_linear_few_kernel<KIND>;
+    auto kernel = mx_linear_few_kernel<KIND, KT, Y>;
     if (!f[0]) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)MX_MAX_SMEM);
         for (int i = 3; i >= 0 && e == cudaSuccess; --i) {   // f[0] last: it marks the table as filled
@@ -460,14 +446,41 @@ int few_plan(int tiles, int n_kb, int dev, FewPlan *out) {
     int64_t best = -1;
     for (int i = 0; i < 4; ++i) {
         const int s = 1 << i, n = std::min(tiles, f[i]);
-        if (s > n_kb) break;
-        const int64_t cost = (int64_t)((tiles + n - 1) / n) * ((n_kb + s - 1) / s + (i ? TILE_COST : 0));
+        if (s > n_ks || (i && n < tiles)) break;
+        const int64_t cost = (int64_t)((tiles + n - 1) / n) * ((n_ks + s - 1) / s) + (i ? TILE_COST : 0);
         if (best < 0 || cost < best) best = cost, out->split = s, out->clusters = n;
     }
     return LORA_OK;
 }
 
-template <int KIND>
+template <int KIND, int KT, typename Y>
+int launch_few_kt(MxFewArgs &a, int dev, cudaStream_t st) {
+    a.n_ks = (a.n_kt + KT - 1) / KT;
+    FewPlan plan;
+    const int rc = few_plan<KIND, KT, Y>(a.tiles, a.n_ks, dev, &plan);
+    if (rc != LORA_OK) return rc;
+    a.split = plan.split;
+    const int acc_cols = (a.bn + 31) / 32 * 32;
+    a.own_red = a.bn <= 32;
+    const size_t room = MX_MAX_SMEM - 1024 - (plan.split > 1 && a.own_red ? (size_t)(a.bn + 8) * 512 : 0);
+    a.stages = (int)std::min<size_t>(FEW_STAGES, room / few_slot_bytes<KIND>(KT, a.bn, a.bands));
+    a.stages = std::min(a.stages, (512 - 2 * acc_cols) / (int)few_sf_cols(KT, a.bn));
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(plan.split * plan.clusters));
+    cfg.blockDim = dim3(FEW_THREADS);
+    cfg.dynamicSmemBytes = MX_MAX_SMEM;   // one block an SM: two might wait for each other's tensor memory
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)plan.split;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, mx_linear_few_kernel<KIND, KT, Y>, a);
+    return cuda_rc(e != cudaSuccess ? e : cudaGetLastError());
+}
+
+template <int KIND, typename Y>
 int launch_few(const MxLinArgs &l, const lora_mx *x, const lora_mx *w, int dev, cudaStream_t st) {
     MxFewArgs a{};
     const uint64_t xb = (uint64_t)mx_row_bytes(x->format, x->cols), wb = (uint64_t)mx_row_bytes(w->format, w->cols);
@@ -480,32 +493,12 @@ int launch_few(const MxLinArgs &l, const lora_mx *x, const lora_mx *w, int dev, 
     if (rc == LORA_OK) rc = tensor_map_mx(&a.tmX, x->q, xb, (uint64_t)l.T, xb, (uint32_t)a.bn, false);
     if (rc != LORA_OK) return rc;
     a.sw = l.sw, a.sx = l.sx, a.y = l.y, a.ld_y = l.ld_y, a.T = l.T, a.d_out = l.d_out, a.n_kt = l.n_kt;
-    a.n_kb = (l.n_kt + 1) / 2;
     a.x_bands = (l.T + 127) / 128;
     a.bands = std::min(a.x_bands, a.nt == 1 ? (a.bn + 127) / 128 : (a.bn + 126) / 128 + 1);
-    a.y_bf16 = l.y_bf16;
     a.status = l.status;
-    FewPlan plan;
-    rc = few_plan<KIND>(a.tiles, a.n_kb, dev, &plan);
-    if (rc != LORA_OK) return rc;
-    a.split = plan.split;
-    const uint32_t acc_cols = ((uint32_t)a.bn + 31u) & ~31u, sf_cols = a.bn > 128 ? 24u : 16u;
-    a.sf_slots = std::min(FEW_SF, (int)((512 - 2 * acc_cols) / sf_cols));
-    const size_t slot = 16384 + (size_t)a.bn * 128, sf = (size_t)a.sf_slots * (1 + a.bands) * 2 * MX_TILE_BYTES;
-    a.stages = (int)std::min<size_t>(FEW_STAGES, (MX_MAX_SMEM - 1024 - sf - (plan.split > 1 ? FEW_XCH * 8192 : 0)) / slot);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(plan.split * plan.clusters));
-    cfg.blockDim = dim3(FEW_THREADS);
-    cfg.dynamicSmemBytes = MX_MAX_SMEM;   // one block an SM: two might wait for each other's tensor memory
-    cfg.stream = st;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)plan.split;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, mx_linear_few_kernel<KIND>, a);
-    return cuda_rc(e != cudaSuccess ? e : cudaGetLastError());
+    // MXFP8: two scale tiles a slot while four slots fit (up to 64 rows), else one
+    if (KIND == MX_A4 || a.bn <= 64) return launch_few_kt<KIND, 2, Y>(a, dev, st);
+    return launch_few_kt<KIND, KIND == MX_A8 ? 1 : 2, Y>(a, dev, st);
 }
 
 // ---------------------------------------------------------------- many rows
@@ -578,7 +571,7 @@ __global__ void __launch_bounds__(BIG_THREADS, 1) mx_linear_big_kernel(const __g
     constexpr uint32_t SLOT = big_slot_stride<KIND>();
     constexpr uint32_t SF_COLS = 12 * TPS;   // one stage's scales: 4 columns a tile for x, 8 for W
     constexpr uint32_t TX = 2u * (KIND == MX_A8 ? 16384u + 8192u : 32768u);   // packed4 boxes count packed bytes
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(FULL, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t base = (smem_u32(mx_sm) + 1023u) & ~1023u;
     const int rank = (int)cluster_rank();
     const int pair = (int)blockIdx.x >> 1, pairs = (int)gridDim.x >> 1;
@@ -610,27 +603,26 @@ __global__ void __launch_bounds__(BIG_THREADS, 1) mx_linear_big_kernel(const __g
     __syncthreads();
     cluster_sync_all();   // the pair's barriers and tensor memory are ready
     tc_fence_after();
-    const uint32_t tmem = tmem_sm, sf = tmem + 256;
+    const uint32_t tmem = __shfl_sync(FULL, tmem_sm, 0), sf = tmem + 256;
     bool failed = false;
 
     if (warp == 0) {
-        if (elect_one()) {
-            int it = 0;
-            for (int t = pair; t < a.tiles && !failed; t += pairs) {
-                const int m0 = (t % a.mt) * 256 + 128 * rank, nb = t / a.mt * 2;   // nb: first 128-row band of W
-                // bands past the last hold rows that no result uses: any scales will do
-                const uint8_t *sx = a.sx + (int64_t)min(m0 / 128, a.x_bands - 1) * a.n_kt * MX_TILE_BYTES;
-                const uint8_t *sw0 = a.sw + (int64_t)nb * a.n_kt * MX_TILE_BYTES;
-                const uint8_t *sw1 = a.sw + (int64_t)min(nb + 1, a.w_bands - 1) * a.n_kt * MX_TILE_BYTES;
-                for (int i = 0; i < a.n_stage; ++i, ++it) {
-                    const int s = it % BIG_STAGES;
-                    if (it >= BIG_STAGES && !mbar_wait(empty(s), (unsigned)(it / BIG_STAGES - 1) & 1u, a.status, failed))
-                        break;
-                    const uint32_t slot = base + (uint32_t)s * SLOT, bar = map_rank(full(s), 0);
+        Ring ring(BIG_STAGES);
+        for (int t = pair; t < a.tiles && !failed; t += pairs) {
+            const int m0 = (t % a.mt) * 256 + 128 * rank, nb = t / a.mt * 2;   // nb: first 128-row band of W
+            // bands past the last hold rows that no result uses: any scales will do
+            const uint8_t *sx = a.sx + (int64_t)min(m0 / 128, a.x_bands - 1) * a.n_kt * MX_TILE_BYTES;
+            const uint8_t *sw0 = a.sw + (int64_t)nb * a.n_kt * MX_TILE_BYTES;
+            const uint8_t *sw1 = a.sw + (int64_t)min(nb + 1, a.w_bands - 1) * a.n_kt * MX_TILE_BYTES;
+            for (int i = 0; i < a.n_stage; ++i, ring.next()) {
+                const int s = ring.slot;
+                if (ring.reused() && !uniform_wait(empty(s), ring.parity ^ 1u, a.status, failed)) break;
+                const uint32_t slot = base + (uint32_t)s * SLOT, bar = map_rank(full(s), 0);
+                const uint32_t sfs = slot + 32768u, sb = (uint32_t)min(TPS, a.n_kt - i * TPS) * MX_TILE_BYTES;
+                if (elect_one()) {
                     if (rank == 0) mbar_expect_tx(full(s), TX);
                     tma_2d_pair(slot, &a.tmX, i * 128, m0, bar);
                     tma_2d_pair(slot + 16384u, &a.tmW, i * 128, (nb + rank) * 128, bar);
-                    const uint32_t sfs = slot + 32768u, sb = (uint32_t)min(TPS, a.n_kt - i * TPS) * MX_TILE_BYTES;
                     const int64_t off = (int64_t)i * TPS * MX_TILE_BYTES;
                     mbar_expect_tx(sf_full(s), 3 * sb);
                     bulk_g2s(sfs, sx + off, sb, sf_full(s));
@@ -638,37 +630,36 @@ __global__ void __launch_bounds__(BIG_THREADS, 1) mx_linear_big_kernel(const __g
                     bulk_g2s(sfs + 2 * TPS * MX_TILE_BYTES, sw1 + off, sb, sf_full(s));
                 }
             }
-            // after a failed wait: both blocks' copies under way land before the pair goes
-            for (int j = failed ? max(0, it - BIG_STAGES) : it; j < it; ++j) {
-                const unsigned par = (unsigned)(j / BIG_STAGES) & 1u;
-                for (unsigned w = 0; w < 1024 && !mbar_try<false>(sf_full(j % BIG_STAGES), par); ++w) {}
-                for (unsigned w = 0; rank == 0 && w < 1024 && !mbar_try<false>(full(j % BIG_STAGES), par); ++w) {}
-            }
         }
-        __syncwarp();
+        if (failed) {   // both blocks' copies under way land before the pair goes
+            drain_ring(ring, sf_full(0));
+            if (rank == 0) drain_ring(ring, full(0));
+        }
     } else if (warp == 1) {
-        if (rank == 0 && elect_one()) {
+        if (rank == 0) {
             constexpr uint32_t idesc = KIND == MX_A8 ? mx_idesc(0, 5, 256, 256) : mx_idesc(1, 1, 256, 256);
-            int it = 0, n = 0;
+            Ring ring(BIG_STAGES);
+            int n = 0;
             for (int t = pair; t < a.tiles && !failed; t += pairs, ++n) {
-                if (n > 0 && !mbar_wait<true>(acc_empty, (unsigned)(n - 1) & 1u, a.status, failed)) break;
+                if (n > 0 && !uniform_wait(acc_empty, (unsigned)(n - 1) & 1u, a.status, failed)) break;
                 tc_fence_after();
-                for (int i = 0; i < a.n_stage; ++i, ++it) {
-                    const int s = it % BIG_STAGES;
-                    if (!mbar_wait(full(s), (unsigned)(it / BIG_STAGES) & 1u, a.status, failed) ||
-                        !mbar_wait(sf_ready(s), (unsigned)(it / BIG_STAGES) & 1u, a.status, failed))
+                for (int i = 0; i < a.n_stage; ++i, ring.next()) {
+                    const int s = ring.slot;
+                    if (!uniform_wait(sf_ready(s), ring.parity, a.status, failed) ||
+                        !uniform_wait(full(s), ring.parity, a.status, failed))
                         break;
                     tc_fence_after();
                     const uint32_t slot = base + (uint32_t)s * SLOT;
                     const uint32_t ta = sf + SF_COLS * (uint32_t)s, tb = ta + 4 * TPS;
                     const int tiles = min(TPS, a.n_kt - i * TPS);
-                    mx_stage_mmas<KIND, true>(tmem, slot, slot + 16384u, ta, tb, 8, tiles, idesc, i == 0);
-                    tc_commit_pair(empty(s));
+                    if (elect_one()) {
+                        mx_stage_mmas<KIND, true>(tmem, slot, slot + 16384u, ta, tb, 8, tiles, idesc, i == 0);
+                        tc_commit_pair(empty(s));
+                    }
                 }
-                tc_commit_pair(acc_full);
+                if (elect_one()) tc_commit_pair(acc_full);
             }
         }
-        __syncwarp();
     } else if (warp < 6) {
         // The scales of a stage from shared to tensor memory: lane r of each of the four
         // partitions gets the 16 bytes of rows r, r + 32, r + 64, r + 96.  The slot's columns are free
@@ -793,7 +784,7 @@ int launch_big(const MxLinArgs &l, const lora_mx *x, const lora_mx *w, int sms, 
 template <int KIND>
 int launch_linear(const MxLinArgs &a, const lora_mx *x, const lora_mx *w, int dev, int sms, cudaStream_t st) {
     if (a.T > 512) return a.y_bf16 ? launch_big<KIND, true>(a, x, w, sms, st) : launch_big<KIND, false>(a, x, w, sms, st);
-    return launch_few<KIND>(a, x, w, dev, st);
+    return a.y_bf16 ? launch_few<KIND, __nv_bfloat16>(a, x, w, dev, st) : launch_few<KIND, float>(a, x, w, dev, st);
 }
 
 }  // namespace
