@@ -534,7 +534,7 @@ class MxTensor:
     include/lora_delta.h.  ``fmt``: LORA_MXFP8 or LORA_MXFP4.  Calls that take fewer
     rows use the first ones."""
 
-    __slots__ = ("rows", "cols", "fmt", "q", "scales", "device", "c", "ref")
+    __slots__ = ("rows", "cols", "fmt", "q", "scales", "device", "index", "c", "ref")
 
     def __init__(self, rows, cols, fmt, q=None, scales=None, device=None):
         row_bytes, n_scales = lora_mx_row_bytes(fmt, cols), lora_mx_scale_bytes(rows, cols)
@@ -552,64 +552,86 @@ class MxTensor:
         if q.device != scales.device:
             raise LoraError("q and scales must be on one device")
         self.rows, self.cols, self.fmt, self.q, self.scales, self.device = rows, cols, fmt, q, scales, q.device
+        self.index = q.get_device() if q.is_cuda else -1
         self.c = lora_mx(q.data_ptr(), scales.data_ptr(), rows, cols, fmt)
         self.ref = ctypes.addressof(self.c)
 
 
 def _mx(t, what):
-    if not isinstance(t, MxTensor):
+    if type(t) is not MxTensor:
         raise LoraError(f"{what} must be an MxTensor")
-    if t.device.type != "cuda":
+    if t.index < 0:
         raise LoraError(f"{what} must be on a CUDA device")
     return t
 
 
-def _matrix(t, what, rows=None, cols=None):
+def _matrix(t, what, rows=-1, cols=-1):
     """(rows, columns, row stride) of a 2-D operand with unit column stride."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise LoraError(f"{what} must be 2-D with unit column stride")
     n, d = t.shape
-    if (rows is not None and n != rows) or (cols is not None and d != cols):
-        raise LoraError(f"{what} must be [{'rows' if rows is None else rows}, {'columns' if cols is None else cols}]")
-    ld = t.stride(0) if n > 1 else d
-    if ld < d:
+    ld, one = t.stride()
+    if one != 1 and d > 1:
+        raise LoraError(f"{what} must be 2-D with unit column stride")
+    if (rows >= 0 and n != rows) or (cols >= 0 and d != cols):
+        raise LoraError(f"{what} must be [{'rows' if rows < 0 else rows}, {'columns' if cols < 0 else cols}]")
+    if n <= 1:
+        ld = d
+    elif ld < d:
         raise LoraError(f"{what}'s rows overlap")
     return n, d, ld
 
 
-def _on_one_device(device, stream, *operands):
-    """The device and stream of a call: every operand on `device`, which becomes the
-    current one for the launch; the stream defaults to that device's current one."""
-    for t, what in operands:
-        if t is not None and t.device != device:
-            raise LoraError(f"{what} must be on {device}")
+_CODES = {torch.bfloat16: LORA_BF16, torch.float32: LORA_FP32}
+
+
+def _cuda_on(t, what, index):
+    """The address of a tensor that must be on CUDA device `index`."""
+    if not t.is_cuda:
+        raise LoraError(f"{what} must be a CUDA tensor")
+    if t.get_device() != index:
+        raise LoraError(f"{what} must be on cuda:{index}")
+    return t.data_ptr()
+
+
+def _call_on(index, stream, fn, *args):
+    """fn(*args, stream) with device `index` current; the stream defaults to that device's
+    current one."""
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return torch.cuda.device(device), _stream(stream)
+        st = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        st = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, st)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, st)
+    if rc != 0:
+        _check(rc)
+
+
+def _dtype_of(t):
+    code = _CODES.get(t.dtype)
+    return _dtype_code(t) if code is None else code
 
 
 def lora_mx_quantize(q, x, stream=None):
     """Rows of x (bf16 or fp32, [T <= q.rows, q.cols]) into the first T rows of q."""
     _mx(q, "q")
-    T, d, ld = _matrix(x, "x", cols=q.cols)
-    _dev(x, "x")
+    T, d, ld = _matrix(x, "x", -1, q.cols)
     if T > q.rows:
         raise LoraError(f"q holds {q.rows} rows, x has {T}")
-    dev, st = _on_one_device(q.device, stream, (x, "x"))
-    with dev:
-        _check(load().lora_mx_quantize(q.ref, _ptr(x), ld, T, _dtype_code(x), st))
+    _call_on(q.index, stream, (_lib or load()).lora_mx_quantize, q.ref, _cuda_on(x, "x", q.index), ld, T, _dtype_of(x))
 
 
 def lora_mx_dequantize(out, q, stream=None):
     """The values of q's first out.shape[0] rows into out (bf16 or fp32, [T <= q.rows, q.cols])."""
     _mx(q, "q")
-    T, d, ld = _matrix(out, "out", cols=q.cols)
-    _dev(out, "out")
+    T, d, ld = _matrix(out, "out", -1, q.cols)
     if T > q.rows:
         raise LoraError(f"q holds {q.rows} rows, out has {T}")
-    dev, st = _on_one_device(q.device, stream, (out, "out"))
-    with dev:
-        _check(load().lora_mx_dequantize(_ptr(out), ld, q.ref, T, _dtype_code(out), st))
+    _call_on(q.index, stream, (_lib or load()).lora_mx_dequantize, _cuda_on(out, "out", q.index), ld, q.ref, T,
+             _dtype_of(out))
 
 
 def lora_rms_norm(h, x, weight, eps, residual=None, residual_out=None, q=None, stream=None):
@@ -617,36 +639,39 @@ def lora_rms_norm(h, x, weight, eps, residual=None, residual_out=None, q=None, s
     residual_out, by default in place) or x; q (MxTensor, optional): the rows of h
     microscaled as well.  h may be None when q is given."""
     T, d, ld_x = _matrix(x, "x")
-    _dev(x, "x")
-    code = _dtype_code(x)
+    if not x.is_cuda:
+        raise LoraError("x must be a CUDA tensor")
+    index, dtype = x.get_device(), x.dtype
     if h is None and q is None:
         raise LoraError("at least one of h and q")
-    if residual is None and residual_out is not None:
-        raise LoraError("residual_out without residual")
-    if residual is not None and residual_out is None:
-        residual_out = residual
-    ld_h = ld_r = ld_ro = 0
+    ph = pr = po = pq = None
+    ld_h = ld_r = ld_o = 0
     if h is not None:
         ld_h = _matrix(h, "h", T, d)[2]
-    if residual is not None:
-        ld_r = _matrix(residual, "residual", T, d)[2]
-        ld_ro = _matrix(residual_out, "residual_out", T, d)[2]
-    if not isinstance(weight, torch.Tensor) or weight.dim() != 1 or weight.numel() != d or \
-            not weight.is_contiguous():
-        raise LoraError("weight must be contiguous [d]")
-    for t in (h, residual, residual_out, weight):
-        if t is not None and t.dtype != x.dtype:
+        ph = _cuda_on(h, "h", index)
+        if h.dtype != dtype:
             raise LoraError("x, h, residual and weight share one dtype")
+    if residual is not None:
+        if residual_out is None:
+            residual_out = residual
+        ld_r = _matrix(residual, "residual", T, d)[2]
+        ld_o = _matrix(residual_out, "residual_out", T, d)[2]
+        pr, po = _cuda_on(residual, "residual", index), _cuda_on(residual_out, "residual_out", index)
+        if residual.dtype != dtype or residual_out.dtype != dtype:
+            raise LoraError("x, h, residual and weight share one dtype")
+    elif residual_out is not None:
+        raise LoraError("residual_out without residual")
+    if not isinstance(weight, torch.Tensor) or weight.shape != (d,) or not weight.is_contiguous():
+        raise LoraError("weight must be contiguous [d]")
+    if weight.dtype != dtype:
+        raise LoraError("x, h, residual and weight share one dtype")
     if q is not None:
         _mx(q, "q")
-        if q.cols != d or q.rows < T:
-            raise LoraError("q must hold at least T rows of d columns")
-    dev, st = _on_one_device(x.device, stream, (h, "h"), (weight, "weight"), (residual, "residual"),
-                             (residual_out, "residual_out"), (q, "q"))
-    with dev:
-        _check(load().lora_rms_norm(_ptr(h), ld_h, _ptr(x), ld_x, _ptr(residual), ld_r, _ptr(residual_out),
-                                    ld_ro, _ptr(weight), float(eps), T, d, None if q is None else q.ref, code,
-                                    st))
+        if q.cols != d or q.rows < T or q.index != index:
+            raise LoraError("q must hold at least T rows of d columns, on x's device")
+        pq = q.ref
+    _call_on(index, stream, (_lib or load()).lora_rms_norm, ph, ld_h, x.data_ptr(), ld_x, pr, ld_r, po, ld_o,
+             _cuda_on(weight, "weight", index), float(eps), T, d, pq, _dtype_of(x))
 
 
 def lora_mx_linear(y, x, w, status, stream=None):
@@ -654,17 +679,16 @@ def lora_mx_linear(y, x, w, status, stream=None):
     y bf16 or fp32, T = y.shape[0] <= x.rows."""
     _mx(x, "x")
     _mx(w, "w")
-    T, n, ld = _matrix(y, "y", cols=w.rows)
-    _dev(y, "y")
+    T, n, ld = _matrix(y, "y", -1, w.rows)
     if x.cols != w.cols:
         raise LoraError(f"x has {x.cols} columns, w {w.cols}")
     if T > x.rows:
         raise LoraError(f"x holds {x.rows} rows, y has {T}")
     if w.fmt != LORA_MXFP4:
         raise LoraError("w must be MXFP4")
-    _dev(status, "status")
-    if status.dtype != torch.int32 or status.numel() < 1:
+    if w.index != x.index:
+        raise LoraError(f"w must be on cuda:{x.index}")
+    if not isinstance(status, torch.Tensor) or status.dtype != torch.int32 or status.numel() < 1:
         raise LoraError("status must be an int32 tensor")
-    dev, st = _on_one_device(x.device, stream, (y, "y"), (w, "w"), (status, "status"))
-    with dev:
-        _check(load().lora_mx_linear(_ptr(y), ld, x.ref, w.ref, T, _dtype_code(y), _ptr(status), st))
+    _call_on(x.index, stream, (_lib or load()).lora_mx_linear, _cuda_on(y, "y", x.index), ld, x.ref, w.ref, T,
+             _dtype_of(y), _cuda_on(status, "status", x.index))

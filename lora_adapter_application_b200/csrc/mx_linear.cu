@@ -176,7 +176,7 @@ struct MxFewArgs {
     int T, d_out, n_kt, n_ks;   // k in scale tiles and in ring slots
     int bn, nt, tiles;          // rows of a tile, row tiles, all tiles
     int bands, x_bands;         // 128-row bands of x scales one tile may touch; that x has
-    int stages, split;
+    int stages, split_log2;     // ring depth; blocks of a cluster
     int own_red;                // the partial sums' place is behind the ring
     int32_t *status;
 };
@@ -210,20 +210,23 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
     auto sf_full = [&](int s) { return bar(2 * FEW_STAGES + s); };
     auto acc_full = [&](int b) { return bar(3 * FEW_STAGES + b); };
     auto acc_empty = [&](int b) { return bar(3 * FEW_STAGES + 2 + b); };
-    const int S = a.split, rank = S > 1 ? (int)cluster_rank() : 0;
-    const int c0 = (int)blockIdx.x / S, clusters = (int)gridDim.x / S;
-    const int k_lo = (int)((int64_t)a.n_ks * rank / S), k_hi = (int)((int64_t)a.n_ks * (rank + 1) / S);
+    const int S = 1 << a.split_log2, rank = (int)blockIdx.x & (S - 1);   // clusters are S consecutive blocks
+    const int c0 = (int)blockIdx.x >> a.split_log2, clusters = (int)gridDim.x >> a.split_log2;
+    const int k_lo = a.n_ks * rank >> a.split_log2, k_hi = a.n_ks * (rank + 1) >> a.split_log2;
     const uint32_t acc_cols = ((uint32_t)a.bn + 31u) & ~31u, xc = a.bn > 128 ? 8u : 4u;
     const uint32_t sf_cols = few_sf_cols(KT, a.bn), tmem_cols = pow2_cols(2 * acc_cols + (uint32_t)a.stages * sf_cols);
     bool failed = false;
 
     // a warp's place: tile t (m0, n0: its first feature and row)
-    int t = c0, m0 = c0 / a.nt * 128, n0 = c0 % a.nt * a.bn;
-    Ring ring(a.stages);
-    auto next_tile = [&]() {
-        t += clusters;
-        m0 = t / a.nt * 128, n0 = t % a.nt * a.bn;
+    int t, m0, n0;
+    auto place = [&](int tile) {
+        t = tile;
+        const int mi = a.nt == 1 ? t : t / a.nt;
+        m0 = mi * 128, n0 = (t - mi * a.nt) * a.bn;
     };
+    auto next_tile = [&]() { place(t + clusters); };
+    place(c0);
+    Ring ring(a.stages);
 
     if (warp == 0) {
         for (int i = lane; i < 3 * FEW_STAGES + 4; i += 32) {
@@ -233,6 +236,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
         }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         if (lane == 0) prefetch_tmap(&a.tmW);
+        __syncwarp();
+        asm volatile("bar.sync 1, 64;\nbar.arrive 2, %0;\n" ::"n"(FEW_THREADS) : "memory");
     } else if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&tmem_sm)),
                      "r"(tmem_cols)
@@ -240,12 +245,18 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
     } else if (warp == 10) {
         if (lane == 0) prefetch_tmap(&a.tmX);
+        __syncwarp();
+        asm volatile("bar.sync 1, 64;\nbar.arrive 2, %0;\n" ::"n"(FEW_THREADS) : "memory");
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
+    uint32_t tmem = 0;
+    if (warp != 0 && warp != 10) {   // the copying warps go ahead: barriers are enough for them
+        tc_fence_before();
+        asm volatile("bar.sync 2, %0;\n" ::"n"(FEW_THREADS) : "memory");
+        tc_fence_after();
+        tmem = __shfl_sync(FULL, tmem_sm, 0);
+    }
     if (S > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");   // this block's barriers are set
-    const uint32_t tmem = __shfl_sync(FULL, tmem_sm, 0), sf = tmem + 2 * acc_cols;
+    const uint32_t sf = tmem + 2 * acc_cols;
 
     if (warp == 0) {
         for (; t < a.tiles && !failed; next_tile())
@@ -410,17 +421,18 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
     }
 }
 
-// Blocks along k, clusters of them that fit the device at once, and the time they would take (in ring slots
-// a block goes through, a tile's fixed cost counted as TILE_COST of them).
+// Blocks along k and clusters of them, by the time they would take: a scale tile of k costs a block what W's 8 KB of
+// it take from HBM (215 ns a block) or its operands take into shared memory (98 bytes a ns), an
+// exchange of partial sums 1.5 us and 40 ns a row.  Measured: 64 x 4096 x 6144 11.0 us whole, 11.6 in two;
+// 64 x 4096 x 4096 10.6, 11.0 in two, 9.7 in four; 1 x 4096 x 4096 9.6, 7.8, 7.0; 257 x 14336 x 4096 40.9, 30.0.
 struct FewPlan {
-    int split = 1, clusters = 1;
+    int split_log2 = 0, clusters = 1;
 };
 template <int KIND, int KT, typename Y>
-int few_plan(int tiles, int n_ks, int dev, FewPlan *out) {
+int few_plan(const MxFewArgs &a, int dev, FewPlan *out) {
     // clusters resident at once: a property of the device and the kernel, asked for once
     static std::mutex mu;
     static int fit[64][4] = {};
-    constexpr int TILE_COST = 3;
     std::lock_guard<std::mutex> lock(mu);
     int *f = fit[dev & 63];
     auto kernel = mx_linear_few_kernel<KIND, KT, Y>;
@@ -443,12 +455,13 @@ int few_plan(int tiles, int n_ks, int dev, FewPlan *out) {
         }
         if (e != cudaSuccess) return cuda_rc(e);
     }
+    const int64_t kt_ns = std::max(215, KIND == MX_A8 ? 167 + 13 * a.bn / 10 : 83 + 65 * a.bn / 100);
     int64_t best = -1;
     for (int i = 0; i < 4; ++i) {
-        const int s = 1 << i, n = std::min(tiles, f[i]);
-        if (s > n_ks || (i && n < tiles)) break;
-        const int64_t cost = (int64_t)((tiles + n - 1) / n) * ((n_ks + s - 1) / s) + (i ? TILE_COST : 0);
-        if (best < 0 || cost < best) best = cost, out->split = s, out->clusters = n;
+        const int s = 1 << i, n = std::min(a.tiles, f[i]);
+        if (s > a.n_ks || (i && n < a.tiles)) break;
+        const int64_t cost = (int64_t)((a.tiles + n - 1) / n) * ((a.n_ks + s - 1) / s) * KT * kt_ns + (i ? 1500 + 40 * a.bn : 0);
+        if (best < 0 || cost < best) best = cost, out->split_log2 = i, out->clusters = n;
     }
     return LORA_OK;
 }
@@ -457,22 +470,22 @@ template <int KIND, int KT, typename Y>
 int launch_few_kt(MxFewArgs &a, int dev, cudaStream_t st) {
     a.n_ks = (a.n_kt + KT - 1) / KT;
     FewPlan plan;
-    const int rc = few_plan<KIND, KT, Y>(a.tiles, a.n_ks, dev, &plan);
+    const int rc = few_plan<KIND, KT, Y>(a, dev, &plan);
     if (rc != LORA_OK) return rc;
-    a.split = plan.split;
+    a.split_log2 = plan.split_log2;
     const int acc_cols = (a.bn + 31) / 32 * 32;
     a.own_red = a.bn <= 32;
-    const size_t room = MX_MAX_SMEM - 1024 - (plan.split > 1 && a.own_red ? (size_t)(a.bn + 8) * 512 : 0);
+    const size_t room = MX_MAX_SMEM - 1024 - (plan.split_log2 && a.own_red ? (size_t)(a.bn + 8) * 512 : 0);
     a.stages = (int)std::min<size_t>(FEW_STAGES, room / few_slot_bytes<KIND>(KT, a.bn, a.bands));
     a.stages = std::min(a.stages, (512 - 2 * acc_cols) / (int)few_sf_cols(KT, a.bn));
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(plan.split * plan.clusters));
+    cfg.gridDim = dim3((unsigned)(plan.clusters << plan.split_log2));
     cfg.blockDim = dim3(FEW_THREADS);
     cfg.dynamicSmemBytes = MX_MAX_SMEM;   // one block an SM: two might wait for each other's tensor memory
     cfg.stream = st;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)plan.split;
+    attr.val.clusterDim.x = 1u << plan.split_log2;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
