@@ -18,6 +18,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 namespace lora {
 
@@ -32,7 +33,6 @@ struct MxLinArgs {   // a call, as the launchers take it
     int T, d_out;
     int n_kt;      // scale tiles along k: padded columns / 128
     int n_stage;   // ring stages of k
-    int y_bf16;
     int32_t *status;
 };
 
@@ -427,6 +427,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
 // 64 x 4096 x 4096 10.6, 11.0 in two, 9.7 in four; 1 x 4096 x 4096 9.6, 7.8, 7.0; 257 x 14336 x 4096 40.9, 30.0.
 struct FewPlan {
     int split_log2 = 0, clusters = 1;
+    int64_t ns = 0;
 };
 template <int KIND, int KT, typename Y>
 int few_plan(const MxFewArgs &a, int dev, FewPlan *out) {
@@ -463,15 +464,18 @@ int few_plan(const MxFewArgs &a, int dev, FewPlan *out) {
         const int64_t cost = (int64_t)((a.tiles + n - 1) / n) * ((a.n_ks + s - 1) / s) * KT * kt_ns + (i ? 1500 + 40 * a.bn : 0);
         if (best < 0 || cost < best) best = cost, out->split_log2 = i, out->clusters = n;
     }
+    out->ns = best + 4500;
     return LORA_OK;
 }
 
+// The call on this kernel unless it would take longer than limit_ns (*took = 0 then).
 template <int KIND, int KT, typename Y>
-int launch_few_kt(MxFewArgs &a, int dev, cudaStream_t st) {
+int launch_few_kt(MxFewArgs &a, int dev, int64_t limit_ns, int *took, cudaStream_t st) {
     a.n_ks = (a.n_kt + KT - 1) / KT;
     FewPlan plan;
     const int rc = few_plan<KIND, KT, Y>(a, dev, &plan);
-    if (rc != LORA_OK) return rc;
+    *took = rc == LORA_OK && plan.ns <= limit_ns;
+    if (!*took) return rc;
     a.split_log2 = plan.split_log2;
     const int acc_cols = (a.bn + 31) / 32 * 32;
     a.own_red = a.bn <= 32;
@@ -494,14 +498,13 @@ int launch_few_kt(MxFewArgs &a, int dev, cudaStream_t st) {
 }
 
 template <int KIND, typename Y>
-int launch_few(const MxLinArgs &l, const lora_mx *x, const lora_mx *w, int dev, cudaStream_t st) {
+int launch_few(const MxLinArgs &l, const lora_mx *x, const lora_mx *w, int dev, int64_t limit_ns, int *took, cudaStream_t st) {
     MxFewArgs a{};
     const uint64_t xb = (uint64_t)mx_row_bytes(x->format, x->cols), wb = (uint64_t)mx_row_bytes(w->format, w->cols);
     a.nt = (l.T + FEW_ROWS - 1) / FEW_ROWS;
     a.bn = ((l.T + a.nt - 1) / a.nt + 15) / 16 * 16;
     a.nt = (l.T + a.bn - 1) / a.bn;
-    const int mt = (l.d_out + 127) / 128;
-    a.tiles = mt * a.nt;
+    a.tiles = (l.d_out + 127) / 128 * a.nt;
     int rc = tensor_map_mx(&a.tmW, w->q, wb, (uint64_t)l.d_out, wb, 128, KIND == MX_A8);
     if (rc == LORA_OK) rc = tensor_map_mx(&a.tmX, x->q, xb, (uint64_t)l.T, xb, (uint32_t)a.bn, false);
     if (rc != LORA_OK) return rc;
@@ -510,8 +513,8 @@ int launch_few(const MxLinArgs &l, const lora_mx *x, const lora_mx *w, int dev, 
     a.bands = std::min(a.x_bands, a.nt == 1 ? (a.bn + 127) / 128 : (a.bn + 126) / 128 + 1);
     a.status = l.status;
     // MXFP8: two scale tiles a slot while four slots fit (up to 64 rows), else one
-    if (KIND == MX_A4 || a.bn <= 64) return launch_few_kt<KIND, 2, Y>(a, dev, st);
-    return launch_few_kt<KIND, KIND == MX_A8 ? 1 : 2, Y>(a, dev, st);
+    if (KIND == MX_A4 || a.bn <= 64) return launch_few_kt<KIND, 2, Y>(a, dev, limit_ns, took, st);
+    return launch_few_kt<KIND, KIND == MX_A8 ? 1 : 2, Y>(a, dev, limit_ns, took, st);
 }
 
 // ---------------------------------------------------------------- many rows
@@ -794,10 +797,18 @@ int launch_big(const MxLinArgs &l, const lora_mx *x, const lora_mx *w, int sms, 
     return cuda_rc(e != cudaSuccess ? e : cudaGetLastError());
 }
 
-template <int KIND>
+// Few rows or many, by the time each would take.  The pair kernel: 5.5 us, and per round of its 256 x 256 tiles 3.5 us
+// and 360 (MXFP8) or 180 ns a scale tile of k.  Measured, 4096 -> 28672 and 14336 -> 4096 with x in MXFP8, us few / many:
+// 128 rows 25.9 / 35.6, -; 256 rows 45.9 / 36.9, 27.0 / 45.4; 512 rows 61.7 / 61.8, 42.2 / 45.3; in MXFP4: 128 rows
+// 19.0 / 25.1, -; 256 rows 28.3 / 26.0, 19.9 / 25.0; 512 rows 41.4 / 40.3, 28.3 / 25.6.
+template <int KIND, typename Y>
 int launch_linear(const MxLinArgs &a, const lora_mx *x, const lora_mx *w, int dev, int sms, cudaStream_t st) {
-    if (a.T > 512) return a.y_bf16 ? launch_big<KIND, true>(a, x, w, sms, st) : launch_big<KIND, false>(a, x, w, sms, st);
-    return a.y_bf16 ? launch_few<KIND, __nv_bfloat16>(a, x, w, dev, st) : launch_few<KIND, float>(a, x, w, dev, st);
+    const int64_t tiles = (int64_t)((a.T + 255) / 256) * ((a.d_out + 255) / 256), pairs = std::max(1, sms / 2);
+    const int64_t many_ns = 5500 + (tiles + pairs - 1) / pairs * (3500 + (int64_t)a.n_kt * (KIND == MX_A8 ? 360 : 180));
+    int took = 0;
+    const int rc = launch_few<KIND, Y>(a, x, w, dev, many_ns, &took, st);
+    if (rc != LORA_OK || took) return rc;
+    return launch_big<KIND, std::is_same<Y, __nv_bfloat16>::value>(a, x, w, sms, st);
 }
 
 }  // namespace
@@ -822,19 +833,18 @@ int lora_mx_linear(void *y, int64_t ld_y, const lora_mx *x, const lora_mx *w, in
     MxLinArgs a{};
     a.sw = w->scales, a.sx = x->scales, a.y = y, a.ld_y = ld_y, a.T = T, a.d_out = w->rows;
     a.n_kt = (int)(mx_padded(x->cols) / MX_TILE_COLS);
-    a.y_bf16 = dtype == LORA_BF16;
     a.status = status;
     int dev = 0, sms = 148;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return cuda_rc(e);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (x->format == LORA_MXFP8) {
-        a.n_stage = a.n_kt;
-        return launch_linear<MX_A8>(a, x, w, dev, sms, st);
-    }
-    a.n_stage = (a.n_kt + 1) / 2;
-    return launch_linear<MX_A4>(a, x, w, dev, sms, st);
+    const bool a8 = x->format == LORA_MXFP8;
+    a.n_stage = a8 ? a.n_kt : (a.n_kt + 1) / 2;
+    if (dtype == LORA_BF16)
+        return a8 ? launch_linear<MX_A8, __nv_bfloat16>(a, x, w, dev, sms, st)
+                  : launch_linear<MX_A4, __nv_bfloat16>(a, x, w, dev, sms, st);
+    return a8 ? launch_linear<MX_A8, float>(a, x, w, dev, sms, st) : launch_linear<MX_A4, float>(a, x, w, dev, sms, st);
 }
 
 }  // extern "C"
