@@ -98,86 +98,155 @@ __device__ __forceinline__ void mx_unpack_e2m1(uint32_t q, float *v) {
     for (int i = 0; i < 4; ++i) mx_half2(h[i], v + 2 * i);
 }
 
-// A warp holds 256 consecutive columns of one row, 8 per lane (v: fp32, zeros
-// past the row's end).  Returns the lane's four-block scale word (the same for
-// its 16 lanes) and leaves the elements scaled in v.
-template <bool FP4>
-__device__ __forceinline__ uint32_t mx_scale_warp(float *v) {
-    uint32_t m = 0;
+// Largest magnitude of 8 elements as fp32 bits, from their raw form (bf16: two to a
+// word, compared as 16-bit integers).
+__device__ __forceinline__ uint32_t mx_top(const uint4 &u) {
+    const uint32_t m = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+    return max(m << 16, m & 0xffff0000u);
+}
+struct Raw32 {   // 8 fp32 elements
+    uint4 a, b;
+};
+__device__ __forceinline__ uint32_t mx_top(const Raw32 &u) {
+    const uint32_t k = 0x7fffffffu;
+    const uint32_t m = max(max(u.a.x & k, u.a.y & k), max(u.a.z & k, u.a.w & k));
+    return max(m, max(max(u.b.x & k, u.b.y & k), max(u.b.z & k, u.b.w & k)));
+}
+__device__ __forceinline__ void raw_values(const uint4 &u, float *v) {
+    v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
+    v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
+}
+__device__ __forceinline__ void raw_values(const Raw32 &u, float *v) {
+    v[0] = __uint_as_float(u.a.x), v[1] = __uint_as_float(u.a.y), v[2] = __uint_as_float(u.a.z), v[3] = __uint_as_float(u.a.w);
+    v[4] = __uint_as_float(u.b.x), v[5] = __uint_as_float(u.b.y), v[6] = __uint_as_float(u.b.z), v[7] = __uint_as_float(u.b.w);
+}
+// fp32 values rounded to the raw form
+__device__ __forceinline__ void raw_round(const float *v, uint4 &u) {
+    u = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+__device__ __forceinline__ void raw_round(const float *v, Raw32 &u) {
+    u.a = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    u.b = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+}
+template <typename E>
+struct RawOf {
+    using type = uint4;
+};
+template <>
+struct RawOf<float> {
+    using type = Raw32;
+};
+
+// A warp works on 256 consecutive columns of a row from c0 (a multiple of 256), 8 per lane.
+//   VEC   lane l holds columns c0 + 8 l ..: 16-byte accesses, a scale's block is 4 lanes
+//   else  lane l holds columns c0 + 32 i + l: rows that 16-byte accesses do not suit (8 neighbours a lane, one
+//         by one, took twice as long in the norm)
+template <bool VEC>
+__device__ __forceinline__ void load8(const __nv_bfloat16 *row, int c0, int cols, int lane, uint4 &u) {
+    if (VEC) {
+        u = c0 + 8 * lane < cols ? *reinterpret_cast<const uint4 *>(row + c0 + 8 * lane) : make_uint4(0, 0, 0, 0);
+    } else {
+        uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+        for (int i = 0; i < 8; ++i)
+            w[i] = c0 + 32 * i + lane < cols ? __bfloat16_as_ushort(row[c0 + 32 * i + lane]) : 0u;
+        u = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void load8(const float *row, int c0, int cols, int lane, Raw32 &u) {
+    if (VEC) {
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        const bool there = c0 + 8 * lane < cols;
+        const uint4 *p = reinterpret_cast<const uint4 *>(row + c0 + 8 * lane);
+        u.a = there ? p[0] : z;
+        u.b = there ? p[1] : z;
+    } else {
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c0 + 32 * i + lane < cols ? row[c0 + 32 * i + lane] : 0.f;
+        raw_round(v, u);
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(__nv_bfloat16 *row, int c0, int cols, int lane, const uint4 &u) {
+    if (VEC) {
+        if (c0 + 8 * lane < cols) *reinterpret_cast<uint4 *>(row + c0 + 8 * lane) = u;
+    } else {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c0 + 32 * i + lane < cols)
+                row[c0 + 32 * i + lane] = __ushort_as_bfloat16((unsigned short)(w[i >> 1] >> (16 * (i & 1))));
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void store8(float *row, int c0, int cols, int lane, const Raw32 &u) {
+    if (VEC) {
+        if (c0 + 8 * lane < cols) {
+            uint4 *p = reinterpret_cast<uint4 *>(row + c0 + 8 * lane);
+            p[0] = u.a;
+            p[1] = u.b;
+        }
+    } else {
+        float v[8];
+        raw_values(u, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c0 + 32 * i + lane < cols) row[c0 + 32 * i + lane] = v[i];
+    }
+}
+
+// Elements c0 + 32 i + lane of the warp's lanes to c0 + 8 lane + i and back, through
+// 256 floats of shared memory of its own.
+__device__ __forceinline__ void lanes_to_rows(float *v, float *sm, int lane) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sm[32 * i + lane] = v[i];
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4 *>(v + i) = *reinterpret_cast<const float4 *>(sm + 8 * lane + i);
+}
+__device__ __forceinline__ void rows_to_lanes(float *v, float *sm, int lane) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) *reinterpret_cast<float4 *>(sm + 8 * lane + i) = *reinterpret_cast<const float4 *>(v + i);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = sm[32 * i + lane];
+}
+
+// The warp's 256 columns, microscaled, to a stored row q and the scales of its row r; a lane holds
+// columns c0 + 8 lane .. (v, fp32, and their largest magnitude's bits m).
+// pad: the stored columns; there: the row exists (whole warps take part either way).
+template <bool FP4>
+__device__ __forceinline__ void mx_emit(unsigned char *q, uint8_t *scales, int64_t r, int c0, int pad, int lane, bool there,
+                                        float *v, uint32_t m) {
     m = max(m, __shfl_xor_sync(FULL, m, 1));
     m = max(m, __shfl_xor_sync(FULL, m, 2));
     const uint32_t code = mx_code<FP4>(m);
     const float inv = mx_inverse(code);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = code == 255u ? 0.f : v[i] * inv;
-    uint32_t word = code << (8 * ((threadIdx.x >> 2) & 3));
+    for (int i = 0; i < 8; ++i) v[i] *= inv;
+    if (__any_sync(FULL, code == 255u) && code == 255u)   // elements of a NaN block: zeros
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    uint32_t word = code << (8 * ((lane >> 2) & 3));
     word |= __shfl_xor_sync(FULL, word, 4);
     word |= __shfl_xor_sync(FULL, word, 8);
-    return word;
-}
-// the lane's 8 scaled elements to column col of a stored row
-template <bool FP4>
-__device__ __forceinline__ void mx_store8(unsigned char *row, int64_t col, const float *v) {
-    if (FP4) *reinterpret_cast<uint32_t *>(row + (col >> 1)) = mx_pack_e2m1(v);
-    else *reinterpret_cast<uint2 *>(row + col) = mx_pack_e4m3(v);
-}
-
-// 8 consecutive elements as fp32; VEC: 16-byte loads (n is then 8 or <= 0)
-template <bool VEC>
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, int64_t n, float *v) {
-    if (VEC) {
-        const uint4 u = n > 0 ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
-        v[0] = bf16_lo(u.x), v[1] = bf16_hi(u.x), v[2] = bf16_lo(u.y), v[3] = bf16_hi(u.y);
-        v[4] = bf16_lo(u.z), v[5] = bf16_hi(u.z), v[6] = bf16_lo(u.w), v[7] = bf16_hi(u.w);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? load_elem(p + i) : 0.f;
+    const int col = c0 + 8 * lane;
+    if (there && col < pad) {
+        if (FP4) *reinterpret_cast<uint32_t *>(q + (col >> 1)) = mx_pack_e2m1(v);
+        else *reinterpret_cast<uint2 *>(q + col) = mx_pack_e4m3(v);
+        if ((lane & 15) == 0) *reinterpret_cast<uint32_t *>(scales + mx_scale_word(r, col >> 7, pad / MX_TILE_COLS)) = word;
     }
 }
-template <bool VEC>
-__device__ __forceinline__ void load8(const float *p, int64_t n, float *v) {
-    if (VEC) {
-        const float4 z = make_float4(0, 0, 0, 0);
-        const float4 a = n > 0 ? *reinterpret_cast<const float4 *>(p) : z;
-        const float4 b = n > 0 ? *reinterpret_cast<const float4 *>(p + 4) : z;
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    } else {
+__device__ __forceinline__ uint32_t mx_top(const float *v) {
+    uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? load_elem(p + i) : 0.f;
-    }
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    return m;
 }
-template <bool VEC>
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, int64_t n, const float *v) {
-    if (VEC) {
-        if (n > 0)
-            *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                       pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) store_elem(p + i, v[i]);
-    }
-}
-template <bool VEC>
-__device__ __forceinline__ void store8(float *p, int64_t n, const float *v) {
-    if (VEC) {
-        if (n > 0) {
-            *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n) store_elem(p + i, v[i]);
-    }
-}
-// v as the type E holds it
-__device__ __forceinline__ float round_to(const __nv_bfloat16 *, float v) {
-    return __bfloat162float(__float2bfloat16_rn(v));
-}
-__device__ __forceinline__ float round_to(const float *, float v) { return v; }
 
 // tmaps.cu: a map over the bytes of a microscaled matrix's q
 int tensor_map_mx(CUtensorMap *out, const void *base, uint64_t inner, uint64_t rows, uint64_t pitch,

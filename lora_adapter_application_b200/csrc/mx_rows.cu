@@ -16,91 +16,85 @@ namespace {
 
 constexpr int ROWS_THREADS = 256;
 
-// The rows a warp takes at once: r, r + 32, r + 64, r + 96 of a 128-row band,
-// whose scale words are neighbours (16 bytes of a tile).  Small matrices have
-// fewer of them; row R of a band of height h is there if R < h.
+// The rows a warp takes at once: r, r + 32, r + 64, r + 96 of a 128-row band (J = 4), whose
+// scale words are neighbours (16 bytes of a tile), or one row (J = 1: small matrices, more warps).
+// Grid: groups of 256 columns (a warp each), rows within 32 (or 128), bands.
 struct RowItem {
-    int64_t band;   // first row of the 128-row band
-    int r;          // row within 32
-    int64_t group;  // 256-column group
+    int64_t row;   // the first row
+    int c0;        // the first column
 };
-__device__ __forceinline__ RowItem row_item(int64_t item, int r_count, int64_t groups) {
-    RowItem it;
-    it.group = item % groups;
-    const int64_t rest = item / groups;
-    it.r = (int)(rest % r_count);
-    it.band = rest / r_count * MX_TILE_ROWS;
-    return it;
+__device__ __forceinline__ RowItem row_item() {
+    return RowItem{(int64_t)blockIdx.z * MX_TILE_ROWS + blockIdx.y,
+                   (int)(blockIdx.x * (ROWS_THREADS / 32) + (threadIdx.x >> 5)) * 256};
 }
 
-template <typename E, bool FP4, bool VEC>
+template <typename E, bool FP4, bool VEC, int J>
 __global__ void __launch_bounds__(ROWS_THREADS)
-    mx_quantize_kernel(unsigned char *q, uint8_t *scales, const E *x, int64_t ld_x, int T, int cols, int r_count,
-                       int64_t items) {
-    const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * (ROWS_THREADS / 32) + (threadIdx.x >> 5);
-    if (item >= items) return;
-    const int64_t pad = mx_padded(cols), groups = (pad + 255) / 256, n_kt = pad / MX_TILE_COLS;
+    mx_quantize_kernel(unsigned char *q, uint8_t *scales, const E *x, int64_t ld_x, int T, int cols) {
+    using Raw = typename RawOf<E>::type;
+    const int lane = threadIdx.x & 31, pad = (int)mx_padded(cols);
     const int64_t row_bytes = FP4 ? pad / 2 : pad;
-    const RowItem it = row_item(item, r_count, groups);
-    const int64_t col = it.group * 256 + lane * 8;
-    float v[4][8];
+    const RowItem it = row_item();
+    if (it.c0 >= pad) return;
+    Raw u[J];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t row = it.band + it.r + 32 * j;
-        load8<VEC>(x + (row < T ? row : 0) * ld_x + col, row < T ? cols - col : 0, v[j]);
-    }
-    uint32_t word[4];
+    for (int j = 0; j < J; ++j) {
+        const int64_t row = it.row + 32 * j;
+        const E *p = x + (row < T ? row : 0) * ld_x;
+        const int n = row < T ? cols : 0;
+        if (VEC) {
+            load8<true>(p, it.c0, n, lane, u[j]);
+        } else {   // 8 neighbours one by one: the lines they share come from L1
+            float v[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) word[j] = mx_scale_warp<FP4>(v[j]);
-    if (col >= pad) return;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t row = it.band + it.r + 32 * j;
-        if (row < T) {
-            mx_store8<FP4>(q + row * row_bytes, col, v[j]);
-            if ((lane & 15) == 0)
-                *reinterpret_cast<uint32_t *>(scales + mx_scale_word(row, col >> 7, n_kt)) = word[j];
+            for (int i = 0; i < 8; ++i) v[i] = it.c0 + 8 * lane + i < n ? load_elem(p + it.c0 + 8 * lane + i) : 0.f;
+            raw_round(v, u[j]);
         }
     }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+        const int64_t row = it.row + 32 * j;
+        float v[8];
+        raw_values(u[j], v);
+        mx_emit<FP4>(q + row * row_bytes, scales, row, it.c0, pad, lane, row < T, v, mx_top(u[j]));
+    }
 }
 
-template <typename E, bool FP4, bool VEC>
+template <typename E, bool FP4, bool VEC, int J>
 __global__ void __launch_bounds__(ROWS_THREADS)
-    mx_dequantize_kernel(E *out, int64_t ld_out, const unsigned char *q, const uint8_t *scales, int T, int cols,
-                         int r_count, int64_t items) {
-    const int lane = threadIdx.x & 31;
-    const int64_t item = (int64_t)blockIdx.x * (ROWS_THREADS / 32) + (threadIdx.x >> 5);
-    if (item >= items) return;
-    const int64_t pad = mx_padded(cols), groups = (pad + 255) / 256, n_kt = pad / MX_TILE_COLS;
+    mx_dequantize_kernel(E *out, int64_t ld_out, const unsigned char *q, const uint8_t *scales, int T, int cols) {
+    __shared__ __align__(16) float turn[VEC ? 1 : ROWS_THREADS * 8];
+    const int lane = threadIdx.x & 31, pad = (int)mx_padded(cols);
     const int64_t row_bytes = FP4 ? pad / 2 : pad;
-    const RowItem it = row_item(item, r_count, groups);
-    const int64_t col = it.group * 256 + lane * 8;
-    if (col >= cols) return;
-    uint2 e[4];
-    uint32_t code[4];
+    const RowItem it = row_item();
+    const int col = it.c0 + 8 * lane;
+    uint2 e[J];
+    uint32_t code[J];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t row = it.band + it.r + 32 * j;
-        if (row < T) {
+    for (int j = 0; j < J; ++j) {
+        const int64_t row = it.row + 32 * j;
+        e[j] = make_uint2(0, 0), code[j] = 0;
+        if (row < T && col < cols) {
             const unsigned char *p = q + row * row_bytes;
             if (FP4) e[j].x = *reinterpret_cast<const uint32_t *>(p + (col >> 1));
             else e[j] = *reinterpret_cast<const uint2 *>(p + col);
-            code[j] = scales[mx_scale_word(row, col >> 7, n_kt) + ((col >> 5) & 3)];
+            code[j] = scales[mx_scale_word(row, col >> 7, pad / MX_TILE_COLS) + ((col >> 5) & 3)];
         }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int64_t row = it.band + it.r + 32 * j;
-        if (row < T) {
-            float v[8];
-            if (FP4) mx_unpack_e2m1(e[j].x, v);
-            else mx_unpack_e4m3(e[j], v);
-            const float s = mx_scale(code[j]);
+    for (int j = 0; j < J; ++j) {
+        const int64_t row = it.row + 32 * j;
+        if (row >= T) break;
+        float v[8];
+        if (FP4) mx_unpack_e2m1(e[j].x, v);
+        else mx_unpack_e4m3(e[j], v);
+        const float s = mx_scale(code[j]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= s;
-            store8<VEC>(out + row * ld_out + col, cols - col, v);
-        }
+        for (int i = 0; i < 8; ++i) v[i] *= s;
+        if (!VEC) rows_to_lanes(v, turn + (VEC ? 0 : (threadIdx.x >> 5) * 256), lane);
+        typename RawOf<E>::type u;
+        raw_round(v, u);
+        store8<VEC>(out + row * ld_out, it.c0, cols, lane, u);
     }
 }
 
@@ -123,11 +117,12 @@ struct NormArgs {
 enum { NORM_NO_Q = 0, NORM_FP8 = 1, NORM_FP4 = 2 };
 
 // One row per TPR threads.  V > 0: the row stays in registers (V * 8 columns a
-// thread) between the sum of squares and the scaling; V = 0: longer rows, read a
+// thread, as the type holds them: r is rounded to it) between the sum of squares and the scaling; V = 0: longer rows, read a
 // second time (from the stored sum where there is a residual).
 template <typename E, int V, int Q, bool VEC, bool RES>
 __global__ void __launch_bounds__(1024) rms_norm_kernel(const __grid_constant__ NormArgs a, int tpr) {
     __shared__ float part[32];
+    extern __shared__ __align__(16) float turn[];   // 256 floats a warp where !VEC && Q
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t = threadIdx.x % tpr;
     const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
@@ -135,28 +130,42 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const __grid_constant__ 
     const E *x = static_cast<const E *>(a.x) + row * a.ld_x;
     const E *res = RES ? static_cast<const E *>(a.residual) + row * a.ld_r : nullptr;
     E *sum = RES ? static_cast<E *>(a.sum) + row * a.ld_s : nullptr;
-    const int64_t pad = mx_padded(a.d);
-    const int64_t end = Q ? pad : a.d;   // columns the warps walk over
-    float keep[V > 0 ? V : 1][8];
+    const int pad = (int)mx_padded(a.d), end = Q ? pad : a.d;   // columns the warps walk over
+    using Raw = typename RawOf<E>::type;
+    Raw keep[V > 0 ? V : 1];
     float ss = 0.f;
-    auto first = [&](int64_t c, float *v) {   // the row's (summed) 8 columns at c
-        const int64_t n = a.d - c;
-        load8<VEC>(x + c, n, v);
+    auto first = [&](int c0, Raw &u, const Raw &res_u) {   // the warp's (summed) 256 columns at c0
+        float v[8];
+        raw_values(u, v);
         if (RES) {
             float r[8];
-            load8<VEC>(res + c, n, r);
+            raw_values(res_u, r);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = round_to(x, v[i] + r[i]);
-            store8<VEC>(sum + c, n, v);
+            for (int i = 0; i < 8; ++i) v[i] += r[i];
+            raw_round(v, u);
+            store8<VEC>(sum, c0, a.d, lane, u);
+            raw_values(u, v);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
     };
+    const int w0 = 8 * (t - lane), step = 8 * tpr;   // the warp's first columns, and from one to the next
     if (V > 0) {
+        Raw r[RES && V > 0 ? V : 1];
 #pragma unroll
-        for (int k = 0; k < V; ++k) first(8 * ((int64_t)t + (int64_t)k * tpr), keep[k]);
+        for (int k = 0; k < V; ++k) {   // every load first
+            load8<VEC>(x, w0 + k * step, a.d, lane, keep[k]);
+            if (RES) load8<VEC>(res, w0 + k * step, a.d, lane, r[RES ? k : 0]);
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) first(w0 + k * step, keep[k], r[RES ? k : 0]);
     } else {
-        for (int64_t c = 8 * t; c < a.d; c += 8 * (int64_t)tpr) first(c, keep[0]);
+        for (int c0 = w0; c0 < a.d; c0 += step) {
+            Raw r;
+            load8<VEC>(x, c0, a.d, lane, keep[0]);
+            if (RES) load8<VEC>(res, c0, a.d, lane, r);
+            first(c0, keep[0], r);
+        }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(FULL, ss, o);
@@ -170,52 +179,61 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const __grid_constant__ 
     const float rstd = 1.f / sqrtf(ss / (float)a.d + a.eps);
     E *h = a.h ? static_cast<E *>(a.h) + row * a.ld_h : nullptr;
     const E *w = static_cast<const E *>(a.weight);
-    auto second = [&](int64_t c, float *v) {
-        const int64_t n = a.d - c;
-        float g[8];
-        load8<VEC>(w + c, n, g);
+    auto second = [&](int c0, Raw &u) {
+        Raw g;
+        load8<VEC>(w, c0, a.d, lane, g);
+        float v[8], gv[8];
+        raw_values(u, v);
+        raw_values(g, gv);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = round_to(x, v[i] * rstd * g[i]);
-        if (h) store8<VEC>(h + c, n, v);
+        for (int i = 0; i < 8; ++i) v[i] = v[i] * rstd * gv[i];
+        raw_round(v, u);
+        if (h) store8<VEC>(h, c0, a.d, lane, u);
         if (Q) {   // of the rounded row: the base product sees what the adapters see
-            const uint32_t word = mx_scale_warp<Q == NORM_FP4>(v);
-            if (c < pad) {
-                mx_store8<Q == NORM_FP4>(a.q + row * (Q == NORM_FP4 ? pad / 2 : pad), c, v);
-                if ((lane & 15) == 0)
-                    *reinterpret_cast<uint32_t *>(a.scales + mx_scale_word(row, c >> 7, pad / MX_TILE_COLS)) = word;
-            }
+            raw_values(u, v);
+            if (!VEC) lanes_to_rows(v, turn + warp * 256, lane);
+            if (c0 + 256 > a.d)   // columns past the row's end are zeros, which 0 * rstd need not be
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c0 + 8 * lane + i >= a.d) v[i] = 0.f;
+            mx_emit<Q == NORM_FP4>(a.q + row * (Q == NORM_FP4 ? pad / 2 : pad), a.scales, row, c0, pad, lane, true, v, mx_top(v));
         }
     };
     if (V > 0) {
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const int64_t c = 8 * ((int64_t)t + (int64_t)k * tpr);
-            if (c - 8 * lane < end) second(c, keep[k]);   // the whole warp: its first column
-        }
+        for (int k = 0; k < V; ++k)
+            if (w0 + k * step < end) second(w0 + k * step, keep[k]);
     } else {
-        for (int64_t c = 8 * t; c - 8 * lane < end; c += 8 * (int64_t)tpr) {
-            load8<VEC>((RES ? sum : x) + c, a.d - c, keep[0]);
-            second(c, keep[0]);
+        for (int c0 = w0; c0 < end; c0 += step) {
+            load8<VEC>(RES ? sum : x, c0, a.d, lane, keep[0]);
+            second(c0, keep[0]);
         }
     }
 }
 
 template <typename E, int V, int Q, bool VEC>
 void norm_launch_res(const NormArgs &a, int tpr, unsigned blocks, int threads, cudaStream_t st) {
-    if (a.residual) rms_norm_kernel<E, V, Q, VEC, true><<<blocks, threads, 0, st>>>(a, tpr);
-    else rms_norm_kernel<E, V, Q, VEC, false><<<blocks, threads, 0, st>>>(a, tpr);
+    const size_t smem = !VEC && Q ? (size_t)threads * 32 : 0;
+    if (a.residual) rms_norm_kernel<E, V, Q, VEC, true><<<blocks, threads, smem, st>>>(a, tpr);
+    else rms_norm_kernel<E, V, Q, VEC, false><<<blocks, threads, smem, st>>>(a, tpr);
 }
 
 template <typename E, int Q, bool VEC>
 void norm_launch(const NormArgs &a, int sms, cudaStream_t st) {
     const int64_t vecs = (mx_padded(a.d) + 7) / 8;   // 8-column groups of a row
-    // Many rows: four groups a thread (one warp of loads in flight per row); few
-    // rows: one group a thread, the shortest way through one row.
-    int v = a.T >= 4 * sms ? 4 : 1;
+    const bool many = a.T >= 4 * sms;
+    // Few rows: one group a thread, the shortest way through one row.  Many rows: four a thread (loads in
+    // flight), but not more than a warp's share of a short row; rows past the registers of 1024
+    // threads are read twice, the second time from L2.  So are, where there are many, rows whose registers would
+    // leave an SM one block of 1024 threads: bf16 2048 x 28672 67 us in blocks of 512 against 83 us, fp32 as fast
+    // either way; rows off 16-byte steps from 2048 columns on (fp32 4000 x 9001 116 us in blocks of 256, 198 us).
+    int v = many && VEC ? 4 : 1;
+    while (v > 1 && 32 * (v / 2) >= vecs) v /= 2;
     while (v < 4 && vecs > (int64_t)v * 1024) v *= 2;
     int64_t tpr = 32;
     while (tpr < 1024 && tpr * v < vecs) tpr *= 2;
-    if (tpr * v < vecs) v = 0;
+    if (tpr * v < vecs || (many && VEC && sizeof(E) == 2 && vecs > 4 * 512)) v = 0, tpr = 512;
+    if (many && !VEC && vecs > 256) v = 0, tpr = vecs > 2048 ? 512 : 256;
     const int threads = (int)std::max<int64_t>(tpr, tpr == 32 ? 128 : tpr);
     const int rows = threads / (int)tpr;
     const unsigned blocks = (unsigned)((a.T + rows - 1) / rows);
@@ -234,36 +252,43 @@ void norm_dispatch(const NormArgs &a, int q, bool vec, int sms, cudaStream_t st)
     else vec ? norm_launch<E, NORM_FP4, true>(a, sms, st) : norm_launch<E, NORM_FP4, false>(a, sms, st);
 }
 
+// Rows of a warp: four where that still gives every SM 32 warps.
 struct RowGrid {
-    int r_count;
-    int64_t items;
-    unsigned blocks;
+    dim3 grid;
+    bool four;
 };
 RowGrid row_grid(int64_t T, int64_t cols) {
+    const int64_t groups = (mx_padded(cols) + 255) / 256, per = ROWS_THREADS / 32, bands = (T + MX_TILE_ROWS - 1) / MX_TILE_ROWS;
     RowGrid g;
-    const int64_t groups = (mx_padded(cols) + 255) / 256, bands = (T + MX_TILE_ROWS - 1) / MX_TILE_ROWS;
-    g.r_count = (int)std::min<int64_t>(T, 32);
-    g.items = bands * g.r_count * groups;
-    g.blocks = (unsigned)((g.items + ROWS_THREADS / 32 - 1) / (ROWS_THREADS / 32));
+    g.four = groups * T / 4 >= 148 * 32;
+    g.grid = dim3((unsigned)((groups + per - 1) / per), (unsigned)std::min<int64_t>(T, g.four ? 32 : 128), (unsigned)bands);
     return g;
 }
 
-template <typename E, bool FP4>
-void quantize_launch(const lora_mx *m, const void *x, int64_t ld_x, int T, bool vec, cudaStream_t st) {
+template <typename E, bool FP4, bool VEC>
+void quantize_launch_vec(const lora_mx *m, const E *x, int64_t ld_x, int T, cudaStream_t st) {
     const RowGrid g = row_grid(T, m->cols);
     auto *q = static_cast<unsigned char *>(m->q);
-    auto *p = static_cast<const E *>(x);
-    if (vec) mx_quantize_kernel<E, FP4, true><<<g.blocks, ROWS_THREADS, 0, st>>>(q, m->scales, p, ld_x, T, m->cols, g.r_count, g.items);
-    else mx_quantize_kernel<E, FP4, false><<<g.blocks, ROWS_THREADS, 0, st>>>(q, m->scales, p, ld_x, T, m->cols, g.r_count, g.items);
+    if (g.four) mx_quantize_kernel<E, FP4, VEC, 4><<<g.grid, ROWS_THREADS, 0, st>>>(q, m->scales, x, ld_x, T, m->cols);
+    else mx_quantize_kernel<E, FP4, VEC, 1><<<g.grid, ROWS_THREADS, 0, st>>>(q, m->scales, x, ld_x, T, m->cols);
+}
+template <typename E, bool FP4>
+void quantize_launch(const lora_mx *m, const void *x, int64_t ld_x, int T, bool vec, cudaStream_t st) {
+    if (vec) quantize_launch_vec<E, FP4, true>(m, static_cast<const E *>(x), ld_x, T, st);
+    else quantize_launch_vec<E, FP4, false>(m, static_cast<const E *>(x), ld_x, T, st);
 }
 
-template <typename E, bool FP4>
-void dequantize_launch(const lora_mx *m, void *out, int64_t ld_out, int T, bool vec, cudaStream_t st) {
+template <typename E, bool FP4, bool VEC>
+void dequantize_launch_vec(const lora_mx *m, E *out, int64_t ld_out, int T, cudaStream_t st) {
     const RowGrid g = row_grid(T, m->cols);
     auto *q = static_cast<const unsigned char *>(m->q);
-    auto *p = static_cast<E *>(out);
-    if (vec) mx_dequantize_kernel<E, FP4, true><<<g.blocks, ROWS_THREADS, 0, st>>>(p, ld_out, q, m->scales, T, m->cols, g.r_count, g.items);
-    else mx_dequantize_kernel<E, FP4, false><<<g.blocks, ROWS_THREADS, 0, st>>>(p, ld_out, q, m->scales, T, m->cols, g.r_count, g.items);
+    if (g.four) mx_dequantize_kernel<E, FP4, VEC, 4><<<g.grid, ROWS_THREADS, 0, st>>>(out, ld_out, q, m->scales, T, m->cols);
+    else mx_dequantize_kernel<E, FP4, VEC, 1><<<g.grid, ROWS_THREADS, 0, st>>>(out, ld_out, q, m->scales, T, m->cols);
+}
+template <typename E, bool FP4>
+void dequantize_launch(const lora_mx *m, void *out, int64_t ld_out, int T, bool vec, cudaStream_t st) {
+    if (vec) dequantize_launch_vec<E, FP4, true>(m, static_cast<E *>(out), ld_out, T, st);
+    else dequantize_launch_vec<E, FP4, false>(m, static_cast<E *>(out), ld_out, T, st);
 }
 
 }  // namespace

@@ -174,6 +174,27 @@ def test_norm_microscaled_output_is_quantized_h(cuda_lib, T, d, fmt, dtype):
     assert torch.equal(b.q, c.q) and torch.equal(b.scales, c.scales)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("d", [8, 77, 136, 1003, 33008])
+def test_norm_microscaled_rows_of_nan(cuda_lib, d, fmt, dtype):
+    """Rows whose norm is not finite: every block of the row reads back as NaN where h does, and the
+    padding's blocks stay zeros with e = 0."""
+    x = torch.ones(3, d, dtype=dtype, device="cuda")
+    x[0, d // 2] = float("nan")
+    x[1, 0] = float("inf")
+    w, h = torch.ones(d, dtype=dtype, device="cuda"), torch.empty_like(x)
+    a, b = lora.MxTensor(3, d, fmt), lora.MxTensor(3, d, fmt)
+    a.q.fill_(0xFF), a.scales.fill_(0xFF)
+    lora.lora_rms_norm(h, x, w, 1e-5, q=a)
+    lora.lora_mx_quantize(b, h)
+    ca, sa = from_device(a)
+    cb, sb = from_device(b)
+    np.testing.assert_array_equal(ca, cb)
+    np.testing.assert_array_equal(sa, sb)
+    assert (sa[0, :-(-d // 32)] == 255).all() and (sa[:, -(-d // 32):] == 0).all() and (ca[:, d:] == 0).all()
+
+
 @pytest.mark.parametrize("d", [96, 1003, 8192, 33000])
 def test_norm_in_place_and_strided(cuda_lib, d):
     T = 20
