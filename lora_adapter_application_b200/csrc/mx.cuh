@@ -248,6 +248,32 @@ __device__ __forceinline__ uint32_t mx_top(const float *v) {
     return m;
 }
 
+// Programmatic dependent launch: a kernel launched by launch_after may be set up while the one before it on
+// the stream ends.  pdl_wait: everything before it on the stream has completed and is visible (ahead of any access to
+// memory that other kernels use).  pdl_next: the next kernel's blocks may come, once every block of this one has said
+// so or ended (they then wait in their own pdl_wait).
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void pdl_next() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
+template <typename... P, typename... A>
+int launch_after(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, unsigned cluster, cudaStream_t st, A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+    return cuda_rc(e != cudaSuccess ? e : cudaGetLastError());
+}
+
 // tmaps.cu: a map over the bytes of a microscaled matrix's q
 int tensor_map_mx(CUtensorMap *out, const void *base, uint64_t inner, uint64_t rows, uint64_t pitch,
                   uint32_t box_rows, bool packed4);

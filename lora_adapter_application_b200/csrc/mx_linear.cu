@@ -257,6 +257,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
     }
     if (S > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");   // this block's barriers are set
     const uint32_t sf = tmem + 2 * acc_cols;
+    pdl_next();
+    if (warp < 1 || warp > 5) pdl_wait();   // the copying and the storing warps
 
     if (warp == 0) {
         for (; t < a.tiles && !failed; next_tile())
@@ -482,19 +484,9 @@ int launch_few_kt(MxFewArgs &a, int dev, int64_t limit_ns, int *took, cudaStream
     const size_t room = MX_MAX_SMEM - 1024 - (plan.split_log2 && a.own_red ? (size_t)(a.bn + 8) * 512 : 0);
     a.stages = (int)std::min<size_t>(FEW_STAGES, room / few_slot_bytes<KIND>(KT, a.bn, a.bands));
     a.stages = std::min(a.stages, (512 - 2 * acc_cols) / (int)few_sf_cols(KT, a.bn));
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(plan.clusters << plan.split_log2));
-    cfg.blockDim = dim3(FEW_THREADS);
-    cfg.dynamicSmemBytes = MX_MAX_SMEM;   // one block an SM: two might wait for each other's tensor memory
-    cfg.stream = st;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 1u << plan.split_log2;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, mx_linear_few_kernel<KIND, KT, Y>, a);
-    return cuda_rc(e != cudaSuccess ? e : cudaGetLastError());
+    // all of the shared memory: one block an SM (two might wait for each other's tensor memory)
+    return launch_after(mx_linear_few_kernel<KIND, KT, Y>, dim3((unsigned)(plan.clusters << plan.split_log2)), FEW_THREADS, MX_MAX_SMEM,
+                        1u << plan.split_log2, st, a);
 }
 
 template <int KIND, typename Y>
@@ -621,6 +613,8 @@ __global__ void __launch_bounds__(BIG_THREADS, 1) mx_linear_big_kernel(const __g
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(FULL, tmem_sm, 0), sf = tmem + 256;
     bool failed = false;
+    pdl_next();
+    if (warp < 1 || warp > 5) pdl_wait();   // the copying and the storing warps
 
     if (warp == 0) {
         Ring ring(BIG_STAGES);
@@ -782,19 +776,8 @@ int launch_big(const MxLinArgs &l, const lora_mx *x, const lora_mx *w, int sms, 
     auto kernel = mx_linear_big_kernel<KIND, BF16>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)MX_MAX_SMEM);
     if (e != cudaSuccess) return cuda_rc(e);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(2 * std::min(a.tiles, sms / 2)));
-    cfg.blockDim = dim3(BIG_THREADS);
-    cfg.dynamicSmemBytes = MX_MAX_SMEM;   // one block an SM, by its tensor memory
-    cfg.stream = st;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kernel, a);
-    return cuda_rc(e != cudaSuccess ? e : cudaGetLastError());
+    // all of the shared memory: one block an SM, as its tensor memory asks for
+    return launch_after(kernel, dim3((unsigned)(2 * std::min(a.tiles, sms / 2))), BIG_THREADS, MX_MAX_SMEM, 2, st, a);
 }
 
 // Few rows or many, by the time each would take.  The pair kernel: 5.5 us, and per round of its 256 x 256 tiles 3.5 us

@@ -35,6 +35,8 @@ __global__ void __launch_bounds__(ROWS_THREADS)
     const int lane = threadIdx.x & 31, pad = (int)mx_padded(cols);
     const int64_t row_bytes = FP4 ? pad / 2 : pad;
     const RowItem it = row_item();
+    pdl_next();
+    pdl_wait();
     if (it.c0 >= pad) return;
     Raw u[J];
 #pragma unroll
@@ -68,6 +70,8 @@ __global__ void __launch_bounds__(ROWS_THREADS)
     const int64_t row_bytes = FP4 ? pad / 2 : pad;
     const RowItem it = row_item();
     const int col = it.c0 + 8 * lane;
+    pdl_next();
+    pdl_wait();
     uint2 e[J];
     uint32_t code[J];
 #pragma unroll
@@ -126,6 +130,8 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const __grid_constant__ 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t = threadIdx.x % tpr;
     const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
+    pdl_next();
+    pdl_wait();
     if (row >= a.T) return;   // whole warps; only blocks of one warp per row hold several rows
     const E *x = static_cast<const E *>(a.x) + row * a.ld_x;
     const E *res = RES ? static_cast<const E *>(a.residual) + row * a.ld_r : nullptr;
@@ -212,14 +218,14 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(const __grid_constant__ 
 }
 
 template <typename E, int V, int Q, bool VEC>
-void norm_launch_res(const NormArgs &a, int tpr, unsigned blocks, int threads, cudaStream_t st) {
+int norm_launch_res(const NormArgs &a, int tpr, unsigned blocks, int threads, cudaStream_t st) {
     const size_t smem = !VEC && Q ? (size_t)threads * 32 : 0;
-    if (a.residual) rms_norm_kernel<E, V, Q, VEC, true><<<blocks, threads, smem, st>>>(a, tpr);
-    else rms_norm_kernel<E, V, Q, VEC, false><<<blocks, threads, smem, st>>>(a, tpr);
+    if (a.residual) return launch_after(rms_norm_kernel<E, V, Q, VEC, true>, dim3(blocks), (unsigned)threads, smem, 0, st, a, tpr);
+    return launch_after(rms_norm_kernel<E, V, Q, VEC, false>, dim3(blocks), (unsigned)threads, smem, 0, st, a, tpr);
 }
 
 template <typename E, int Q, bool VEC>
-void norm_launch(const NormArgs &a, int sms, cudaStream_t st) {
+int norm_launch(const NormArgs &a, int sms, cudaStream_t st) {
     const int64_t vecs = (mx_padded(a.d) + 7) / 8;   // 8-column groups of a row
     const bool many = a.T >= 4 * sms;
     // Few rows: one group a thread, the shortest way through one row.  Many rows: four a thread (loads in
@@ -238,18 +244,18 @@ void norm_launch(const NormArgs &a, int sms, cudaStream_t st) {
     const int rows = threads / (int)tpr;
     const unsigned blocks = (unsigned)((a.T + rows - 1) / rows);
     switch (v) {
-        case 1: norm_launch_res<E, 1, Q, VEC>(a, (int)tpr, blocks, threads, st); break;
-        case 2: norm_launch_res<E, 2, Q, VEC>(a, (int)tpr, blocks, threads, st); break;
-        case 4: norm_launch_res<E, 4, Q, VEC>(a, (int)tpr, blocks, threads, st); break;
-        default: norm_launch_res<E, 0, Q, VEC>(a, (int)tpr, blocks, threads, st);
+        case 1: return norm_launch_res<E, 1, Q, VEC>(a, (int)tpr, blocks, threads, st);
+        case 2: return norm_launch_res<E, 2, Q, VEC>(a, (int)tpr, blocks, threads, st);
+        case 4: return norm_launch_res<E, 4, Q, VEC>(a, (int)tpr, blocks, threads, st);
+        default: return norm_launch_res<E, 0, Q, VEC>(a, (int)tpr, blocks, threads, st);
     }
 }
 
 template <typename E>
-void norm_dispatch(const NormArgs &a, int q, bool vec, int sms, cudaStream_t st) {
-    if (q == NORM_NO_Q) vec ? norm_launch<E, NORM_NO_Q, true>(a, sms, st) : norm_launch<E, NORM_NO_Q, false>(a, sms, st);
-    else if (q == NORM_FP8) vec ? norm_launch<E, NORM_FP8, true>(a, sms, st) : norm_launch<E, NORM_FP8, false>(a, sms, st);
-    else vec ? norm_launch<E, NORM_FP4, true>(a, sms, st) : norm_launch<E, NORM_FP4, false>(a, sms, st);
+int norm_dispatch(const NormArgs &a, int q, bool vec, int sms, cudaStream_t st) {
+    if (q == NORM_NO_Q) return vec ? norm_launch<E, NORM_NO_Q, true>(a, sms, st) : norm_launch<E, NORM_NO_Q, false>(a, sms, st);
+    if (q == NORM_FP8) return vec ? norm_launch<E, NORM_FP8, true>(a, sms, st) : norm_launch<E, NORM_FP8, false>(a, sms, st);
+    return vec ? norm_launch<E, NORM_FP4, true>(a, sms, st) : norm_launch<E, NORM_FP4, false>(a, sms, st);
 }
 
 // Rows of a warp: four where that still gives every SM 32 warps.
@@ -266,29 +272,28 @@ RowGrid row_grid(int64_t T, int64_t cols) {
 }
 
 template <typename E, bool FP4, bool VEC>
-void quantize_launch_vec(const lora_mx *m, const E *x, int64_t ld_x, int T, cudaStream_t st) {
+int quantize_launch_vec(const lora_mx *m, const E *x, int64_t ld_x, int T, cudaStream_t st) {
     const RowGrid g = row_grid(T, m->cols);
-    auto *q = static_cast<unsigned char *>(m->q);
-    if (g.four) mx_quantize_kernel<E, FP4, VEC, 4><<<g.grid, ROWS_THREADS, 0, st>>>(q, m->scales, x, ld_x, T, m->cols);
-    else mx_quantize_kernel<E, FP4, VEC, 1><<<g.grid, ROWS_THREADS, 0, st>>>(q, m->scales, x, ld_x, T, m->cols);
+    auto kernel = g.four ? mx_quantize_kernel<E, FP4, VEC, 4> : mx_quantize_kernel<E, FP4, VEC, 1>;
+    return launch_after(kernel, g.grid, ROWS_THREADS, 0, 0, st, static_cast<unsigned char *>(m->q), m->scales, x, ld_x, T, m->cols);
 }
 template <typename E, bool FP4>
-void quantize_launch(const lora_mx *m, const void *x, int64_t ld_x, int T, bool vec, cudaStream_t st) {
-    if (vec) quantize_launch_vec<E, FP4, true>(m, static_cast<const E *>(x), ld_x, T, st);
-    else quantize_launch_vec<E, FP4, false>(m, static_cast<const E *>(x), ld_x, T, st);
+int quantize_launch(const lora_mx *m, const void *x, int64_t ld_x, int T, bool vec, cudaStream_t st) {
+    return vec ? quantize_launch_vec<E, FP4, true>(m, static_cast<const E *>(x), ld_x, T, st)
+               : quantize_launch_vec<E, FP4, false>(m, static_cast<const E *>(x), ld_x, T, st);
 }
 
 template <typename E, bool FP4, bool VEC>
-void dequantize_launch_vec(const lora_mx *m, E *out, int64_t ld_out, int T, cudaStream_t st) {
+int dequantize_launch_vec(const lora_mx *m, E *out, int64_t ld_out, int T, cudaStream_t st) {
     const RowGrid g = row_grid(T, m->cols);
-    auto *q = static_cast<const unsigned char *>(m->q);
-    if (g.four) mx_dequantize_kernel<E, FP4, VEC, 4><<<g.grid, ROWS_THREADS, 0, st>>>(out, ld_out, q, m->scales, T, m->cols);
-    else mx_dequantize_kernel<E, FP4, VEC, 1><<<g.grid, ROWS_THREADS, 0, st>>>(out, ld_out, q, m->scales, T, m->cols);
+    auto kernel = g.four ? mx_dequantize_kernel<E, FP4, VEC, 4> : mx_dequantize_kernel<E, FP4, VEC, 1>;
+    return launch_after(kernel, g.grid, ROWS_THREADS, 0, 0, st, out, ld_out, static_cast<const unsigned char *>(m->q), m->scales, T,
+                        m->cols);
 }
 template <typename E, bool FP4>
-void dequantize_launch(const lora_mx *m, void *out, int64_t ld_out, int T, bool vec, cudaStream_t st) {
-    if (vec) dequantize_launch_vec<E, FP4, true>(m, static_cast<E *>(out), ld_out, T, st);
-    else dequantize_launch_vec<E, FP4, false>(m, static_cast<E *>(out), ld_out, T, st);
+int dequantize_launch(const lora_mx *m, void *out, int64_t ld_out, int T, bool vec, cudaStream_t st) {
+    return vec ? dequantize_launch_vec<E, FP4, true>(m, static_cast<E *>(out), ld_out, T, st)
+               : dequantize_launch_vec<E, FP4, false>(m, static_cast<E *>(out), ld_out, T, st);
 }
 
 }  // namespace
@@ -331,12 +336,9 @@ int lora_mx_quantize(const lora_mx *q, const void *x, int64_t ld_x, int32_t T, l
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool fp4 = q->format == LORA_MXFP4, vec = mx_vec(x, ld_x, q->cols, dtype == LORA_BF16 ? 2 : 4);
     if (dtype == LORA_BF16)
-        fp4 ? quantize_launch<__nv_bfloat16, true>(q, x, ld_x, T, vec, st)
-            : quantize_launch<__nv_bfloat16, false>(q, x, ld_x, T, vec, st);
-    else
-        fp4 ? quantize_launch<float, true>(q, x, ld_x, T, vec, st)
-            : quantize_launch<float, false>(q, x, ld_x, T, vec, st);
-    return cuda_rc(cudaGetLastError());
+        return fp4 ? quantize_launch<__nv_bfloat16, true>(q, x, ld_x, T, vec, st)
+                   : quantize_launch<__nv_bfloat16, false>(q, x, ld_x, T, vec, st);
+    return fp4 ? quantize_launch<float, true>(q, x, ld_x, T, vec, st) : quantize_launch<float, false>(q, x, ld_x, T, vec, st);
 }
 
 int lora_mx_dequantize(void *out, int64_t ld_out, const lora_mx *q, int32_t T, lora_dtype dtype, void *stream) {
@@ -351,12 +353,9 @@ int lora_mx_dequantize(void *out, int64_t ld_out, const lora_mx *q, int32_t T, l
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool fp4 = q->format == LORA_MXFP4, vec = mx_vec(out, ld_out, q->cols, dtype == LORA_BF16 ? 2 : 4);
     if (dtype == LORA_BF16)
-        fp4 ? dequantize_launch<__nv_bfloat16, true>(q, out, ld_out, T, vec, st)
-            : dequantize_launch<__nv_bfloat16, false>(q, out, ld_out, T, vec, st);
-    else
-        fp4 ? dequantize_launch<float, true>(q, out, ld_out, T, vec, st)
-            : dequantize_launch<float, false>(q, out, ld_out, T, vec, st);
-    return cuda_rc(cudaGetLastError());
+        return fp4 ? dequantize_launch<__nv_bfloat16, true>(q, out, ld_out, T, vec, st)
+                   : dequantize_launch<__nv_bfloat16, false>(q, out, ld_out, T, vec, st);
+    return fp4 ? dequantize_launch<float, true>(q, out, ld_out, T, vec, st) : dequantize_launch<float, false>(q, out, ld_out, T, vec, st);
 }
 
 int lora_rms_norm(void *h, int64_t ld_h, const void *x, int64_t ld_x, const void *residual, int64_t ld_r,
@@ -386,9 +385,7 @@ int lora_rms_norm(void *h, int64_t ld_h, const void *x, int64_t ld_x, const void
     if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int form = !q ? NORM_NO_Q : q->format == LORA_MXFP4 ? NORM_FP4 : NORM_FP8;
-    if (dtype == LORA_BF16) norm_dispatch<__nv_bfloat16>(a, form, vec, sms, st);
-    else norm_dispatch<float>(a, form, vec, sms, st);
-    return cuda_rc(cudaGetLastError());
+    return dtype == LORA_BF16 ? norm_dispatch<__nv_bfloat16>(a, form, vec, sms, st) : norm_dispatch<float>(a, form, vec, sms, st);
 }
 
 }  // extern "C"
