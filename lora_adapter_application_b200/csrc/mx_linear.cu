@@ -140,6 +140,25 @@ struct Ring {
     __device__ bool reused() const { return left == 0; }
 };
 
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {   // address mapped with map_rank
+    asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(addr), "f"(v) : "memory");
+}
+// Every other row from `from` of a block's `to` rows: the S partial sums at
+// [source][row of own][128 features], in order, to y.
+template <int S, typename Y>
+__device__ __forceinline__ void sum_rows(Y *y, int64_t ld, uint32_t red, int own, int from, int to) {
+#pragma unroll 4
+    for (int j = from; j < to; j += 2) {
+        float v[S];
+#pragma unroll
+        for (int k = 0; k < S; ++k) v[k] = __uint_as_float(lds32(red + (uint32_t)(k * own + j) * 512u));
+        float t = v[0];
+#pragma unroll
+        for (int k = 1; k < S; ++k) t += v[k];
+        store_elem(y + j * ld, t);
+    }
+}
+
 // after a failed wait: the copies that a thread has under way into a ring land before its block goes
 __device__ __forceinline__ void drain_ring(Ring r, uint32_t full) {
     for (int j = 0; j < r.n; ++j, r.next())   // oldest first: parity ^ 1 is that of the slot's last use
@@ -377,30 +396,37 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
                         if (there && c + j < rows) store_elem(p, d[j]);
                 }
             } else {
-                const int own = (rows + S - 1) / S;   // rows of a block
-                if (!a.own_red) cluster_sync_all();   // every block's products are done with its ring
+                // rows of a block: a power of two up to 16, or a multiple of 16, so that 16 rows' owners follow from
+                // shifts or are one
+                const int fair = (rows + S - 1) >> a.split_log2, own_log2 = fair <= 1 ? 0 : 32 - __clz(min(fair, 16) - 1);
+                const int own = fair <= 16 ? 1 << own_log2 : (fair + 15) & ~15;
                 const uint32_t mine = red + (uint32_t)(rank * own * 128 + f) * 4u;   // [source][row][feature]
+                if (!a.own_red) cluster_sync_all();   // every block's products are done with its ring
                 for (int c = half; c < rows; c += 32) {
                     float d[16];
                     tc_ld16(src_acc + c, d);
-                    int to = c / own, left = own - (c - to * own);
-                    uint32_t at = map_rank(mine, (uint32_t)to) + (uint32_t)(own - left) * 512u;
-                    tc_wait_ld();
+                    if (own >= 16) {
+                        const int to = c / own;
+                        const uint32_t at = map_rank(mine, (uint32_t)to) + (uint32_t)(c - to * own) * 512u;
+                        tc_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        if (c + j >= rows) break;
-                        asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(at), "f"(d[j]) : "memory");
-                        at += 512;
-                        if (--left == 0) left = own, at = map_rank(mine, (uint32_t)min(++to, S - 1));
+                        for (int i = 0; i < 16; ++i)
+                            if (c + i < rows) st_cluster(at + 512u * i, d[i]);
+                    } else {
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (c + i < rows)
+                                st_cluster(map_rank(mine, (uint32_t)(c + i) >> own_log2) + 512u * (i & (own - 1)), d[i]);
                     }
                 }
                 cluster_sync_all();
-                Y *p = y + (int64_t)(rank * own + (half >> 4)) * a.ld_y;
-                for (int j = half >> 4; there && j < min(own, rows - rank * own); j += 2, p += 2 * a.ld_y) {
-                    const uint32_t at = red + (uint32_t)(j * 128 + f) * 4u;
-                    float v = 0.f;
-                    for (int src = 0; src < S; ++src) v += __uint_as_float(lds32(at + (uint32_t)(src * own) * 512u));
-                    store_elem(p, v);
+                if (there) {
+                    const int to = min(own, rows - rank * own);
+                    Y *p = y + (int64_t)(rank * own) * a.ld_y;
+                    if (S == 2) sum_rows<2>(p, a.ld_y, red + 4u * f, own, half >> 4, to);
+                    else if (S == 4) sum_rows<4>(p, a.ld_y, red + 4u * f, own, half >> 4, to);
+                    else sum_rows<8>(p, a.ld_y, red + 4u * f, own, half >> 4, to);
                 }
             }
             tc_fence_before();
@@ -481,7 +507,7 @@ int launch_few_kt(MxFewArgs &a, int dev, int64_t limit_ns, int *took, cudaStream
     a.split_log2 = plan.split_log2;
     const int acc_cols = (a.bn + 31) / 32 * 32;
     a.own_red = a.bn <= 32;
-    const size_t room = MX_MAX_SMEM - 1024 - (plan.split_log2 && a.own_red ? (size_t)(a.bn + 8) * 512 : 0);
+    const size_t room = MX_MAX_SMEM - 1024 - (plan.split_log2 && a.own_red ? (size_t)(2 * a.bn + 16) * 512 : 0);
     a.stages = (int)std::min<size_t>(FEW_STAGES, room / few_slot_bytes<KIND>(KT, a.bn, a.bands));
     a.stages = std::min(a.stages, (512 - 2 * acc_cols) / (int)few_sf_cols(KT, a.bn));
     // all of the shared memory: one block an SM (two might wait for each other's tensor memory)
@@ -515,11 +541,14 @@ int launch_few(const MxLinArgs &l, const lora_mx *x, const lora_mx *w, int dev, 
 // tensor cores share the halves, so a block moves 32 KB of a stage for 256 x 256 x 32
 // bytes of products, half of what two 128 x 256 tiles would.  At the 4-bit rate that
 // is 64 bytes a clock and SM from L2: the reason for the pair.  Persistent: pair p
-// takes tiles p, p + pairs, ..., x's tiles fastest (concurrent pairs share W's rows and keep x in L2).
+// takes tiles p, p + pairs, ... of bands of 16 x tiles, x's tiles fastest: concurrent pairs share W's rows and few enough
+// of x's to find both in the nearer half of L2 (8192 x 8192 x 28672 in MXFP8, steady 1650 -> 1510 us;
+// 8192 x 4096 x 4096 in MXFP4 66.6 -> 65.0).
 // The fp32 accumulator (256 columns) is drained to registers by eight warps in one
 // go, the next tile's products start, and the rows are stored meanwhile.
 constexpr int BIG_THREADS = 448;      // warp 0 copies, warp 1 MMAs, warps 2-5 scales, warps 6-13 epilogue
 constexpr int BIG_STAGES = 6;
+constexpr int BIG_BAND = 16;
 
 struct MxBigArgs {
     CUtensorMap tmX, tmW;
@@ -528,7 +557,7 @@ struct MxBigArgs {
     void *y;
     int64_t ld_y;
     int T, d_out, n_kt, n_stage;
-    int mt, tiles;    // 256-row tiles of x; all tiles
+    int mt, nt, tiles;    // 256-row tiles of x, of W; all
     int vec;          // y rows allow 16-byte stores
     int32_t *status;
 };
@@ -615,11 +644,18 @@ __global__ void __launch_bounds__(BIG_THREADS, 1) mx_linear_big_kernel(const __g
     bool failed = false;
     pdl_next();
     if (warp < 1 || warp > 5) pdl_wait();   // the copying and the storing warps
+    auto place = [&](int t, int &mi, int &ni) {   // of tile t
+        const int per = BIG_BAND * a.nt, band = t / per, left = t - band * per, high = min(BIG_BAND, a.mt - band * BIG_BAND);
+        ni = left / high;
+        mi = band * BIG_BAND + left - ni * high;
+    };
 
     if (warp == 0) {
         Ring ring(BIG_STAGES);
         for (int t = pair; t < a.tiles && !failed; t += pairs) {
-            const int m0 = (t % a.mt) * 256 + 128 * rank, nb = t / a.mt * 2;   // nb: first 128-row band of W
+            int mi, ni;
+            place(t, mi, ni);
+            const int m0 = mi * 256 + 128 * rank, nb = 2 * ni;   // nb: first 128-row band of W
             // bands past the last hold rows that no result uses: any scales will do
             const uint8_t *sx = a.sx + (int64_t)min(m0 / 128, a.x_bands - 1) * a.n_kt * MX_TILE_BYTES;
             const uint8_t *sw0 = a.sw + (int64_t)nb * a.n_kt * MX_TILE_BYTES;
@@ -700,8 +736,9 @@ __global__ void __launch_bounds__(BIG_THREADS, 1) mx_linear_big_kernel(const __g
         for (int t = pair; t < a.tiles; t += pairs, ++n) {
             if (!warp_wait(acc_full, (unsigned)n & 1u, a.status, failed)) break;
             tc_fence_after();
-            const int64_t row = (int64_t)(t % a.mt) * 256 + 128 * rank + 32 * q + lane;
-            const int64_t col = (int64_t)(t / a.mt) * 256 + 128 * half;
+            int mi, ni;
+            place(t, mi, ni);
+            const int64_t row = (int64_t)mi * 256 + 128 * rank + 32 * q + lane, col = (int64_t)ni * 256 + 128 * half;
             auto drained = [&] {   // this warp's part of the accumulator is in registers
                 tc_fence_before();
                 __syncwarp();
@@ -770,7 +807,8 @@ int launch_big(const MxLinArgs &l, const lora_mx *x, const lora_mx *w, int sms, 
     a.sx = l.sx, a.sw = l.sw, a.x_bands = (l.T + 127) / 128, a.w_bands = (l.d_out + 127) / 128;
     a.y = l.y, a.ld_y = l.ld_y, a.T = l.T, a.d_out = l.d_out, a.n_kt = l.n_kt, a.n_stage = l.n_stage;
     a.mt = (l.T + 255) / 256;
-    a.tiles = a.mt * ((l.d_out + 255) / 256);
+    a.nt = (l.d_out + 255) / 256;
+    a.tiles = a.mt * a.nt;
     a.vec = mx_vec(l.y, l.ld_y, l.d_out, BF16 ? 2 : 4);
     a.status = l.status;
     auto kernel = mx_linear_big_kernel<KIND, BF16>;
