@@ -449,10 +449,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
     }
 }
 
-// Blocks along k and clusters of them, by the time they would take: a scale tile of k costs a block what W's 8 KB of
-// it take from HBM (215 ns a block) or its operands take into shared memory (98 bytes a ns), an
-// exchange of partial sums 1.5 us and 40 ns a row.  Measured: 64 x 4096 x 6144 11.0 us whole, 11.6 in two;
-// 64 x 4096 x 4096 10.6, 11.0 in two, 9.7 in four; 1 x 4096 x 4096 9.6, 7.8, 7.0; 257 x 14336 x 4096 40.9, 30.0.
+// Blocks along k and clusters of them, by the time they would take: a scale tile of k costs a block 180 (MXFP8) or
+// 150 ns, more from 64 rows on, when the operands' way into shared memory bounds it; an exchange of partial sums 0.95 us for each
+// doubling of S and 12 ns a row; all 3 us and 8 ns a row besides.  Measured (us, S = 1, 2, 4): 1 x 4096 x 4096 7.8, 6.0,
+// 5.6; 64 x 4096 x 4096 9.0, 7.9, 7.3; 64 x 1024 x 4096 4.7, 5.4, 5.4; 128 x 4096 x 4096 11.9, 10.1, 9.4;
+// 257 x 14336 x 4096 38.7, 24.6.
 struct FewPlan {
     int split_log2 = 0, clusters = 1;
     int64_t ns = 0;
@@ -484,15 +485,15 @@ int few_plan(const MxFewArgs &a, int dev, FewPlan *out) {
         }
         if (e != cudaSuccess) return cuda_rc(e);
     }
-    const int64_t kt_ns = std::max(215, KIND == MX_A8 ? 167 + 13 * a.bn / 10 : 83 + 65 * a.bn / 100);
+    const int64_t kt_ns = KIND == MX_A8 ? std::max(180, 110 + 12 * a.bn / 10) : std::max(150, 90 + 66 * a.bn / 100);
     int64_t best = -1;
     for (int i = 0; i < 4; ++i) {
         const int s = 1 << i, n = std::min(a.tiles, f[i]);
         if (s > a.n_ks || (i && n < a.tiles)) break;
-        const int64_t cost = (int64_t)((a.tiles + n - 1) / n) * ((a.n_ks + s - 1) / s) * KT * kt_ns + (i ? 1500 + 40 * a.bn : 0);
+        const int64_t cost = (int64_t)((a.tiles + n - 1) / n) * ((a.n_ks + s - 1) / s) * KT * kt_ns + (i ? 950 * i + 12 * a.bn : 0);
         if (best < 0 || cost < best) best = cost, out->split_log2 = i, out->clusters = n;
     }
-    out->ns = best + 4500;
+    out->ns = best + 3000 + 8 * a.bn;
     return LORA_OK;
 }
 
@@ -818,14 +819,15 @@ int launch_big(const MxLinArgs &l, const lora_mx *x, const lora_mx *w, int sms, 
     return launch_after(kernel, dim3((unsigned)(2 * std::min(a.tiles, sms / 2))), BIG_THREADS, MX_MAX_SMEM, 2, st, a);
 }
 
-// Few rows or many, by the time each would take.  The pair kernel: 5.5 us, and per round of its 256 x 256 tiles 3.5 us
-// and 360 (MXFP8) or 180 ns a scale tile of k.  Measured, 4096 -> 28672 and 14336 -> 4096 with x in MXFP8, us few / many:
-// 128 rows 25.9 / 35.6, -; 256 rows 45.9 / 36.9, 27.0 / 45.4; 512 rows 61.7 / 61.8, 42.2 / 45.3; in MXFP4: 128 rows
-// 19.0 / 25.1, -; 256 rows 28.3 / 26.0, 19.9 / 25.0; 512 rows 41.4 / 40.3, 28.3 / 25.6.
+// Few rows or many, by the time each would take.  The pair kernel: 4.5 us, and per round of its 256 x 256 tiles 3.5 us
+// and 310 (MXFP8) or 165 ns a scale tile of k.  Measured, us few / many, MXFP8 then MXFP4: 128 x 4096 x 28672 24.9 / 31.6,
+// 18.4 / 23.8; 256 x 4096 x 28672 44.4 / 32.2, 27.1 / 24.3; 256 x 14336 x 4096 22.9 / 39.7, 15.8 / 23.9;
+// 512 x 14336 x 4096 43.2 / 40.4, 27.7 / 24.5; 768 x 4096 x 4096 15.9 / 17.4, 10.7 / 12.4; 1024 x 14336 x 1024 25.5 / 39.2,
+// 18.0 / 23.4.
 template <int KIND, typename Y>
 int launch_linear(const MxLinArgs &a, const lora_mx *x, const lora_mx *w, int dev, int sms, cudaStream_t st) {
     const int64_t tiles = (int64_t)((a.T + 255) / 256) * ((a.d_out + 255) / 256), pairs = std::max(1, sms / 2);
-    const int64_t many_ns = 5500 + (tiles + pairs - 1) / pairs * (3500 + (int64_t)a.n_kt * (KIND == MX_A8 ? 360 : 180));
+    const int64_t many_ns = 4500 + (tiles + pairs - 1) / pairs * (3500 + (int64_t)a.n_kt * (KIND == MX_A8 ? 310 : 165));
     int took = 0;
     const int rc = launch_few<KIND, Y>(a, x, w, dev, many_ns, &took, st);
     if (rc != LORA_OK || took) return rc;
