@@ -166,13 +166,14 @@ __device__ __forceinline__ void drain_ring(Ring r, uint32_t full) {
 }
 
 // ---------------------------------------------------------------- few rows
-// A cluster takes 128 output features (the MMA's M side: W's rows, which a small
+// A cluster takes 128 MT output features (the MMA's M side: W's rows, which a small
 // batch reads once) x BN rows of x (its N side, any multiple of 16 up to 192), each of its S
 // blocks over 1 / S of k; persistent, cluster c takes tiles c, c + clusters, ....
 // A ring slot holds KT scale tiles of k (128 columns each): two, or one where wide x tiles would leave too few
-// slots.  Roles: one warp copies W, one x and scales, one issues MMAs, four move scales from
-// shared to tensor memory, four take the finished
-// accumulator (two of them, so the next tile's products overlap).  S > 1 only where every cluster has one tile:
+// slots.  Roles: one warp copies W and its scales, one x and its, one issues MMAs, four move scales from
+// shared to tensor memory, eight take the finished
+// accumulator.  There are two: one tile's sums are stored while the next one's products go on; or, MT = 2, one for each
+// 128 features, which reads x once for both and may leave a block one tile in place of two (256 x 4096 x 14336 25.4 -> 20.5 us).  S > 1 only where every cluster has one tile:
 // its blocks then add their partial sums, in block order, through distributed shared memory: each owns
 // 1 / S of the rows, and gets the others' sums by plain stores between cluster barriers (st.async, which counts every
 // 16 bytes on a barrier, took 1.4 us per 16 rows).  They land behind the ring (few rows) or, once every
@@ -181,7 +182,7 @@ __device__ __forceinline__ void drain_ring(Ring r, uint32_t full) {
 // Bound: W's bytes from HBM (64 rows, 4096 -> 28672: 66 MB), or, per SM, filling shared memory.  What
 // a warp does per slot counts as much: a stage of the MMA warp with a barrier for each 128
 // columns and one for its scales took 1200 clocks per 256 columns, the products 320.
-// warp 0 copies W, 1 MMAs, 2-5 scales, 6-9 and 11-14 sums and stores (every other 16 rows), 10 copies x and scales
+// warp 0 copies W, 1 MMAs, 2-5 scales, 6-9 and 11-14 sums and stores (every other 16 rows), 10 copies x
 constexpr int FEW_THREADS = 480;
 constexpr int FEW_STAGES = 12;
 constexpr int FEW_ROWS = 192;         // widest BN
@@ -194,34 +195,34 @@ struct MxFewArgs {
     int64_t ld_y;
     int T, d_out, n_kt, n_ks;   // k in scale tiles and in ring slots
     int bn, nt, tiles;          // rows of a tile, row tiles, all tiles
-    int bands, x_bands;         // 128-row bands of x scales one tile may touch; that x has
+    int bands, x_bands, w_bands;   // 128-row bands of x scales one tile may touch; that x and W have
     int stages, split_log2;     // ring depth; blocks of a cluster
     int own_red;                // the partial sums' place is behind the ring
     int32_t *status;
 };
 
-// A slot: W (16 KB a box: a scale tile of MXFP8's k, two of MXFP4's), x, then the scales of W and of
-// x's bands (KT tiles each)
+// A slot: W (16 KB a box: a scale tile of MXFP8's k, two of MXFP4's) of each 128 features, x, then the scales of W's
+// and of x's bands (KT tiles each)
 template <int KIND>
 __host__ __device__ constexpr int mx_boxes(int kt) { return KIND == MX_A8 ? kt : kt / 2; }
 template <int KIND>
-__host__ __device__ constexpr uint32_t few_x_at(int kt) { return 16384u * mx_boxes<KIND>(kt); }
+__host__ __device__ constexpr uint32_t few_x_at(int kt, int mt) { return 16384u * mt * mx_boxes<KIND>(kt); }
 template <int KIND>
-__host__ __device__ constexpr uint32_t few_sf_at(int kt, int bn) { return (16384u + 128u * bn) * mx_boxes<KIND>(kt); }
+__host__ __device__ constexpr uint32_t few_sf_at(int kt, int mt, int bn) { return (16384u * mt + 128u * bn) * mx_boxes<KIND>(kt); }
 template <int KIND>
-__host__ __device__ constexpr uint32_t few_slot_bytes(int kt, int bn, int bands) {
-    return (few_sf_at<KIND>(kt, bn) + (1 + bands) * kt * MX_TILE_BYTES + 1023u) & ~1023u;
+__host__ __device__ constexpr uint32_t few_slot_bytes(int kt, int mt, int bn, int bands) {
+    return (few_sf_at<KIND>(kt, mt, bn) + (mt + bands) * kt * MX_TILE_BYTES + 1023u) & ~1023u;
 }
-__host__ __device__ constexpr uint32_t few_sf_cols(int kt, int bn) { return kt * (bn > 128 ? 12 : 8); }
+__host__ __device__ constexpr uint32_t few_sf_cols(int kt, int mt, int bn) { return kt * (4 * mt + (bn > 128 ? 8 : 4)); }
 
-template <int KIND, int KT, typename Y>
+template <int KIND, int KT, int MT, typename Y>
 __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __grid_constant__ MxFewArgs a) {
     extern __shared__ __align__(1024) unsigned char mx_sm[];
     __shared__ uint32_t tmem_sm;
     __shared__ __align__(8) uint64_t bars[3 * FEW_STAGES + 4];
     constexpr int BOXES = mx_boxes<KIND>(KT);
     const int warp = __shfl_sync(FULL, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const uint32_t slot_bytes = few_slot_bytes<KIND>(KT, a.bn, a.bands), sf_at = few_sf_at<KIND>(KT, a.bn);
+    const uint32_t slot_bytes = few_slot_bytes<KIND>(KT, MT, a.bn, a.bands), sf_at = few_sf_at<KIND>(KT, MT, a.bn);
     const uint32_t base = (smem_u32(mx_sm) + 1023u) & ~1023u, red = base + (a.own_red ? (uint32_t)a.stages * slot_bytes : 0u);
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     auto full = [&](int s) { return bar(s); };
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
     const int c0 = (int)blockIdx.x >> a.split_log2, clusters = (int)gridDim.x >> a.split_log2;
     const int k_lo = a.n_ks * rank >> a.split_log2, k_hi = a.n_ks * (rank + 1) >> a.split_log2;
     const uint32_t acc_cols = ((uint32_t)a.bn + 31u) & ~31u, xc = a.bn > 128 ? 8u : 4u;
-    const uint32_t sf_cols = few_sf_cols(KT, a.bn), tmem_cols = pow2_cols(2 * acc_cols + (uint32_t)a.stages * sf_cols);
+    const uint32_t sf_cols = few_sf_cols(KT, MT, a.bn), tmem_cols = pow2_cols(2 * acc_cols + (uint32_t)a.stages * sf_cols);
     bool failed = false;
 
     // a warp's place: tile t (m0, n0: its first feature and row)
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
     auto place = [&](int tile) {
         t = tile;
         const int mi = a.nt == 1 ? t : t / a.nt;
-        m0 = mi * 128, n0 = (t - mi * a.nt) * a.bn;
+        m0 = mi * 128 * MT, n0 = (t - mi * a.nt) * a.bn;
     };
     auto next_tile = [&]() { place(t + clusters); };
     place(c0);
@@ -249,9 +250,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
 
     if (warp == 0) {
         for (int i = lane; i < 3 * FEW_STAGES + 4; i += 32) {
-            // full: both copying warps and the four scale warps; acc_empty: eight warps
-            const bool six = i < FEW_STAGES, eight = i >= 3 * FEW_STAGES + 2;
-            mbar_init(bar(i), six ? 6 : eight ? 8 : 1);
+            // full: both copying warps and the four scale warps; sf_full: both; acc_empty: eight warps
+            const bool six = i < FEW_STAGES, two = i >= 2 * FEW_STAGES && i < 3 * FEW_STAGES, eight = i >= 3 * FEW_STAGES + 2;
+            mbar_init(bar(i), six ? 6 : two ? 2 : eight ? 8 : 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         if (lane == 0) prefetch_tmap(&a.tmW);
@@ -279,40 +280,49 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
     pdl_next();
     if (warp < 1 || warp > 5) pdl_wait();   // the copying and the storing warps
 
-    if (warp == 0) {
-        for (; t < a.tiles && !failed; next_tile())
+    const int64_t band = (int64_t)a.n_kt * MX_TILE_BYTES;   // scale bytes of 128 rows
+    if (warp == 0) {   // W and its scales
+        for (; t < a.tiles && !failed; next_tile()) {
+            const uint8_t *sw = a.sw + m0 / 128 * band;
+            // features past the last band: any scales will do
+            const int64_t sw1 = MT == 2 && m0 / 128 + 1 < a.w_bands ? band : 0;
             for (int k = k_lo; k < k_hi; ++k, ring.next()) {
-                const uint32_t b = full(ring.slot), slot = base + (uint32_t)ring.slot * slot_bytes;
+                const uint32_t b = full(ring.slot), sb = sf_full(ring.slot), slot = base + (uint32_t)ring.slot * slot_bytes;
                 if (ring.reused() && !uniform_wait(empty(ring.slot), ring.parity ^ 1u, a.status, failed)) break;
                 if (elect_one()) {
+                    const uint32_t n = (uint32_t)min(KT, a.n_kt - KT * k) * MX_TILE_BYTES;
+                    const uint8_t *p = sw + (int64_t)k * KT * MX_TILE_BYTES;
                     // packed4 boxes count packed bytes; a box past k's end arrives as zeros that no MMA reads
-                    mbar_expect_tx(b, (KIND == MX_A8 ? 8192u : 16384u) * BOXES);
+                    mbar_expect_tx(b, (KIND == MX_A8 ? 8192u : 16384u) * (BOXES * MT));
 #pragma unroll
-                    for (int x = 0; x < BOXES; ++x) tma_2d(slot + 16384u * x, &a.tmW, (BOXES * k + x) * 128, m0, b);
+                    for (int u = 0; u < MT; ++u)
+#pragma unroll
+                        for (int x = 0; x < BOXES; ++x)
+                            tma_2d(slot + 16384u * (BOXES * u + x), &a.tmW, (BOXES * k + x) * 128, m0 + 128 * u, b);
+                    mbar_expect_tx(sb, MT * n);
+                    bulk_g2s(slot + sf_at, p, n, sb);
+                    if (MT == 2) bulk_g2s(slot + sf_at + KT * MX_TILE_BYTES, p + sw1, n, sb);
                 }
             }
-        if (failed) drain_ring(ring, full(0));
-    } else if (warp == 10) {
+        }
+        if (failed) drain_ring(ring, sf_full(0)), drain_ring(ring, full(0));
+    } else if (warp == 10) {   // x and its scales
         const uint32_t x_bytes = (uint32_t)a.bn * 128u;
         for (; t < a.tiles && !failed; next_tile()) {
             const int xb = n0 / 128, nb = min(a.bands, a.x_bands - xb);
-            const uint8_t *sw = a.sw + (int64_t)(m0 / 128) * a.n_kt * MX_TILE_BYTES;
-            const uint8_t *sx = a.sx + (int64_t)xb * a.n_kt * MX_TILE_BYTES;
+            const uint8_t *sx = a.sx + xb * band;
             for (int k = k_lo; k < k_hi; ++k, ring.next()) {
-                const uint32_t b = full(ring.slot), slot = base + (uint32_t)ring.slot * slot_bytes;
+                const uint32_t b = full(ring.slot), sb = sf_full(ring.slot), slot = base + (uint32_t)ring.slot * slot_bytes;
                 if (ring.reused() && !uniform_wait(empty(ring.slot), ring.parity ^ 1u, a.status, failed)) break;
                 if (elect_one()) {
-                    const uint32_t sb = sf_full(ring.slot), n = (uint32_t)min(KT, a.n_kt - KT * k) * MX_TILE_BYTES;
-                    const int64_t off = (int64_t)k * KT * MX_TILE_BYTES;
-                    mbar_expect_tx(sb, (uint32_t)(1 + nb) * n);
-                    bulk_g2s(slot + sf_at, sw + off, n, sb);
-                    for (int i = 0; i < nb; ++i)
-                        bulk_g2s(slot + sf_at + (uint32_t)((1 + i) * KT) * MX_TILE_BYTES,
-                                 sx + off + (int64_t)i * a.n_kt * MX_TILE_BYTES, n, sb);
+                    const uint32_t n = (uint32_t)min(KT, a.n_kt - KT * k) * MX_TILE_BYTES;
+                    const uint8_t *p = sx + (int64_t)k * KT * MX_TILE_BYTES;
                     mbar_expect_tx(b, x_bytes * BOXES);
 #pragma unroll
                     for (int x = 0; x < BOXES; ++x)
-                        tma_2d(slot + few_x_at<KIND>(KT) + x_bytes * x, &a.tmX, (BOXES * k + x) * 128, n0, b);
+                        tma_2d(slot + few_x_at<KIND>(KT, MT) + x_bytes * x, &a.tmX, (BOXES * k + x) * 128, n0, b);
+                    mbar_expect_tx(sb, (uint32_t)nb * n);
+                    for (int i = 0; i < nb; ++i) bulk_g2s(slot + sf_at + (uint32_t)((MT + i) * KT) * MX_TILE_BYTES, p + i * band, n, sb);
                 }
             }
         }
@@ -322,8 +332,14 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
         const uint32_t x_bytes = (uint32_t)a.bn * 128u;
         int n = 0;
         for (; t < a.tiles && !failed; next_tile(), ++n) {
-            const int b = n & 1;
-            if (n >= 2 && !uniform_wait(acc_empty(b), (unsigned)(n / 2 - 1) & 1u, a.status, failed)) break;
+            const int b = MT == 2 ? 0 : n & 1;
+            if (MT == 2) {
+                if (n >= 1 && !(uniform_wait(acc_empty(0), (unsigned)(n - 1) & 1u, a.status, failed) &&
+                                uniform_wait(acc_empty(1), (unsigned)(n - 1) & 1u, a.status, failed)))
+                    break;
+            } else if (n >= 2 && !uniform_wait(acc_empty(b), (unsigned)(n / 2 - 1) & 1u, a.status, failed)) {
+                break;
+            }
             const uint32_t d = tmem + (uint32_t)b * acc_cols;
             for (int k = k_lo; k < k_hi; ++k, ring.next()) {
                 const uint32_t slot = base + (uint32_t)ring.slot * slot_bytes, ta = sf + sf_cols * (uint32_t)ring.slot;
@@ -332,14 +348,20 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int x = 0; x < BOXES; ++x)
-                        if (KIND == MX_A4 || x < tiles)
-                            mx_stage_mmas<KIND, false>(d, slot + 16384u * x, slot + few_x_at<KIND>(KT) + x_bytes * x, ta + 4 * x,
-                                                       ta + 4 * KT + xc * x, (int)xc, tiles, idesc, k == k_lo && x == 0);
+                    for (int u = 0; u < MT; ++u)
+#pragma unroll
+                        for (int x = 0; x < BOXES; ++x)
+                            if (KIND == MX_A4 || x < tiles)
+                                mx_stage_mmas<KIND, false>(d + acc_cols * u, slot + 16384u * (BOXES * u + x),
+                                                           slot + few_x_at<KIND>(KT, MT) + x_bytes * x, ta + 4 * (KT * u + x),
+                                                           ta + 4 * KT * MT + xc * x, (int)xc, tiles, idesc, k == k_lo && x == 0);
                     tc_commit(empty(ring.slot));
                 }
             }
-            if (elect_one()) tc_commit(acc_full(b));
+            if (elect_one()) {
+                tc_commit(acc_full(b));
+                if (MT == 2) tc_commit(acc_full(1));
+            }
         }
     } else if (warp < 6) {
         const uint32_t dst = sf + ((uint32_t)(32 * (warp & 3)) << 16);
@@ -351,7 +373,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
 #pragma unroll
             for (int g = 0; g < 8; ++g) {
                 const int row = n0 + 32 * g + lane, band = min(row / 128 - xb, last);
-                at[g] = sf_at + (uint32_t)((1 + band) * KT) * MX_TILE_BYTES + (uint32_t)(row % 32 * 16 + row / 32 % 4 * 4);
+                at[g] = sf_at + (uint32_t)((MT + band) * KT) * MX_TILE_BYTES + (uint32_t)(row % 32 * 16 + row / 32 % 4 * 4);
             }
             for (int k = k_lo; k < k_hi; ++k, ring.next()) {
                 if (!uniform_wait(sf_full(ring.slot), ring.parity, a.status, failed)) break;
@@ -359,11 +381,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
 #pragma unroll
                 for (int i = 0; i < KT; ++i) {   // a tile past k's end is old data that no MMA reads
                     const uint32_t src = slot + i * MX_TILE_BYTES;
-                    tmem_st4(to + 4 * i, lds128(src + sf_at + 16 * lane));
-                    tmem_st4(to + 4 * KT + xc * i, make_uint4(lds32(src + at[0]), lds32(src + at[1]), lds32(src + at[2]),
+#pragma unroll
+                    for (int u = 0; u < MT; ++u)
+                        tmem_st4(to + 4 * (KT * u + i), lds128(src + sf_at + u * (KT * MX_TILE_BYTES) + 16 * lane));
+                    tmem_st4(to + 4 * KT * MT + xc * i, make_uint4(lds32(src + at[0]), lds32(src + at[1]), lds32(src + at[2]),
                                                               lds32(src + at[3])));
                     if (xc == 8)
-                        tmem_st4(to + 4 * KT + xc * i + 4, make_uint4(lds32(src + at[4]), lds32(src + at[5]),
+                        tmem_st4(to + 4 * KT * MT + xc * i + 4, make_uint4(lds32(src + at[4]), lds32(src + at[5]),
                                                                       lds32(src + at[6]), lds32(src + at[7])));
                 }
                 tmem_st_wait();
@@ -377,12 +401,12 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
         const int half = 16 * (warp > 10);           // its first row; then every other 16
         const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16);
         if (S > 1) asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");   // every block's barriers are set
-        int n = 0;
-        for (; t < a.tiles && !failed; next_tile(), ++n) {
-            const int b = n & 1, rows = min(a.bn, a.T - n0);
+        // n counts accumulators: tile by tile, or the two of a tile
+        for (int n = 0; t < a.tiles && !failed; ++n) {
+            const int b = n & 1, rows = min(a.bn, a.T - n0), m = m0 + (MT == 2 ? 128 * b : 0) + f;
             const uint32_t src_acc = acc + (uint32_t)b * acc_cols;
-            const bool there = m0 + f < a.d_out;
-            Y *y = static_cast<Y *>(a.y) + (int64_t)n0 * a.ld_y + m0 + f;
+            const bool there = m < a.d_out;
+            Y *y = static_cast<Y *>(a.y) + (int64_t)n0 * a.ld_y + m;
             if (!warp_wait(acc_full(b), (unsigned)(n / 2) & 1u, a.status, failed) && S == 1) break;
             tc_fence_after();
             if (S == 1) {
@@ -432,6 +456,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(acc_empty(b));
+            if (MT == 1 || b == 1) next_tile();
         }
     }
     // ---------------------------------------------------------------- teardown
@@ -449,23 +474,25 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
     }
 }
 
-// Blocks along k and clusters of them, by the time they would take: a scale tile of k costs a block 180 (MXFP8) or
-// 150 ns, more from 64 rows on, when the operands' way into shared memory bounds it; an exchange of partial sums 0.95 us for each
-// doubling of S and 12 ns a row; all 3 us and 8 ns a row besides.  Measured (us, S = 1, 2, 4): 1 x 4096 x 4096 7.8, 6.0,
-// 5.6; 64 x 4096 x 4096 9.0, 7.9, 7.3; 64 x 1024 x 4096 4.7, 5.4, 5.4; 128 x 4096 x 4096 11.9, 10.1, 9.4;
-// 257 x 14336 x 4096 38.7, 24.6.
+// Blocks along k and clusters of them, by the time they would take: a scale tile of k costs a block `one`, bound by
+// its latency or its operands' way into shared memory, or `more` where every SM streams; an exchange of partial sums
+// 0.95 us for each doubling of S and 12 ns a row; all 3 us and 8 ns a row and accumulator besides.  Measured (us, S = 1, 2,
+// 4): 1 x 4096 x 4096 7.8, 6.0, 5.6; 64 x 4096 x 4096 9.0, 7.9, 7.3; 64 x 1024 x 4096 4.7, 5.4, 5.4;
+// 257 x 14336 x 4096 38.7, 24.6.  MT = 1 / 2, MXFP8: 1 x 4096 x 28672 16.0 / 16.5, 64 rows 19.1 / 19.2, 128 rows 25.1 / 23.2,
+// 256 x 4096 x 14336 25.4 / 20.5, 64 x 4096 x 50000 28.0 / 34.9; MXFP4: 15.4 / 14.1, 16.5 / 16.2, 18.1 / 17.9, 15.8 / 14.0,
+// 24.5 / 27.7.
 struct FewPlan {
     int split_log2 = 0, clusters = 1;
     int64_t ns = 0;
 };
-template <int KIND, int KT, typename Y>
+template <int KIND, int KT, int MT, typename Y>
 int few_plan(const MxFewArgs &a, int dev, FewPlan *out) {
     // clusters resident at once: a property of the device and the kernel, asked for once
     static std::mutex mu;
     static int fit[64][4] = {};
     std::lock_guard<std::mutex> lock(mu);
     int *f = fit[dev & 63];
-    auto kernel = mx_linear_few_kernel<KIND, KT, Y>;
+    auto kernel = mx_linear_few_kernel<KIND, KT, MT, Y>;
     if (!f[0]) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)MX_MAX_SMEM);
         for (int i = 3; i >= 0 && e == cudaSuccess; --i) {   // f[0] last: it marks the table as filled
@@ -485,35 +512,58 @@ int few_plan(const MxFewArgs &a, int dev, FewPlan *out) {
         }
         if (e != cudaSuccess) return cuda_rc(e);
     }
-    const int64_t kt_ns = KIND == MX_A8 ? std::max(180, 110 + 12 * a.bn / 10) : std::max(150, 90 + 66 * a.bn / 100);
+    const bool a8 = KIND == MX_A8;
+    const int one = a8 ? std::max(180, 110 + 12 * a.bn / 10) : std::max(150, 90 + 66 * a.bn / 100);
+    const int more = MT == 2 ? (a8 ? 410 + a.bn : 345 + a.bn / 2) : (a8 ? 195 + a.bn * 7 / 8 : 190 + a.bn / 4);
     int64_t best = -1;
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < (MT == 2 ? 1 : 4); ++i) {
         const int s = 1 << i, n = std::min(a.tiles, f[i]);
         if (s > a.n_ks || (i && n < a.tiles)) break;
-        const int64_t cost = (int64_t)((a.tiles + n - 1) / n) * ((a.n_ks + s - 1) / s) * KT * kt_ns + (i ? 950 * i + 12 * a.bn : 0);
+        const int64_t rounds = (a.tiles + n - 1) / n, kt_ns = MT == 2 || rounds > 1 ? more : one;
+        const int64_t cost = rounds * ((a.n_ks + s - 1) / s) * KT * kt_ns + (i ? 950 * i + 12 * a.bn : 0);
         if (best < 0 || cost < best) best = cost, out->split_log2 = i, out->clusters = n;
     }
-    out->ns = best + 3000 + 8 * a.bn;
+    out->ns = best + 3000 + 8 * a.bn * MT;
     return LORA_OK;
 }
 
-// The call on this kernel unless it would take longer than limit_ns (*took = 0 then).
-template <int KIND, int KT, typename Y>
-int launch_few_kt(MxFewArgs &a, int dev, int64_t limit_ns, int *took, cudaStream_t st) {
+template <int KIND, int KT, int MT>
+void few_tiles(MxFewArgs &a) {
     a.n_ks = (a.n_kt + KT - 1) / KT;
-    FewPlan plan;
-    const int rc = few_plan<KIND, KT, Y>(a, dev, &plan);
-    *took = rc == LORA_OK && plan.ns <= limit_ns;
-    if (!*took) return rc;
+    a.tiles = (a.w_bands + MT - 1) / MT * a.nt;
+}
+template <int KIND, int KT, int MT, typename Y>
+int launch_few_as(MxFewArgs &a, const FewPlan &plan, cudaStream_t st) {
+    few_tiles<KIND, KT, MT>(a);
     a.split_log2 = plan.split_log2;
     const int acc_cols = (a.bn + 31) / 32 * 32;
     a.own_red = a.bn <= 32;
     const size_t room = MX_MAX_SMEM - 1024 - (plan.split_log2 && a.own_red ? (size_t)(2 * a.bn + 16) * 512 : 0);
-    a.stages = (int)std::min<size_t>(FEW_STAGES, room / few_slot_bytes<KIND>(KT, a.bn, a.bands));
-    a.stages = std::min(a.stages, (512 - 2 * acc_cols) / (int)few_sf_cols(KT, a.bn));
+    a.stages = (int)std::min<size_t>(FEW_STAGES, room / few_slot_bytes<KIND>(KT, MT, a.bn, a.bands));
+    a.stages = std::min(a.stages, (512 - 2 * acc_cols) / (int)few_sf_cols(KT, MT, a.bn));
     // all of the shared memory: one block an SM (two might wait for each other's tensor memory)
-    return launch_after(mx_linear_few_kernel<KIND, KT, Y>, dim3((unsigned)(plan.clusters << plan.split_log2)), FEW_THREADS, MX_MAX_SMEM,
-                        1u << plan.split_log2, st, a);
+    return launch_after(mx_linear_few_kernel<KIND, KT, MT, Y>, dim3((unsigned)(plan.clusters << plan.split_log2)), FEW_THREADS,
+                        MX_MAX_SMEM, 1u << plan.split_log2, st, a);
+}
+
+// The call on this kernel unless it would take longer than limit_ns (*took = 0 then).  KT1, KT2: scale tiles a
+// slot with MT = 1 and 2.
+template <int KIND, int KT1, int KT2, typename Y>
+int launch_few_kt(MxFewArgs &a, int dev, int64_t limit_ns, int *took, cudaStream_t st) {
+    FewPlan one, two;
+    few_tiles<KIND, KT1, 1>(a);
+    int rc = few_plan<KIND, KT1, 1, Y>(a, dev, &one);
+    if (rc != LORA_OK) return rc;
+    // two accumulators a tile only where they save blocks a second tile, and their slots are four or more
+    two.ns = one.ns + 1;
+    if (a.tiles > one.clusters && a.bn <= 128) {
+        few_tiles<KIND, KT2, 2>(a);
+        rc = few_plan<KIND, KT2, 2, Y>(a, dev, &two);
+        if (rc != LORA_OK) return rc;
+    }
+    *took = std::min(one.ns, two.ns) <= limit_ns;
+    if (!*took) return LORA_OK;
+    return two.ns < one.ns ? launch_few_as<KIND, KT2, 2, Y>(a, two, st) : launch_few_as<KIND, KT1, 1, Y>(a, one, st);
 }
 
 template <int KIND, typename Y>
@@ -523,17 +573,17 @@ int launch_few(const MxLinArgs &l, const lora_mx *x, const lora_mx *w, int dev, 
     a.nt = (l.T + FEW_ROWS - 1) / FEW_ROWS;
     a.bn = ((l.T + a.nt - 1) / a.nt + 15) / 16 * 16;
     a.nt = (l.T + a.bn - 1) / a.bn;
-    a.tiles = (l.d_out + 127) / 128 * a.nt;
     int rc = tensor_map_mx(&a.tmW, w->q, wb, (uint64_t)l.d_out, wb, 128, KIND == MX_A8);
     if (rc == LORA_OK) rc = tensor_map_mx(&a.tmX, x->q, xb, (uint64_t)l.T, xb, (uint32_t)a.bn, false);
     if (rc != LORA_OK) return rc;
     a.sw = l.sw, a.sx = l.sx, a.y = l.y, a.ld_y = l.ld_y, a.T = l.T, a.d_out = l.d_out, a.n_kt = l.n_kt;
-    a.x_bands = (l.T + 127) / 128;
+    a.x_bands = (l.T + 127) / 128, a.w_bands = (l.d_out + 127) / 128;
     a.bands = std::min(a.x_bands, a.nt == 1 ? (a.bn + 127) / 128 : (a.bn + 126) / 128 + 1);
     a.status = l.status;
     // MXFP8: two scale tiles a slot while four slots fit (up to 64 rows), else one
-    if (KIND == MX_A4 || a.bn <= 64) return launch_few_kt<KIND, 2, Y>(a, dev, limit_ns, took, st);
-    return launch_few_kt<KIND, KIND == MX_A8 ? 1 : 2, Y>(a, dev, limit_ns, took, st);
+    if (KIND == MX_A4) return launch_few_kt<MX_A4, 2, 2, Y>(a, dev, limit_ns, took, st);
+    if (a.bn <= 64) return launch_few_kt<MX_A8, 2, 1, Y>(a, dev, limit_ns, took, st);
+    return launch_few_kt<MX_A8, 1, 1, Y>(a, dev, limit_ns, took, st);
 }
 
 // ---------------------------------------------------------------- many rows
