@@ -546,44 +546,70 @@ int launch_few_as(MxFewArgs &a, const FewPlan &plan, cudaStream_t st) {
                         MX_MAX_SMEM, 1u << plan.split_log2, st, a);
 }
 
-// The call on this kernel unless it would take longer than limit_ns (*took = 0 then).  KT1, KT2: scale tiles a
-// slot with MT = 1 and 2.
-template <int KIND, int KT1, int KT2, typename Y>
-int launch_few_kt(MxFewArgs &a, int dev, int64_t limit_ns, int *took, cudaStream_t st) {
-    FewPlan one, two;
+// A shape of the tiles and what it would take.
+struct FewShape {
+    int bn = 0, nt = 0, mt = 0;
+    FewPlan plan;
+};
+// Scale tiles of a slot: two while three slots fit, else one (MXFP8: KT = 1 from 145 rows on; 257 x 14336 x 4096
+// 24.8 us with one, 22.5 with two).
+template <int KIND>
+constexpr int few_kt(bool wide, int mt) { return KIND == MX_A4 || (mt == 1 && !wide) ? 2 : 1; }
+inline bool few_wide(int bn) { return bn > 144; }
+
+template <int KIND, bool WIDE, typename Y>
+int few_consider(MxFewArgs &a, int dev, FewShape *best) {
+    constexpr int KT1 = few_kt<KIND>(WIDE, 1), KT2 = few_kt<KIND>(WIDE, 2);
+    auto keep = [&](const FewPlan &p, int mt) {
+        if (!best->mt || p.ns < best->plan.ns) best->bn = a.bn, best->nt = a.nt, best->mt = mt, best->plan = p;
+    };
+    FewPlan p;
     few_tiles<KIND, KT1, 1>(a);
-    int rc = few_plan<KIND, KT1, 1, Y>(a, dev, &one);
+    int rc = few_plan<KIND, KT1, 1, Y>(a, dev, &p);
     if (rc != LORA_OK) return rc;
-    // two accumulators a tile only where they save blocks a second tile, and their slots are four or more
-    two.ns = one.ns + 1;
-    if (a.tiles > one.clusters && a.bn <= 128) {
+    keep(p, 1);
+    if (a.tiles > p.clusters && a.bn <= 128) {   // blocks with a second tile, and room for four slots
         few_tiles<KIND, KT2, 2>(a);
-        rc = few_plan<KIND, KT2, 2, Y>(a, dev, &two);
+        rc = few_plan<KIND, KT2, 2, Y>(a, dev, &p);
         if (rc != LORA_OK) return rc;
+        keep(p, 2);
     }
-    *took = std::min(one.ns, two.ns) <= limit_ns;
-    if (!*took) return LORA_OK;
-    return two.ns < one.ns ? launch_few_as<KIND, KT2, 2, Y>(a, two, st) : launch_few_as<KIND, KT1, 1, Y>(a, one, st);
+    return LORA_OK;
+}
+template <int KIND, bool WIDE, typename Y>
+int few_run(MxFewArgs &a, const FewShape &s, cudaStream_t st) {
+    constexpr int KT1 = few_kt<KIND>(WIDE, 1), KT2 = few_kt<KIND>(WIDE, 2);
+    return s.mt == 2 ? launch_few_as<KIND, KT2, 2, Y>(a, s.plan, st) : launch_few_as<KIND, KT1, 1, Y>(a, s.plan, st);
 }
 
+// The call on this kernel unless it would take longer than limit_ns (*took = 0 then).
 template <int KIND, typename Y>
 int launch_few(const MxLinArgs &l, const lora_mx *x, const lora_mx *w, int dev, int64_t limit_ns, int *took, cudaStream_t st) {
     MxFewArgs a{};
+    a.sw = l.sw, a.sx = l.sx, a.y = l.y, a.ld_y = l.ld_y, a.T = l.T, a.d_out = l.d_out, a.n_kt = l.n_kt;
+    a.x_bands = (l.T + 127) / 128, a.w_bands = (l.d_out + 127) / 128;
+    a.status = l.status;
+    auto shape = [&](int nt) {   // row tiles of equal height, a multiple of 16
+        a.bn = ((l.T + nt - 1) / nt + 15) / 16 * 16;
+        a.nt = (l.T + a.bn - 1) / a.bn;
+        a.bands = std::min(a.x_bands, a.nt == 1 ? (a.bn + 127) / 128 : (a.bn + 126) / 128 + 1);
+    };
+    FewShape best;
+    const int least = (l.T + FEW_ROWS - 1) / FEW_ROWS;
+    for (int nt = least; nt <= least + 2; ++nt) {   // the fewest row tiles, or a little more that fill the SMs better
+        shape(nt);
+        const int rc = few_wide(a.bn) ? few_consider<KIND, true, Y>(a, dev, &best) : few_consider<KIND, false, Y>(a, dev, &best);
+        if (rc != LORA_OK) return rc;
+        if (a.bn <= 64) break;
+    }
+    *took = best.plan.ns <= limit_ns;
+    if (!*took) return LORA_OK;
+    shape(best.nt);
     const uint64_t xb = (uint64_t)mx_row_bytes(x->format, x->cols), wb = (uint64_t)mx_row_bytes(w->format, w->cols);
-    a.nt = (l.T + FEW_ROWS - 1) / FEW_ROWS;
-    a.bn = ((l.T + a.nt - 1) / a.nt + 15) / 16 * 16;
-    a.nt = (l.T + a.bn - 1) / a.bn;
     int rc = tensor_map_mx(&a.tmW, w->q, wb, (uint64_t)l.d_out, wb, 128, KIND == MX_A8);
     if (rc == LORA_OK) rc = tensor_map_mx(&a.tmX, x->q, xb, (uint64_t)l.T, xb, (uint32_t)a.bn, false);
     if (rc != LORA_OK) return rc;
-    a.sw = l.sw, a.sx = l.sx, a.y = l.y, a.ld_y = l.ld_y, a.T = l.T, a.d_out = l.d_out, a.n_kt = l.n_kt;
-    a.x_bands = (l.T + 127) / 128, a.w_bands = (l.d_out + 127) / 128;
-    a.bands = std::min(a.x_bands, a.nt == 1 ? (a.bn + 127) / 128 : (a.bn + 126) / 128 + 1);
-    a.status = l.status;
-    // MXFP8: two scale tiles a slot while four slots fit (up to 64 rows), else one
-    if (KIND == MX_A4) return launch_few_kt<MX_A4, 2, 2, Y>(a, dev, limit_ns, took, st);
-    if (a.bn <= 64) return launch_few_kt<MX_A8, 2, 1, Y>(a, dev, limit_ns, took, st);
-    return launch_few_kt<MX_A8, 1, 1, Y>(a, dev, limit_ns, took, st);
+    return few_wide(a.bn) ? few_run<KIND, true, Y>(a, best, st) : few_run<KIND, false, Y>(a, best, st);
 }
 
 // ---------------------------------------------------------------- many rows
