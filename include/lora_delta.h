@@ -452,7 +452,8 @@ LORA_API int lora_merge_adapter(void *W, int64_t ld_w, int32_t d_out, int32_t d_
  *           block b is byte ((r / 128) * ceil(cols / 128) + b / 4) * 512 +
  *           (r % 32) * 16 + (r / 32 % 4) * 4 + b % 4.  Blocks of the padding
  *           columns have e = 0; bytes of rows past the last one are not used.
- * Both are aligned to LORA_MX_ALIGN bytes (LORA_ERR_ALIGN otherwise).  Where a call takes a
+ * Both are aligned to LORA_MX_ALIGN bytes (LORA_ERR_ALIGN otherwise).  The calls below take the
+ * device that is current, need no workspace and may be captured from the first call on.  Where a call takes a
  * row count T beside a matrix, it uses its rows 0..T-1 and leaves the others as they were.
  */
 typedef enum { LORA_MXFP8 = 0, LORA_MXFP4 = 1 } lora_mx_format;
@@ -499,7 +500,7 @@ LORA_API int lora_mx_dequantize(void *out, int64_t ld_out, const lora_mx *q, int
  * residual and residual_out are both NULL (r = x) or both given, and may be the
  * same array.  h (the x of lora_add_linear) or q (the x of lora_mx_linear; q->cols = d) may
  * be NULL, not both; q is what lora_mx_quantize gives for h, whether h is stored or not.
- * h may be x itself; other outputs overlap nothing.  Sums in fp32.  weight: [d],
+ * h may be x itself; other outputs overlap nothing (h = residual_out: LORA_ERR_SHAPE).  Sums in fp32.  weight: [d],
  * eps >= 0.
  */
 LORA_API int lora_rms_norm(void *h, int64_t ld_h, const void *x, int64_t ld_x,
@@ -511,7 +512,7 @@ LORA_API int lora_rms_norm(void *h, int64_t ld_h, const void *x, int64_t ld_x,
  * Base product y = x W^T over T rows: y[i][o] = sum_j x[i][j] w[o][j] for i < T,
  * o < w->rows, from the stored values of x (LORA_MXFP8 or LORA_MXFP4) and w
  * (LORA_MXFP4; x->cols = w->cols), fp32 accumulation in a fixed order, one
- * rounding into y ([T][ld_y], dtype bf16 or fp32).  A NaN block of x or w makes
+ * rounding into y ([T][ld_y], dtype bf16 or fp32; overlaps neither operand).  A NaN block of x or w makes
  * the elements of y that it enters NaN.  status: device int32, receives LORA_DEV_TIMEOUT if
  * a bounded wait ran out (the call's results are then unreliable).
  */

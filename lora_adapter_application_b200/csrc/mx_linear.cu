@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
     if (S > 1) asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");   // this block's barriers are set
     const uint32_t sf = tmem + 2 * acc_cols;
     pdl_next();
-    if (warp < 1 || warp > 5) pdl_wait();   // the copying and the storing warps
+    pdl_wait();   // all warps: none of the bounded waits below runs while the kernel before this one does
 
     const int64_t band = (int64_t)a.n_kt * MX_TILE_BYTES;   // scale bytes of 128 rows
     if (warp == 0) {   // W and its scales
@@ -489,7 +489,7 @@ template <int KIND, int KT, int MT, typename Y>
 int few_plan(const MxFewArgs &a, int dev, FewPlan *out) {
     // clusters resident at once: a property of the device and the kernel, asked for once
     static std::mutex mu;
-    static int fit[64][4] = {};
+    static int fit[64][4] = {};   // 1 + clusters of 1, 2, 4, 8
     std::lock_guard<std::mutex> lock(mu);
     int *f = fit[dev & 63];
     auto kernel = mx_linear_few_kernel<KIND, KT, MT, Y>;
@@ -508,7 +508,7 @@ int few_plan(const MxFewArgs &a, int dev, FewPlan *out) {
             cfg.numAttrs = 1;
             int n = 0;
             e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-            if (e == cudaSuccess) f[i] = std::max(1, n);
+            if (e == cudaSuccess) f[i] = 1 + n;
         }
         if (e != cudaSuccess) return cuda_rc(e);
     }
@@ -517,7 +517,7 @@ int few_plan(const MxFewArgs &a, int dev, FewPlan *out) {
     const int more = MT == 2 ? (a8 ? 410 + a.bn : 345 + a.bn / 2) : (a8 ? 195 + a.bn * 7 / 8 : 190 + a.bn / 4);
     int64_t best = -1;
     for (int i = 0; i < (MT == 2 ? 1 : 4); ++i) {
-        const int s = 1 << i, n = std::min(a.tiles, f[i]);
+        const int s = 1 << i, n = std::min(a.tiles, i ? f[i] - 1 : std::max(1, f[i] - 1));
         if (s > a.n_ks || (i && n < a.tiles)) break;
         const int64_t rounds = (a.tiles + n - 1) / n, kt_ns = MT == 2 || rounds > 1 ? more : one;
         const int64_t cost = rounds * ((a.n_ks + s - 1) / s) * KT * kt_ns + (i ? 950 * i + 12 * a.bn : 0);
@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(BIG_THREADS, 1) mx_linear_big_kernel(const __g
     const uint32_t tmem = __shfl_sync(FULL, tmem_sm, 0), sf = tmem + 256;
     bool failed = false;
     pdl_next();
-    if (warp < 1 || warp > 5) pdl_wait();   // the copying and the storing warps
+    pdl_wait();   // all warps: none of the bounded waits below runs while the kernel before this one does
     auto place = [&](int t, int &mi, int &ni) {   // of tile t
         const int per = BIG_BAND * a.nt, band = t / per, left = t - band * per, high = min(BIG_BAND, a.mt - band * BIG_BAND);
         ni = left / high;

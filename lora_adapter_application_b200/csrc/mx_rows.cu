@@ -366,6 +366,7 @@ int lora_rms_norm(void *h, int64_t ld_h, const void *x, int64_t ld_x, const void
     if (T < 0 || T > LORA_MAX_ROWS || d < 1 || d > LORA_MX_MAX || !(eps >= 0.f)) return LORA_ERR_SHAPE;
     if (!h && !q) return LORA_ERR_NULL;
     if (!residual != !residual_out) return LORA_ERR_NULL;
+    if (h && h == residual_out) return LORA_ERR_SHAPE;
     if (ld_x < d || (h && ld_h < d) || (residual && (ld_r < d || ld_ro < d))) return LORA_ERR_SHAPE;
     if (q) {
         const int rc = check_mx(q, T);

@@ -134,7 +134,7 @@ def test_norm_refusals(lib):
                        (dict(h=None), NULL), (dict(x=None), NULL), (dict(w=None), NULL), (dict(r=P, ld_r=256), NULL),
                        (dict(ro=P, ld_ro=256), NULL), (dict(ld_x=255), SHAPE), (dict(ld_h=255), SHAPE),
                        (dict(r=P, ro=P, ld_r=255, ld_ro=256), SHAPE), (dict(r=P, ro=P, ld_r=256, ld_ro=255), SHAPE),
-                       (dict(q=_m(cols=128)), SHAPE)]:
+                       (dict(q=_m(cols=128)), SHAPE), (dict(r=2 * P, ro=P, ld_r=256, ld_ro=256), SHAPE)]:
         assert call(**over) == want, over
 
 

@@ -189,3 +189,72 @@ def test_product_beside_the_adapters_kernels(cuda_lib):
     torch.cuda.synchronize()
     assert int(s.status.item()) == 0 and torch.equal(s.y, want)
     assert all(torch.equal(y, base) for y in ys)
+
+
+def test_first_calls_inside_a_capture(cuda_lib):
+    """A fresh process whose first calls of every operator are captured (loading and planning happen there)."""
+    code = """
+import torch, lora_adapter_application_b200 as lora
+T, d, n = 3, 1024, 512
+x = torch.randn(T, d, device="cuda").bfloat16()
+wf = (torch.randn(n, d, device="cuda") / 32).bfloat16()
+wt = torch.ones(d, device="cuda").bfloat16()
+xq, w, big = lora.MxTensor(T, d, 0), lora.MxTensor(n, d, 1), lora.MxTensor(2000, d, 1)
+h, r, y = torch.empty_like(x), torch.zeros_like(x), torch.empty(T, n, device="cuda")
+many, yb = torch.randn(2000, d, device="cuda"), torch.empty(2000, n, device="cuda")
+st = torch.zeros(1, dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+def step():
+    lora.lora_mx_quantize(w, wf)
+    lora.lora_rms_norm(h, x, wt, 1e-5, residual=r, residual_out=torch.empty_like(x), q=xq)
+    lora.lora_mx_linear(y, xq, w, st)
+    lora.lora_mx_quantize(big, many)
+    lora.lora_mx_linear(yb, big, w, st)
+with torch.cuda.graph(g):
+    step()
+g.replay()
+torch.cuda.synchronize()
+a, b = y.clone(), yb.clone()
+y.zero_(), yb.zero_()
+step()
+torch.cuda.synchronize()
+assert torch.equal(a, y) and torch.equal(b, yb) and int(st) == 0 and float(y.abs().max()) > 0
+"""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stderr[-2000:]
+
+
+def test_an_events_wait_between_two_calls(cuda_lib):
+    """A product whose rows another stream wrote, behind a product on its own stream: the event is waited for."""
+    w, st = lora.MxTensor(2048, 2048, lora.LORA_MXFP4), torch.zeros(1, dtype=torch.int32, device="cuda")
+    lora.lora_mx_quantize(w, torch.randn(2048, 2048, device="cuda"))
+    x0, x1 = lora.MxTensor(16, 2048, 0), lora.MxTensor(16, 2048, 0)
+    rows = [torch.randn(16, 2048, device="cuda") for _ in range(20)]
+    lora.lora_mx_quantize(x0, rows[0])
+    want = []
+    for r in rows:
+        lora.lora_mx_quantize(x1, r)
+        want.append(torch.empty(16, 2048, device="cuda"))
+        lora.lora_mx_linear(want[-1], x1, w, st)
+    big = torch.randn(8192, 8192, device="cuda")
+    torch.cuda.synchronize()
+    other, scratch = torch.cuda.Stream(), torch.empty(16, 2048, device="cuda")
+    for r, y in zip(rows, want):
+        got = torch.empty_like(y)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(other):
+            big.mul_(1.0)                              # some time before the rows are there
+            lora.lora_mx_quantize(x1, r)
+            e = torch.cuda.Event()
+            e.record()
+        lora.lora_mx_linear(scratch, x0, w, st)
+        torch.cuda.current_stream().wait_event(e)
+        lora.lora_mx_linear(got, x1, w, st)
+        torch.cuda.synchronize()
+        assert torch.equal(got, y)
+    assert int(st.item()) == 0
