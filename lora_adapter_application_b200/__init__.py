@@ -582,6 +582,22 @@ def _matrix(t, what, rows=-1, cols=-1):
     return n, d, ld
 
 
+def _like(t, what, n, d, index, dtype):
+    """(address, row stride) of an operand that must be [n, d] of dtype on CUDA device index."""
+    if not isinstance(t, torch.Tensor) or t.shape != (n, d) or t.dtype is not dtype:
+        raise LoraError(f"{what} must be [{n}, {d}] of {dtype} (x, h, residual and weight share one dtype)")
+    ld, one = t.stride()
+    if one != 1 and d > 1:
+        raise LoraError(f"{what} must be 2-D with unit column stride")
+    if n <= 1:
+        ld = d
+    elif ld < d:
+        raise LoraError(f"{what}'s rows overlap")
+    if t.get_device() != index:
+        raise LoraError(f"{what} must be on cuda:{index}")
+    return t.data_ptr(), ld
+
+
 _CODES = {torch.bfloat16: LORA_BF16, torch.float32: LORA_FP32}
 
 
@@ -647,24 +663,15 @@ def lora_rms_norm(h, x, weight, eps, residual=None, residual_out=None, q=None, s
     ph = pr = po = pq = None
     ld_h = ld_r = ld_o = 0
     if h is not None:
-        ld_h = _matrix(h, "h", T, d)[2]
-        ph = _cuda_on(h, "h", index)
-        if h.dtype != dtype:
-            raise LoraError("x, h, residual and weight share one dtype")
+        ph, ld_h = _like(h, "h", T, d, index, dtype)
     if residual is not None:
-        if residual_out is None:
-            residual_out = residual
-        ld_r = _matrix(residual, "residual", T, d)[2]
-        ld_o = _matrix(residual_out, "residual_out", T, d)[2]
-        pr, po = _cuda_on(residual, "residual", index), _cuda_on(residual_out, "residual_out", index)
-        if residual.dtype != dtype or residual_out.dtype != dtype:
-            raise LoraError("x, h, residual and weight share one dtype")
+        pr, ld_r = _like(residual, "residual", T, d, index, dtype)
+        po, ld_o = (pr, ld_r) if residual_out is None else _like(residual_out, "residual_out", T, d, index, dtype)
     elif residual_out is not None:
         raise LoraError("residual_out without residual")
-    if not isinstance(weight, torch.Tensor) or weight.shape != (d,) or not weight.is_contiguous():
-        raise LoraError("weight must be contiguous [d]")
-    if weight.dtype != dtype:
-        raise LoraError("x, h, residual and weight share one dtype")
+    if not isinstance(weight, torch.Tensor) or weight.shape != (d,) or weight.dtype is not dtype or \
+            not weight.is_contiguous():
+        raise LoraError("weight must be contiguous [d] of x's dtype")
     if q is not None:
         _mx(q, "q")
         if q.cols != d or q.rows < T or q.index != index:
