@@ -14,9 +14,10 @@
  * "LoRA service: multi-adapter dynamic loading", section 2: A_all
  * [N_adapters, r, d] plus a per-request adapter id; page "LoRA hot load and
  * adapter routing": per-request lora_ids where None means the base model).
- * The shared base product W x is not part of this library: y arrives holding
- * it and leaves holding it plus the delta (merge step of the page "Multi-LoRA
- * Serving", section 2 flowchart: y_i = base_i + delta_i).
+ * The shared base product W x of dense weights is not part of this library: y
+ * arrives holding it and leaves holding it plus the delta (merge step of the page
+ * "Multi-LoRA Serving", section 2 flowchart: y_i = base_i + delta_i).  Over weights
+ * held in microscaled 4-bit form lora_mx_linear computes it.
  *
  * Conventions for every entry point
  *   - Pointers named d_* or documented "device" are device memory owned by the

@@ -111,3 +111,56 @@ def test_no_rows(cuda_lib):
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
     lora.lora_mx_linear(torch.empty(0, 64, device="cuda"), xm, wm, status)
     assert int(status.item()) == 0
+
+
+def _whole_on_gpu(rows, cols, fmt, most, g):
+    v = torch.randint(-most, most + 1, (rows, cols), generator=g, device="cuda", dtype=torch.int8)
+    m = lora.MxTensor(rows, cols, fmt)
+    lora.lora_mx_quantize(m, v.to(torch.bfloat16))
+    return m, v
+
+
+def _check_whole(T, d, n, fmt, dtype, pad, seed):
+    """Whole numbers up to 3 and 2 (exact in every format: a block's largest is at most 3): the exact product."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    (xm, xv), (wm, wv) = _whole_on_gpu(T, d, fmt, 3, g), _whole_on_gpu(n, d, mx.MXFP4, 2, g)
+    y = torch.full((T + 1, n + pad), 99.0, dtype=dtype, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    lora.lora_mx_linear(y[:T, :n], xm, wm, status)
+    ref = torch.zeros(T, n, dtype=torch.float64, device="cuda")
+    for lo in range(0, d, 65536):
+        ref += xv[:, lo:lo + 65536].double() @ wv[:, lo:lo + 65536].double().T
+    assert ref.abs().max() < 2 ** 24 and int(status.item()) == 0
+    assert torch.equal(y[:T, :n], ref.to(dtype)), (T, d, n, fmt, dtype, pad)
+    assert (y[T] == 99).all() and (y[:, n:] == 99).all()
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_random_shapes_are_exact(cuda_lib, seed):
+    r = np.random.default_rng(seed)
+    done = 0
+    while done < 25:
+        T, d, n = int(2 ** r.uniform(0, 11.5)), int(2 ** r.uniform(0, 13.5)), int(2 ** r.uniform(0, 14.5))
+        if r.random() < 0.4:
+            d = max(128, d // 128 * 128)
+        if r.random() < 0.4:
+            n = max(8, n // 8 * 8)
+        if T * d * n > 1 << 36:
+            continue
+        done += 1
+        _check_whole(T, d, n, int(r.integers(2)), DTYPES[int(r.integers(2))], int(r.choice([0, 0, 1, 8])), done)
+
+
+@pytest.mark.parametrize("T,d,n", [(1, 512, 19000), (64, 1024, 28672), (100, 640, 20001), (128, 896, 37888), (128, 896, 38000),
+                                   (17, 384, 18960), (250, 512, 11000)])
+@pytest.mark.parametrize("fmt", FMT)
+def test_wide_outputs_are_exact(cuda_lib, T, d, n, fmt):
+    """Output widths of one to two tiles of features a multiprocessor, and beside them."""
+    for dtype in DTYPES:
+        _check_whole(T, d, n, fmt, dtype, 3, T + n)
+
+
+@pytest.mark.parametrize("T,d,n,fmt", [(1, 1 << 20, 128, 0), (300, 1 << 20, 130, 1), (600, 1 << 19, 128, 0), (131072, 64, 72, 1),
+                                       (1, 96, 1 << 20, 0)])
+def test_largest_sizes_are_exact(cuda_lib, T, d, n, fmt):
+    _check_whole(T, d, n, fmt, torch.float32, 0, 1)

@@ -231,3 +231,37 @@ def test_norm_zero_rows_nan_rows_and_empty(cuda_lib):
     lora.lora_rms_norm(h[:0], empty, w, 1e-5, q=q)
     lora.lora_mx_quantize(q, empty)
     lora.lora_mx_dequantize(out[:0], q)
+
+
+@pytest.mark.parametrize("seed", range(6))
+def test_random_shapes(cuda_lib, seed):
+    """Random sizes, types, strides and formats through all three row operators."""
+    r = np.random.default_rng(seed)
+    for k in range(12):
+        T, d = int(2 ** r.uniform(0, 11)), int(2 ** r.uniform(0, 12))
+        if r.random() < 0.3:
+            d = max(8, d // 8 * 8)
+        dtype, fmt, pad = DTYPES[int(r.integers(2))], int(r.integers(2)), int(r.choice([0, 0, 1, 8]))
+        x = _rows(seed * 100 + k, T, d + pad, dtype).cuda()[:, :d]
+        q = lora.MxTensor(T, d, fmt)
+        lora.lora_mx_quantize(q, x)
+        codes, scales = from_device(q)
+        rc, rs = mx.quantize(as64(x), fmt)
+        np.testing.assert_array_equal(scales, rs)
+        np.testing.assert_array_equal(codes, rc)
+        out = torch.full((T + 1, d + pad), 5.0, device="cuda")
+        lora.lora_mx_dequantize(out[:T, :d], q)
+        np.testing.assert_array_equal(as64(out[:T, :d]), mx.values(rc, rs, fmt, d))
+        assert (out[T] == 5).all() and (out[:, d:] == 5).all()
+        w = torch.randn(d, generator=torch.Generator().manual_seed(k)).to(dtype).cuda()
+        res = _rows(seed * 100 + k + 50, T, d, dtype).cuda()
+        h, s = torch.full((T + 1, d + pad), 5.0, dtype=dtype, device="cuda"), torch.empty_like(res)
+        lora.lora_rms_norm(h[:T, :d], x, w, 1e-6, residual=res, residual_out=s, q=q)
+        rsum, ref = _norm_ref(x.cpu(), res.cpu(), w.cpu(), 1e-6, dtype)
+        np.testing.assert_array_equal(as64(s), rsum)
+        assert (np.abs(as64(h[:T, :d]) - ref) <= _norm_tol(ref, d, dtype)).all()
+        assert (h[T] == 5).all() and (h[:, d:] == 5).all()
+        codes, scales = from_device(q)
+        rc, rs = mx.quantize(as64(h[:T, :d]), fmt)
+        np.testing.assert_array_equal(scales, rs)
+        np.testing.assert_array_equal(codes, rc)
