@@ -8,10 +8,14 @@
 //   X MXFP4, W MXFP4   kind::mxf4, K = 64 (two scales) per instruction, packed
 //
 // Both kinds see rows of 128 bytes with 128-byte swizzle and step 32 bytes per instruction,
-// four to a ring stage: 128 columns of K (MXFP8) or 256 (MXFP4).  The storage's
-// 512-byte scale tile (128 rows x 4 blocks, 16 bytes for rows r, r+32, r+64,
-// r+96) is what tcgen05.cp.32x128b.warpx4 spreads over tensor memory as the
-// MMA wants it: lane r, one column per 32 rows, a byte per block.
+// four to a box: 128 columns of K (MXFP8) or 256 (MXFP4).  Scales lie in tensor memory as the
+// MMA wants them: lane r, one column per 32 rows, a byte per block, the same in all four 32-lane partitions;
+// the storage's 512-byte tile (128 rows x 4 blocks, 16 bytes for rows r, r+32, r+64, r+96) is a
+// lane's four columns.  Warps put them there with tcgen05.st: tcgen05.cp would do it from shared
+// memory, but waits in line with the MMAs (six copies a stage of the pair kernel below: 1003 us
+// at 8192 x 8192 x 28672 in 4 bits, 845 without).
+//
+// Two kernels, for few and many rows of x; which one: launch_linear.
 #include "mx.cuh"
 #include "ptx.cuh"
 #include "tc.cuh"
@@ -173,13 +177,15 @@ __device__ __forceinline__ void drain_ring(Ring r, uint32_t full) {
 // slots.  Roles: one warp copies W and its scales, one x and its, one issues MMAs, four move scales from
 // shared to tensor memory, eight take the finished
 // accumulator.  There are two: one tile's sums are stored while the next one's products go on; or, MT = 2, one for each
-// 128 features, which reads x once for both and may leave a block one tile in place of two (256 x 4096 x 14336 25.4 -> 20.5 us).  S > 1 only where every cluster has one tile:
-// its blocks then add their partial sums, in block order, through distributed shared memory: each owns
+// 128 features, which reads x once for both and may leave a block one tile in place of two (256 x 4096 x 14336 25.4 -> 20.5
+// us; tiles of the height that spreads the features evenly over all SMs took the same time).  S > 1 only where every
+// cluster has one tile: its blocks then add their partial sums, in block order, through distributed shared memory: each owns
 // 1 / S of the rows, and gets the others' sums by plain stores between cluster barriers (st.async, which counts every
 // 16 bytes on a barrier, took 1.4 us per 16 rows).  They land behind the ring (few rows) or, once every
 // block's products are done, in it.
 //
-// Bound: W's bytes from HBM (64 rows, 4096 -> 28672: 66 MB), or, per SM, filling shared memory.  What
+// Bound: W's bytes from HBM (64 rows, 4096 -> 28672: 66 MB in 18.5 us, 3.6 TB/s; x in MXFP4 15.2 us), or, per SM, filling
+// shared memory (257 x 14336 x 4096: 22.8 us).  What
 // a warp does per slot counts as much: a stage of the MMA warp with a barrier for each 128
 // columns and one for its scales took 1200 clocks per 256 columns, the products 320.
 // warp 0 copies W, 1 MMAs, 2-5 scales, 6-9 and 11-14 sums and stores (every other 16 rows), 10 copies x
@@ -617,7 +623,8 @@ int launch_few(const MxLinArgs &l, const lora_mx *x, const lora_mx *w, int dev, 
 // features (N): each block loads its own 128 rows of x and 128 of W's rows, the
 // tensor cores share the halves, so a block moves 32 KB of a stage for 256 x 256 x 32
 // bytes of products, half of what two 128 x 256 tiles would.  At the 4-bit rate that
-// is 64 bytes a clock and SM from L2: the reason for the pair.  Persistent: pair p
+// is 64 bytes a clock and SM from L2: the reason for the pair.  8192 x 8192 x 28672 in 4 bits: 715 us (5.4 PFLOP/s) in a short
+// burst, 829 us steady at 1485 MHz under the power cap, 633 us on zeros.  Persistent: pair p
 // takes tiles p, p + pairs, ... of bands of 16 x tiles, x's tiles fastest: concurrent pairs share W's rows and few enough
 // of x's to find both in the nearer half of L2 (8192 x 8192 x 28672 in MXFP8, steady 1650 -> 1510 us;
 // 8192 x 4096 x 4096 in MXFP4 66.6 -> 65.0).
