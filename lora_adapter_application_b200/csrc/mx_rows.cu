@@ -3,7 +3,7 @@
 // type and, optionally, microscaled.  Contracts: lora_delta.h.
 //
 // All three stream rows once and are bound by HBM: norm 8192 x 8192 bf16 with residual and MXFP8 copy 95 us (6.4 TB/s),
-// quantize 28672 x 8192 to MXFP4 107 us (5.5), dequantize 92 us (6.4); one row of 4096 2.2 us.  A lane holds 8 consecutive
+// quantize 28672 x 8192 to MXFP4 91 us (6.6), dequantize 93 us (6.4); one row of 4096 2.2 us.  A lane holds 8 consecutive
 // columns (one 16-byte bf16 access), so 4 lanes hold a scale's block of 32 and a
 // warp 256 columns = two scale tiles; the block's largest magnitude takes two
 // shuffles, the tile's four scale bytes two more.
@@ -54,12 +54,41 @@ __global__ void __launch_bounds__(ROWS_THREADS)
             raw_round(v, u[j]);
         }
     }
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-        const int64_t row = it.row + 32 * j;
+    if constexpr (J == 1) {
         float v[8];
-        raw_values(u[j], v);
-        mx_emit<FP4>(q + row * row_bytes, scales, row, it.c0, pad, lane, row < T, v, mx_top(u[j]));
+        raw_values(u[0], v);
+        mx_emit<FP4>(q + it.row * row_bytes, scales, it.row, it.c0, pad, lane, it.row < T, v, mx_top(u[0]));
+    } else {
+        // Four rows: lane s of a block's four finds row s's largest magnitude, its code and factor, and stores its scale (a byte;
+        // the rows' 4 words lie side by side).  Each row's own way through mx_emit: 28672 x 8192 bf16 to MXFP4 106 us, 91 so.
+        uint32_t m[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m[j] = mx_top(u[j]);
+        const int s = lane & 3, col = it.c0 + 8 * lane;
+        const bool odd = s & 1, high = s & 2;
+        const uint32_t m0 = max(high ? m[2] : m[0], __shfl_xor_sync(FULL, high ? m[0] : m[2], 2));
+        const uint32_t m1 = max(high ? m[3] : m[1], __shfl_xor_sync(FULL, high ? m[1] : m[3], 2));
+        const uint32_t code = mx_code<FP4>(max(odd ? m1 : m0, __shfl_xor_sync(FULL, odd ? m0 : m1, 1)));
+        const float inverse = mx_inverse(code);
+        if (it.row + 32 * s < T && col < pad)
+            scales[mx_scale_word(it.row, col >> 7, pad / MX_TILE_COLS) + 4 * s + ((col >> 5) & 3)] = (uint8_t)code;
+        const bool nans = __any_sync(FULL, code == 255u);
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int64_t row = it.row + 32 * j;
+            const float inv = __shfl_sync(FULL, inverse, j, 4);
+            float v[8];
+            raw_values(u[j], v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] *= inv;
+            if (nans && inv == 0.f)   // elements of a NaN block: zeros
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = 0.f;
+            if (row < T && col < pad) {
+                if (FP4) *reinterpret_cast<uint32_t *>(q + row * row_bytes + (col >> 1)) = mx_pack_e2m1(v);
+                else *reinterpret_cast<uint2 *>(q + row * row_bytes + col) = mx_pack_e4m3(v);
+            }
+        }
     }
 }
 

@@ -47,6 +47,30 @@ def test_quantize_is_the_oracles(cuda_lib, T, d, dtype, fmt):
 
 @pytest.mark.parametrize("fmt", FMT)
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,d", [(2403, 2056), (2370, 2050), (18990, 100), (19000, 136)])
+def test_quantize_of_four_rows_a_warp(cuda_lib, T, d, dtype, fmt):
+    """Enough rows that a warp takes four of a band: bands of any height, a last group of half its
+    columns, NaN blocks in one of the four rows, in several and beside others; rows behind
+    the last stay as they were."""
+    x = _rows(T + d, T, d, dtype)
+    g = torch.Generator().manual_seed(T)
+    for value in (float("nan"), float("inf"), -float("inf")):
+        x[torch.randint(T, (200,), generator=g), torch.randint(d, (200,), generator=g)] = value
+    x[5, 3] = x[37, 4] = x[101, 31] = float("nan")
+    x[T - 1, d - 1] = float("inf")
+    q = lora.MxTensor(T + 40, d, fmt)
+    q.q.fill_(0xA5)
+    q.scales.fill_(0x5A)
+    lora.lora_mx_quantize(q, x.cuda())
+    codes, scales = from_device(q)
+    rc, rs = mx.quantize(as64(x), fmt)
+    np.testing.assert_array_equal(scales[:T], rs)
+    np.testing.assert_array_equal(codes[:T], rc)
+    assert (q.q[T:] == 0xA5).all() and (scales[T:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_quantize_edge_values(cuda_lib, dtype, fmt):
     """Ties, saturation, the block's largest at and beside powers of two, zeros of both
     signs, the type's largest and smallest (subnormal) numbers; infinities and NaN
