@@ -532,9 +532,13 @@ class MxTensor:
     """A microscaled matrix [rows][cols] (lora_mx): ``q`` uint8 [rows, row bytes] and
     ``scales`` uint8, allocated zero-filled or given by the caller in the layout of
     include/lora_delta.h.  ``fmt``: LORA_MXFP8 or LORA_MXFP4.  Calls that take fewer
-    rows use the first ones."""
+    rows use the first ones.  Its fields are fixed: the C struct ``c`` holds the addresses, and a
+    call refuses a q or scales whose memory was replaced since (resize_, set_, .data)."""
 
-    __slots__ = ("rows", "cols", "fmt", "q", "scales", "device", "index", "c", "ref")
+    __slots__ = ("rows", "cols", "fmt", "q", "scales", "device", "index", "c", "ref", "at_q", "at_scales")
+
+    def __setattr__(self, name, value):
+        raise LoraError("the fields of an MxTensor are fixed: make another one")
 
     def __init__(self, rows, cols, fmt, q=None, scales=None, device=None):
         row_bytes, n_scales = lora_mx_row_bytes(fmt, cols), lora_mx_scale_bytes(rows, cols)
@@ -551,15 +555,18 @@ class MxTensor:
                 raise LoraError(f"{what} must be a contiguous uint8 tensor of at least {n} entries")
         if q.device != scales.device:
             raise LoraError("q and scales must be on one device")
-        self.rows, self.cols, self.fmt, self.q, self.scales, self.device = rows, cols, fmt, q, scales, q.device
-        self.index = q.get_device() if q.is_cuda else -1
-        self.c = lora_mx(q.data_ptr(), scales.data_ptr(), rows, cols, fmt)
-        self.ref = ctypes.addressof(self.c)
+        c = lora_mx(q.data_ptr(), scales.data_ptr(), rows, cols, fmt)
+        for name, value in (("rows", rows), ("cols", cols), ("fmt", fmt), ("q", q), ("scales", scales),
+                            ("device", q.device), ("index", q.get_device() if q.is_cuda else -1), ("c", c),
+                            ("ref", ctypes.addressof(c)), ("at_q", q.data_ptr()), ("at_scales", scales.data_ptr())):
+            object.__setattr__(self, name, value)
 
 
 def _mx(t, what):
     if type(t) is not MxTensor:
         raise LoraError(f"{what} must be an MxTensor")
+    if t.q.data_ptr() != t.at_q or t.scales.data_ptr() != t.at_scales:
+        raise LoraError(f"{what}: its q or scales was given other memory after the MxTensor was made")
     if t.index < 0:
         raise LoraError(f"{what} must be on a CUDA device")
     return t

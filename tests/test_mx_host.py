@@ -182,3 +182,29 @@ def test_binding_refuses_cpu_and_mismatched_operands(lib):
         lora.lora_rms_norm(x, x.t(), x[0], 1e-5)
     with pytest.raises(LoraError, match="overlap"):
         lora.lora_rms_norm(x, x[:1].expand(5, 64), x[0], 1e-5)
+
+
+def test_mxtensor_is_its_memory(lib):
+    """The C struct holds the addresses of construction: fields cannot be replaced, and a tensor that
+    was given other memory in place (the old may belong to someone else by then) is refused by every call."""
+    m = lora.MxTensor(5, 300, lora.LORA_MXFP4, device="cpu")
+    for name, value in [("q", torch.zeros_like(m.q)), ("scales", torch.zeros_like(m.scales)), ("rows", 9), ("cols", 128),
+                        ("fmt", lora.LORA_MXFP8), ("device", "cuda"), ("index", 0)]:
+        with pytest.raises(LoraError, match="fixed"):
+            setattr(m, name, value)
+    x, h, st = torch.zeros(5, 300), torch.zeros(5, 300), torch.zeros(1, dtype=torch.int32)
+    ok = lora.MxTensor(5, 300, lora.LORA_MXFP4, device="cpu")
+    for change in (lambda q: q.q.resize_(4000, 192), lambda q: q.scales.set_(torch.zeros(4096, dtype=torch.uint8)),
+                   lambda q: q.q.set_(), lambda q: setattr(q.scales, "data", q.scales.clone()),
+                   lambda q: q.q.untyped_storage().resize_(0)):
+        m = lora.MxTensor(5, 300, lora.LORA_MXFP4, device="cpu")
+        change(m)
+        for call in (lambda: lora.lora_mx_quantize(m, x), lambda: lora.lora_mx_dequantize(x, m),
+                     lambda: lora.lora_mx_linear(torch.zeros(5, 5), m, ok, st),
+                     lambda: lora.lora_mx_linear(torch.zeros(5, 5), ok, m, st)):
+            with pytest.raises(LoraError, match="memory|CUDA"):
+                call()
+        with pytest.raises(LoraError, match="memory"):
+            lora.lora_mx_quantize(m, x)
+        with pytest.raises(LoraError, match="memory"):
+            lora._mx(m, "q")
