@@ -44,6 +44,7 @@ DEV_BAD_ID, DEV_TILE_OVERFLOW, DEV_BAD_RANK, DEV_TIMEOUT = 1, 2, 4, 8
 ERR_CUDA = -8   # LORA_ERR_CUDA
 MAX_ROWS, MAX_ADAPTERS, MAX_RANK, MAX_SLICES, LONG_TILE = 131072, 4096, 128, 8, 128
 MAX_TILE_ROWS = 64
+MX_MAX = 1048576   # LORA_MX_MAX: rows, columns of a microscaled matrix
 
 _P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
@@ -520,11 +521,16 @@ def lora_merge_adapter(W, A, B, n, ranks, alphas, status, sign=1, stream=None):
 
 
 # ---------------------------------------------------------------- microscaled base
+# Sizes are compared here as Python's whole numbers: ctypes passes what does not fit an int32 modulo 2^32.
 def lora_mx_row_bytes(fmt, cols):
+    if fmt not in (LORA_MXFP8, LORA_MXFP4) or not 1 <= cols <= MX_MAX:
+        return 0
     return int(load().lora_mx_row_bytes(fmt, cols))
 
 
 def lora_mx_scale_bytes(rows, cols):
+    if not (0 <= rows <= MX_MAX and 1 <= cols <= MX_MAX):
+        return 0
     return int(load().lora_mx_scale_bytes(rows, cols))
 
 
@@ -662,6 +668,8 @@ def lora_rms_norm(h, x, weight, eps, residual=None, residual_out=None, q=None, s
     residual_out, by default in place) or x; q (MxTensor, optional): the rows of h
     microscaled as well.  h may be None when q is given."""
     T, d, ld_x = _matrix(x, "x")
+    if T > MAX_ROWS or d > MX_MAX:
+        raise LoraError(f"x has at most {MAX_ROWS} rows of at most {MX_MAX} columns")
     if not x.is_cuda:
         raise LoraError("x must be a CUDA tensor")
     index, dtype = x.get_device(), x.dtype

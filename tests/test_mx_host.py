@@ -208,3 +208,20 @@ def test_mxtensor_is_its_memory(lib):
             lora.lora_mx_quantize(m, x)
         with pytest.raises(LoraError, match="memory"):
             lora._mx(m, "q")
+
+
+def test_sizes_past_32_bits_are_refused(lib):
+    """ctypes would pass them modulo 2^32: a matrix of 2^32 + 64 columns as one of 64, the norm of such a row
+    over its first 64."""
+    big = 1 << 32
+    for fmt, cols in [(0, big + 64), (1, big + 64), (0, 64 - big), (big, 64)]:
+        assert lora.lora_mx_row_bytes(fmt, cols) == 0
+    for rows, cols in [(big + 1, 64), (1 - big, 64), (1, big + 64)]:
+        assert lora.lora_mx_scale_bytes(rows, cols) == 0
+    for a in [(2, big + 64, 0), (big + 2, 64, 0), (2, 64, big)]:
+        with pytest.raises(LoraError, match="at most"):
+            lora.MxTensor(*a, q=torch.zeros(2, 128, dtype=torch.uint8), scales=torch.zeros(512, dtype=torch.uint8))
+    for T, d in [(1, big + 64), (big + 1, 64), (131073, 8), (1, (1 << 20) + 1)]:
+        x, w = torch.empty(T, d, dtype=torch.bfloat16, device="meta"), torch.empty(d, dtype=torch.bfloat16, device="meta")
+        with pytest.raises(LoraError, match="at most"):
+            lora.lora_rms_norm(torch.empty_like(x), x, w, 1e-5)
