@@ -383,6 +383,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
             }
             for (int k = k_lo; k < k_hi; ++k, ring.next()) {
                 if (!uniform_wait(sf_full(ring.slot), ring.parity, a.status, failed)) break;
+                tc_fence_after();   // earlier MMAs read these columns (their commit let the scales' copy go ahead)
                 const uint32_t slot = base + (uint32_t)ring.slot * slot_bytes, to = dst + sf_cols * (uint32_t)ring.slot;
 #pragma unroll
                 for (int i = 0; i < KT; ++i) {   // a tile past k's end is old data that no MMA reads
@@ -800,6 +801,7 @@ __global__ void __launch_bounds__(BIG_THREADS, 1) mx_linear_big_kernel(const __g
             for (int i = 0; i < a.n_stage; ++i, ++it) {
                 const int s = it % BIG_STAGES;
                 if (!warp_wait(sf_full(s), (unsigned)(it / BIG_STAGES) & 1u, a.status, failed)) break;
+                tc_fence_after();   // earlier MMAs read these columns (their commit let the scales' copy go ahead)
                 const uint32_t src = base + (uint32_t)s * SLOT + 32768u + 16u * lane, to = dst + SF_COLS * (uint32_t)s;
 #pragma unroll
                 for (int k = 0; k < TPS; ++k) {   // a tile past k's end is old data that no MMA reads

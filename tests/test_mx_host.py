@@ -225,3 +225,18 @@ def test_sizes_past_32_bits_are_refused(lib):
         x, w = torch.empty(T, d, dtype=torch.bfloat16, device="meta"), torch.empty(d, dtype=torch.bfloat16, device="meta")
         with pytest.raises(LoraError, match="at most"):
             lora.lora_rms_norm(torch.empty_like(x), x, w, 1e-5)
+
+
+def test_tensor_memory_is_fenced_after_every_wait():
+    """The order that no run can be relied on to show wrong: between a wait on another warp's barrier and the first
+    tensor-memory access behind it (store of scales, load of sums, MMAs) stands tcgen05.fence::after_thread_sync."""
+    import os
+    import re
+    src = open(os.path.join(os.path.dirname(lora.__file__), "csrc", "mx_linear.cu")).read()
+    src = src[src.index("mx_linear_few_kernel(const"):]
+    waits = [m.start() for m in re.finditer(r"wait(<\w+>)?\((sf_full|full|acc_full|acc_empty)\b", src)]
+    uses = [m.start() for m in re.finditer(r"\b(tmem_st4|tc_ld16|tc_ld32|mx_stage_mmas<)", src)]
+    assert len(waits) >= 8 and len(uses) >= 8
+    for u in uses:
+        last = max((w for w in waits if w < u), default=None)
+        assert last is None or "tc_fence_after();" in src[last:u], src[last:u]
