@@ -81,7 +81,10 @@
  *                       a few ms, for one shrink signal more than their unit gives:
  *                       the waits run out, LORA_DEV_TIMEOUT is set, the call's
  *                       results are unreliable, and the kernel still completes (the
- *                       context stays usable).
+ *                       context stays usable).  In lora_mx_linear (1 to 5) one warp waits
+ *                       for what never comes, in place of its first wait: the products'
+ *                       (1), one of the scales' (2), one of the sums' (4), either of two
+ *                       that copy (3, 5); its other waits are as short.
  */
 #ifndef LORA_DELTA_H
 #define LORA_DELTA_H

@@ -21,6 +21,7 @@
 #include "tc.cuh"
 
 #include <algorithm>
+#include <cstdlib>
 #include <mutex>
 #include <type_traits>
 
@@ -38,7 +39,11 @@ struct MxLinArgs {   // a call, as the launchers take it
     int n_kt;      // scale tiles along k: padded columns / 128
     int n_stage;   // ring stages of k
     int32_t *status;
+    unsigned limit;   // tries of a bounded wait
+    int stall;        // test hook (STALL_*)
 };
+// The role that waits for what never comes, of LORA_DEBUG_STALL; every other wait is then short too.
+enum { STALL_MMA = 1, STALL_SCALES = 2, STALL_COPY = 3, STALL_SUMS = 4, STALL_COPY_FIRST = 5 };
 
 template <int KIND>
 __host__ __device__ constexpr int mx_tiles_per_stage() { return KIND == MX_A8 ? 1 : 2; }
@@ -83,13 +88,59 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
-// Bounded wait of a whole warp, uniform for all its lanes.
-__device__ __forceinline__ bool uniform_wait(uint32_t bar, unsigned parity, int32_t *status, bool &failed) {
-    for (unsigned it = 0; it < WAIT_LIMIT; ++it)
+// A kernel's bounded waits.  The first that runs out says so in `stop`, a word of the block's shared memory (of both
+// blocks' where a pair works together): every wait that goes on ends too, and the teardown, which all warps reach, lets what
+// is under way come to rest before the block goes.
+struct Bound {
+    uint32_t stop;
+    unsigned limit;   // tries
+    int32_t *status;
+};
+__device__ __forceinline__ uint32_t stopped(uint32_t stop) {
+    uint32_t r;
+    asm volatile("ld.relaxed.cluster.shared::cta.u32 %0, [%1];\n" : "=r"(r) : "r"(stop));
+    return r;
+}
+// Wait of a whole warp, uniform for all its lanes: for warps that copy and issue.
+__device__ __forceinline__ bool uniform_wait(uint32_t bar, unsigned parity, const Bound &w, bool &failed) {
+    if (__all_sync(FULL, mbar_try<false>(bar, parity))) return true;
+    for (unsigned it = 1; it < w.limit && !__any_sync(FULL, stopped(w.stop)); ++it)
         if (__all_sync(FULL, mbar_try<false>(bar, parity))) return true;
-    if (elect_one()) atomicOr(status, LORA_DEV_TIMEOUT);
     failed = true;
     return false;
+}
+// The same, lane by lane: for warps that move scales and sums.  As a uniform_wait theirs took 1 x 4096 x 4096 5.46 -> 5.56 us
+// and 8192 x 4096 x 4096 in MXFP4 65.8 -> 69.0.
+__device__ __forceinline__ bool lanes_wait(uint32_t bar, unsigned parity, const Bound &w, bool &failed) {
+    bool ok = false;
+    for (unsigned it = 0; it < w.limit; ++it) {
+        if ((ok = mbar_try<false>(bar, parity))) break;
+        if (stopped(w.stop)) break;
+    }
+    ok = __all_sync(FULL, ok);
+    if (!ok) failed = true;
+    return ok;
+}
+// A warp's part has ended: after a wait of its own that ran out, or that another's stopped.
+template <bool PAIR>
+__device__ __forceinline__ void leave(const Bound &w, bool failed) {
+    if (failed && elect_one()) {
+        atomicOr(w.status, LORA_DEV_TIMEOUT);
+        if (PAIR) {
+#pragma unroll
+            for (uint32_t k = 0; k < 2; ++k)
+                asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], 1;\n" ::"r"(map_rank(w.stop, k)) : "memory");
+        } else {
+            asm volatile("st.relaxed.cluster.shared::cta.u32 [%0], 1;\n" ::"r"(w.stop) : "memory");
+        }
+    }
+}
+// Wait of the teardown after a wait that ran out: for copies and products in flight, which end by themselves.
+__device__ __forceinline__ void rest_wait(uint32_t bar, unsigned parity) {
+    for (unsigned it = 0; it < 1024 && !__all_sync(FULL, mbar_try<false>(bar, parity)); ++it) {}
+}
+__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, unsigned bytes) {   // as a copy of so many bytes would
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 // 16 bytes to four columns of this thread's tensor-memory lane
@@ -131,17 +182,17 @@ __device__ __forceinline__ void y_store(void *y, int64_t at, float v) {
     else static_cast<float *>(y)[at] = v;
 }
 
-// A place in a ring of n slots: the slot and the parity of its current use.  Kept by counting: an
-// integer division costs as much as the MMAs of a stage.
+// A place in a ring of n slots, after so many uses of slots: the next slot and the parity of its use.  Kept by
+// counting: an integer division costs as much as the MMAs of a stage.
 struct Ring {
-    int slot = 0, n, left;   // left: uses until every slot has been used once
-    unsigned parity = 0;
-    __device__ explicit Ring(int n_) : n(n_), left(n_) {}
+    int slot, n;
+    unsigned uses, parity;
+    __device__ explicit Ring(int n_, unsigned used = 0) : slot((int)(used % (unsigned)n_)), n(n_), uses(used), parity(used / (unsigned)n_ & 1u) {}
     __device__ void next() {
-        left = max(left - 1, 0);
+        ++uses;
         if (++slot == n) slot = 0, parity ^= 1u;
     }
-    __device__ bool reused() const { return left == 0; }
+    __device__ bool reused() const { return uses >= (unsigned)n; }
 };
 
 __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {   // address mapped with map_rank
@@ -163,10 +214,10 @@ __device__ __forceinline__ void sum_rows(Y *y, int64_t ld, uint32_t red, int own
     }
 }
 
-// after a failed wait: the copies that a thread has under way into a ring land before its block goes
+// The last use of each slot of a ring, up to r, is complete on the slots' barriers.
 __device__ __forceinline__ void drain_ring(Ring r, uint32_t full) {
     for (int j = 0; j < r.n; ++j, r.next())   // oldest first: parity ^ 1 is that of the slot's last use
-        for (unsigned w = 0; r.reused() && w < 1024 && !mbar_try<false>(full + 8u * (uint32_t)r.slot, r.parity ^ 1u); ++w) {}
+        if (r.reused()) rest_wait(full + 8u * (uint32_t)r.slot, r.parity ^ 1u);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -205,6 +256,8 @@ struct MxFewArgs {
     int stages, split_log2;     // ring depth; blocks of a cluster
     int own_red;                // the partial sums' place is behind the ring
     int32_t *status;
+    unsigned limit;
+    int stall;
 };
 
 // A slot: W (16 KB a box: a scale tile of MXFP8's k, two of MXFP4's) of each 128 features, x, then the scales of W's
@@ -225,7 +278,8 @@ template <int KIND, int KT, int MT, typename Y>
 __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __grid_constant__ MxFewArgs a) {
     extern __shared__ __align__(1024) unsigned char mx_sm[];
     __shared__ uint32_t tmem_sm;
-    __shared__ __align__(8) uint64_t bars[3 * FEW_STAGES + 4];
+    __shared__ __align__(8) uint64_t bars[3 * FEW_STAGES + 5];
+    __shared__ uint32_t stop_sm, used_sm[6];   // ring uses of the warps that copy W and x and move scales
     constexpr int BOXES = mx_boxes<KIND>(KT);
     const int warp = __shfl_sync(FULL, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t slot_bytes = few_slot_bytes<KIND>(KT, MT, a.bn, a.bands), sf_at = few_sf_at<KIND>(KT, MT, a.bn);
@@ -236,6 +290,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
     auto sf_full = [&](int s) { return bar(2 * FEW_STAGES + s); };
     auto acc_full = [&](int b) { return bar(3 * FEW_STAGES + b); };
     auto acc_empty = [&](int b) { return bar(3 * FEW_STAGES + 2 + b); };
+    const uint32_t rest = bar(3 * FEW_STAGES + 4);   // completes in the teardown after a wait that ran out, else never
+    const Bound bound{smem_u32(&stop_sm), a.limit, a.status};
     const int S = 1 << a.split_log2, rank = (int)blockIdx.x & (S - 1);   // clusters are S consecutive blocks
     const int c0 = (int)blockIdx.x >> a.split_log2, clusters = (int)gridDim.x >> a.split_log2;
     const int k_lo = a.n_ks * rank >> a.split_log2, k_hi = a.n_ks * (rank + 1) >> a.split_log2;
@@ -255,11 +311,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
     Ring ring(a.stages);
 
     if (warp == 0) {
-        for (int i = lane; i < 3 * FEW_STAGES + 4; i += 32) {
+        for (int i = lane; i < 3 * FEW_STAGES + 5; i += 32) {
             // full: both copying warps and the four scale warps; sf_full: both; acc_empty: eight warps
-            const bool six = i < FEW_STAGES, two = i >= 2 * FEW_STAGES && i < 3 * FEW_STAGES, eight = i >= 3 * FEW_STAGES + 2;
+            const bool six = i < FEW_STAGES, two = i >= 2 * FEW_STAGES && i < 3 * FEW_STAGES;
+            const bool eight = i >= 3 * FEW_STAGES + 2 && i < 3 * FEW_STAGES + 4;
             mbar_init(bar(i), six ? 6 : two ? 2 : eight ? 8 : 1);
         }
+        if (lane == 0) stop_sm = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         if (lane == 0) prefetch_tmap(&a.tmW);
         __syncwarp();
@@ -288,13 +346,14 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
 
     const int64_t band = (int64_t)a.n_kt * MX_TILE_BYTES;   // scale bytes of 128 rows
     if (warp == 0) {   // W and its scales
+        if (a.stall == STALL_COPY_FIRST) uniform_wait(rest, 0, bound, failed);
         for (; t < a.tiles && !failed; next_tile()) {
             const uint8_t *sw = a.sw + m0 / 128 * band;
             // features past the last band: any scales will do
             const int64_t sw1 = MT == 2 && m0 / 128 + 1 < a.w_bands ? band : 0;
             for (int k = k_lo; k < k_hi; ++k, ring.next()) {
                 const uint32_t b = full(ring.slot), sb = sf_full(ring.slot), slot = base + (uint32_t)ring.slot * slot_bytes;
-                if (ring.reused() && !uniform_wait(empty(ring.slot), ring.parity ^ 1u, a.status, failed)) break;
+                if (ring.reused() && !uniform_wait(empty(ring.slot), ring.parity ^ 1u, bound, failed)) break;
                 if (elect_one()) {
                     const uint32_t n = (uint32_t)min(KT, a.n_kt - KT * k) * MX_TILE_BYTES;
                     const uint8_t *p = sw + (int64_t)k * KT * MX_TILE_BYTES;
@@ -311,15 +370,16 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
                 }
             }
         }
-        if (failed) drain_ring(ring, sf_full(0)), drain_ring(ring, full(0));
+        if (elect_one()) used_sm[0] = ring.uses;
     } else if (warp == 10) {   // x and its scales
+        if (a.stall == STALL_COPY) uniform_wait(rest, 0, bound, failed);
         const uint32_t x_bytes = (uint32_t)a.bn * 128u;
         for (; t < a.tiles && !failed; next_tile()) {
             const int xb = n0 / 128, nb = min(a.bands, a.x_bands - xb);
             const uint8_t *sx = a.sx + xb * band;
             for (int k = k_lo; k < k_hi; ++k, ring.next()) {
                 const uint32_t b = full(ring.slot), sb = sf_full(ring.slot), slot = base + (uint32_t)ring.slot * slot_bytes;
-                if (ring.reused() && !uniform_wait(empty(ring.slot), ring.parity ^ 1u, a.status, failed)) break;
+                if (ring.reused() && !uniform_wait(empty(ring.slot), ring.parity ^ 1u, bound, failed)) break;
                 if (elect_one()) {
                     const uint32_t n = (uint32_t)min(KT, a.n_kt - KT * k) * MX_TILE_BYTES;
                     const uint8_t *p = sx + (int64_t)k * KT * MX_TILE_BYTES;
@@ -332,25 +392,26 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
                 }
             }
         }
-        if (failed) drain_ring(ring, sf_full(0)), drain_ring(ring, full(0));
+        if (elect_one()) used_sm[1] = ring.uses;
     } else if (warp == 1) {
         const uint32_t idesc = KIND == MX_A8 ? mx_idesc(5, 0, 128, a.bn) : mx_idesc(1, 1, 128, a.bn);
         const uint32_t x_bytes = (uint32_t)a.bn * 128u;
         int n = 0;
+        if (a.stall == STALL_MMA) uniform_wait(rest, 0, bound, failed);
         for (; t < a.tiles && !failed; next_tile(), ++n) {
             const int b = MT == 2 ? 0 : n & 1;
             if (MT == 2) {
-                if (n >= 1 && !(uniform_wait(acc_empty(0), (unsigned)(n - 1) & 1u, a.status, failed) &&
-                                uniform_wait(acc_empty(1), (unsigned)(n - 1) & 1u, a.status, failed)))
+                if (n >= 1 && !(uniform_wait(acc_empty(0), (unsigned)(n - 1) & 1u, bound, failed) &&
+                                uniform_wait(acc_empty(1), (unsigned)(n - 1) & 1u, bound, failed)))
                     break;
-            } else if (n >= 2 && !uniform_wait(acc_empty(b), (unsigned)(n / 2 - 1) & 1u, a.status, failed)) {
+            } else if (n >= 2 && !uniform_wait(acc_empty(b), (unsigned)(n / 2 - 1) & 1u, bound, failed)) {
                 break;
             }
             const uint32_t d = tmem + (uint32_t)b * acc_cols;
             for (int k = k_lo; k < k_hi; ++k, ring.next()) {
                 const uint32_t slot = base + (uint32_t)ring.slot * slot_bytes, ta = sf + sf_cols * (uint32_t)ring.slot;
                 const int tiles = min(KT, a.n_kt - KT * k);
-                if (!uniform_wait(full(ring.slot), ring.parity, a.status, failed)) break;
+                if (!uniform_wait(full(ring.slot), ring.parity, bound, failed)) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -371,6 +432,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
         }
     } else if (warp < 6) {
         const uint32_t dst = sf + ((uint32_t)(32 * (warp & 3)) << 16);
+        if (a.stall == STALL_SCALES && warp == 2) uniform_wait(rest, 0, bound, failed);
         for (; t < a.tiles && !failed; next_tile()) {
             // W: lane r gets the 16 bytes of rows r, r + 32, r + 64, r + 96.  x: the tile's rows may start
             // anywhere in a band; column g, lane r: row n0 + 32 g + r
@@ -382,7 +444,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
                 at[g] = sf_at + (uint32_t)((MT + band) * KT) * MX_TILE_BYTES + (uint32_t)(row % 32 * 16 + row / 32 % 4 * 4);
             }
             for (int k = k_lo; k < k_hi; ++k, ring.next()) {
-                if (!uniform_wait(sf_full(ring.slot), ring.parity, a.status, failed)) break;
+                if (!uniform_wait(sf_full(ring.slot), ring.parity, bound, failed)) break;
                 tc_fence_after();   // earlier MMAs read these columns (their commit let the scales' copy go ahead)
                 const uint32_t slot = base + (uint32_t)ring.slot * slot_bytes, to = dst + sf_cols * (uint32_t)ring.slot;
 #pragma unroll
@@ -403,6 +465,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
                 if (elect_one()) mbar_arrive(full(ring.slot));
             }
         }
+        if (elect_one()) used_sm[warp] = ring.uses;
     } else {
         const int q = warp & 3, f = 32 * q + lane;   // this thread's output feature of the tile
         const int half = 16 * (warp > 10);           // its first row; then every other 16
@@ -414,7 +477,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
             const uint32_t src_acc = acc + (uint32_t)b * acc_cols;
             const bool there = m < a.d_out;
             Y *y = static_cast<Y *>(a.y) + (int64_t)n0 * a.ld_y + m;
-            if (!warp_wait(acc_full(b), (unsigned)(n / 2) & 1u, a.status, failed) && S == 1) break;
+            const bool stall = a.stall == STALL_SUMS && warp == 6;
+            // S > 1: on to the exchange all the same, which every block of the cluster takes part in
+            if (!lanes_wait(stall ? rest : acc_full(b), (unsigned)(n / 2) & 1u, bound, failed) && S == 1) break;
             tc_fence_after();
             if (S == 1) {
                 for (int c = half; c < rows; c += 32) {
@@ -468,6 +533,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
     }
     // ---------------------------------------------------------------- teardown
     __syncwarp();
+    leave<false>(bound, failed);
     if (S > 1 && (warp < 6 || warp == 10)) {   // the barriers that the other warps wait at
         asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
         if (!a.own_red) cluster_sync_all();
@@ -475,6 +541,26 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
     }
     tc_fence_before();
     __syncthreads();
+    if (stop_sm) {
+        // A wait ran out: the other warps stopped where they were.  Each that arrives on the ring's barriers makes up for the
+        // uses that the warps ahead of it began (at most one a slot: none is begun before all are done with the slot's
+        // last one), which then complete as their copies land; the copying warps, whose block's memory these go to, see them land.
+        const unsigned begun = max(used_sm[0], used_sm[1]);
+        const bool copies = warp == 0 || warp == 10;
+        if (copies || (warp >= 2 && warp < 6)) {
+            Ring r(a.stages, used_sm[warp == 10 ? 1 : warp]);
+            for (; r.uses < begun; r.next())
+                if (elect_one()) {
+                    mbar_arrive(full(r.slot));
+                    if (copies) mbar_arrive(sf_full(r.slot));
+                }
+            if (copies) drain_ring(r, sf_full(0)), drain_ring(r, full(0));
+        }
+        if (warp == 1) {   // the products read this memory and tensor memory
+            if (elect_one()) tc_commit(rest);
+            rest_wait(rest, 0);
+        }
+    }
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(tmem_cols) : "memory");
@@ -595,7 +681,7 @@ int launch_few(const MxLinArgs &l, const lora_mx *x, const lora_mx *w, int dev, 
     MxFewArgs a{};
     a.sw = l.sw, a.sx = l.sx, a.y = l.y, a.ld_y = l.ld_y, a.T = l.T, a.d_out = l.d_out, a.n_kt = l.n_kt;
     a.x_bands = (l.T + 127) / 128, a.w_bands = (l.d_out + 127) / 128;
-    a.status = l.status;
+    a.status = l.status, a.limit = l.limit, a.stall = l.stall;
     auto shape = [&](int nt) {   // row tiles of equal height, a multiple of 16
         a.bn = ((l.T + nt - 1) / nt + 15) / 16 * 16;
         a.nt = (l.T + a.bn - 1) / a.bn;
@@ -645,6 +731,8 @@ struct MxBigArgs {
     int mt, nt, tiles;    // 256-row tiles of x, of W; all
     int vec;          // y rows allow 16-byte stores
     int32_t *status;
+    unsigned limit;
+    int stall;
 };
 
 template <int KIND>
@@ -688,7 +776,8 @@ template <int KIND, bool BF16>
 __global__ void __launch_bounds__(BIG_THREADS, 1) mx_linear_big_kernel(const __grid_constant__ MxBigArgs a) {
     extern __shared__ __align__(1024) unsigned char mx_sm[];
     __shared__ uint32_t tmem_sm;
-    __shared__ __align__(8) uint64_t bars[4 * BIG_STAGES + 2];
+    __shared__ __align__(8) uint64_t bars[4 * BIG_STAGES + 3];
+    __shared__ uint32_t stop_sm, used_sm;   // used_sm: ring uses that this block's copies have begun
     constexpr int TPS = mx_tiles_per_stage<KIND>();
     constexpr uint32_t SLOT = big_slot_stride<KIND>();
     constexpr uint32_t SF_COLS = 12 * TPS;   // one stage's scales: 4 columns a tile for x, 8 for W
@@ -702,6 +791,8 @@ __global__ void __launch_bounds__(BIG_THREADS, 1) mx_linear_big_kernel(const __g
     auto sf_full = [&](int s) { return smem_u32(&bars[2 * BIG_STAGES + s]); };    // this block's scales have landed
     auto sf_ready = [&](int s) { return smem_u32(&bars[3 * BIG_STAGES + s]); };   // the leader's: both blocks' are in tensor memory
     const uint32_t acc_full = smem_u32(&bars[4 * BIG_STAGES]), acc_empty = smem_u32(&bars[4 * BIG_STAGES + 1]);
+    const uint32_t rest = smem_u32(&bars[4 * BIG_STAGES + 2]);   // completes in the teardown after a wait that ran out, else never
+    const Bound bound{smem_u32(&stop_sm), a.limit, a.status};
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < BIG_STAGES; ++s) {
@@ -712,6 +803,8 @@ __global__ void __launch_bounds__(BIG_THREADS, 1) mx_linear_big_kernel(const __g
         }
         mbar_init(acc_full, 1);
         mbar_init(acc_empty, 16);   // the leader's: 8 epilogue warps of each block
+        mbar_init(rest, 1);
+        stop_sm = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         prefetch_tmap(&a.tmX);
         prefetch_tmap(&a.tmW);
@@ -737,6 +830,7 @@ __global__ void __launch_bounds__(BIG_THREADS, 1) mx_linear_big_kernel(const __g
 
     if (warp == 0) {
         Ring ring(BIG_STAGES);
+        if (a.stall == (rank ? STALL_COPY : STALL_COPY_FIRST)) uniform_wait(rest, 0, bound, failed);
         for (int t = pair; t < a.tiles && !failed; t += pairs) {
             int mi, ni;
             place(t, mi, ni);
@@ -747,7 +841,7 @@ __global__ void __launch_bounds__(BIG_THREADS, 1) mx_linear_big_kernel(const __g
             const uint8_t *sw1 = a.sw + (int64_t)min(nb + 1, a.w_bands - 1) * a.n_kt * MX_TILE_BYTES;
             for (int i = 0; i < a.n_stage; ++i, ring.next()) {
                 const int s = ring.slot;
-                if (ring.reused() && !uniform_wait(empty(s), ring.parity ^ 1u, a.status, failed)) break;
+                if (ring.reused() && !uniform_wait(empty(s), ring.parity ^ 1u, bound, failed)) break;
                 const uint32_t slot = base + (uint32_t)s * SLOT, bar = map_rank(full(s), 0);
                 const uint32_t sfs = slot + 32768u, sb = (uint32_t)min(TPS, a.n_kt - i * TPS) * MX_TILE_BYTES;
                 if (elect_one()) {
@@ -762,22 +856,20 @@ __global__ void __launch_bounds__(BIG_THREADS, 1) mx_linear_big_kernel(const __g
                 }
             }
         }
-        if (failed) {   // both blocks' copies under way land before the pair goes
-            drain_ring(ring, sf_full(0));
-            if (rank == 0) drain_ring(ring, full(0));
-        }
+        if (elect_one()) used_sm = ring.uses;
     } else if (warp == 1) {
         if (rank == 0) {
             constexpr uint32_t idesc = KIND == MX_A8 ? mx_idesc(0, 5, 256, 256) : mx_idesc(1, 1, 256, 256);
             Ring ring(BIG_STAGES);
             int n = 0;
+            if (a.stall == STALL_MMA) uniform_wait(rest, 0, bound, failed);
             for (int t = pair; t < a.tiles && !failed; t += pairs, ++n) {
-                if (n > 0 && !uniform_wait(acc_empty, (unsigned)(n - 1) & 1u, a.status, failed)) break;
+                if (n > 0 && !uniform_wait(acc_empty, (unsigned)(n - 1) & 1u, bound, failed)) break;
                 tc_fence_after();
                 for (int i = 0; i < a.n_stage; ++i, ring.next()) {
                     const int s = ring.slot;
-                    if (!uniform_wait(sf_ready(s), ring.parity, a.status, failed) ||
-                        !uniform_wait(full(s), ring.parity, a.status, failed))
+                    if (!uniform_wait(sf_ready(s), ring.parity, bound, failed) ||
+                        !uniform_wait(full(s), ring.parity, bound, failed))
                         break;
                     tc_fence_after();
                     const uint32_t slot = base + (uint32_t)s * SLOT;
@@ -797,10 +889,11 @@ __global__ void __launch_bounds__(BIG_THREADS, 1) mx_linear_big_kernel(const __g
         // once its shared memory is: both were read by the same MMAs.
         const uint32_t dst = sf + ((uint32_t)(32 * (warp & 3)) << 16);
         int it = 0;
+        if (a.stall == STALL_SCALES && rank == 1 && warp == 2) uniform_wait(rest, 0, bound, failed);
         for (int t = pair; t < a.tiles && !failed; t += pairs)
             for (int i = 0; i < a.n_stage; ++i, ++it) {
                 const int s = it % BIG_STAGES;
-                if (!warp_wait(sf_full(s), (unsigned)(it / BIG_STAGES) & 1u, a.status, failed)) break;
+                if (!lanes_wait(sf_full(s), (unsigned)(it / BIG_STAGES) & 1u, bound, failed)) break;
                 tc_fence_after();   // earlier MMAs read these columns (their commit let the scales' copy go ahead)
                 const uint32_t src = base + (uint32_t)s * SLOT + 32768u + 16u * lane, to = dst + SF_COLS * (uint32_t)s;
 #pragma unroll
@@ -819,8 +912,9 @@ __global__ void __launch_bounds__(BIG_THREADS, 1) mx_linear_big_kernel(const __g
         const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + 128u * half;
         const uint32_t release = map_rank(acc_empty, 0);
         int n = 0;
-        for (int t = pair; t < a.tiles; t += pairs, ++n) {
-            if (!warp_wait(acc_full, (unsigned)n & 1u, a.status, failed)) break;
+        if (a.stall == STALL_SUMS && rank == 1 && warp == 6) uniform_wait(rest, 0, bound, failed);
+        for (int t = pair; t < a.tiles && !failed; t += pairs, ++n) {
+            if (!lanes_wait(acc_full, (unsigned)n & 1u, bound, failed)) break;
             tc_fence_after();
             int mi, ni;
             place(t, mi, ni);
@@ -875,8 +969,31 @@ __global__ void __launch_bounds__(BIG_THREADS, 1) mx_linear_big_kernel(const __g
         }
     }
     // ---------------------------------------------------------------- teardown
+    __syncwarp();
+    leave<true>(bound, failed);
     tc_fence_before();
     cluster_sync_all();
+    if (stop_sm) {   // a wait ran out: in both blocks, which stopped where they were
+        if (warp == 0) {
+            Ring r(BIG_STAGES, used_sm);
+            drain_ring(r, sf_full(0));
+            if (rank == 0) {
+                // The leader's barriers count both blocks' bytes.  The uses that one block has begun and the other not (at
+                // most one a slot) complete with the bytes of that one.
+                uint32_t other;
+                asm volatile("ld.shared::cluster.u32 %0, [%1];\n" : "=r"(other) : "r"(map_rank(smem_u32(&used_sm), 1)) : "memory");
+                for (uint32_t k = other; k < r.uses; ++k)
+                    if (elect_one()) mbar_complete_tx(full((int)(k % BIG_STAGES)), TX / 2);
+                for (; r.uses < other; r.next())
+                    if (elect_one()) mbar_expect_tx(full(r.slot), TX / 2);
+                drain_ring(r, full(0));
+            }
+        } else if (warp == 1) {   // the products read both blocks' memory and tensor memory
+            if (rank == 0 && elect_one()) tc_commit_pair(rest);
+            rest_wait(rest, 0);
+        }
+        cluster_sync_all();
+    }
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
@@ -896,7 +1013,7 @@ int launch_big(const MxLinArgs &l, const lora_mx *x, const lora_mx *w, int sms, 
     a.nt = (l.d_out + 255) / 256;
     a.tiles = a.mt * a.nt;
     a.vec = mx_vec(l.y, l.ld_y, l.d_out, BF16 ? 2 : 4);
-    a.status = l.status;
+    a.status = l.status, a.limit = l.limit, a.stall = l.stall;
     auto kernel = mx_linear_big_kernel<KIND, BF16>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)MX_MAX_SMEM);
     if (e != cudaSuccess) return cuda_rc(e);
@@ -942,6 +1059,9 @@ int lora_mx_linear(void *y, int64_t ld_y, const lora_mx *x, const lora_mx *w, in
     a.sw = w->scales, a.sx = x->scales, a.y = y, a.ld_y = ld_y, a.T = T, a.d_out = w->rows;
     a.n_kt = (int)(mx_padded(x->cols) / MX_TILE_COLS);
     a.status = status;
+    const char *stall = std::getenv("LORA_DEBUG_STALL");   // test hook: the waits of one role run out, after a short while
+    a.stall = stall ? std::atoi(stall) : 0;
+    a.limit = a.stall ? 64 : WAIT_LIMIT;
     int dev = 0, sms = 148;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);

@@ -164,3 +164,24 @@ def test_wide_outputs_are_exact(cuda_lib, T, d, n, fmt):
                                        (1, 96, 1 << 20, 0)])
 def test_largest_sizes_are_exact(cuda_lib, T, d, n, fmt):
     _check_whole(T, d, n, fmt, torch.float32, 0, 1)
+
+
+# few rows: k split over a cluster with and without a place of its own for the partial sums, one tile and several a block,
+# two accumulators of a tile, all of k within the ring; many rows: one tile a pair and several
+@pytest.mark.parametrize("T,d,n,fmt", [(1, 4096, 4096, 0), (64, 4096, 4096, 1), (257, 14336, 4096, 0), (4, 256, 512, 0), (40, 384, 130, 1),
+                                       (64, 4096, 28672, 0), (128, 4096, 28672, 1), (1024, 2048, 4096, 0), (1200, 256, 2300, 1),
+                                       (3000, 1920, 4500, 0), (3000, 4096, 8192, 1)])
+@pytest.mark.parametrize("role", [1, 2, 3, 4, 5])
+def test_stalled_warp_times_out_and_the_context_survives(cuda_lib, monkeypatch, T, d, n, fmt, role):
+    """LORA_DEBUG_STALL: a warp of one role waits for what never comes.  The bounded wait runs out (a few ms), the other
+    warps stop, LORA_DEV_TIMEOUT is set, nothing behind y is written, and the call returns; the next call is exact."""
+    g = torch.Generator(device="cuda").manual_seed(T + d)
+    (xm, _), (wm, _) = _whole_on_gpu(T, d, fmt, 3, g), _whole_on_gpu(n, d, mx.MXFP4, 2, g)
+    y = torch.full((T + 1, n + 8), 99.0, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    monkeypatch.setenv("LORA_DEBUG_STALL", str(role))
+    lora.lora_mx_linear(y[:T, :n], xm, wm, status)
+    monkeypatch.delenv("LORA_DEBUG_STALL")
+    assert int(status.item()) == lora.DEV_TIMEOUT
+    assert (y[T] == 99).all() and (y[:, n:] == 99).all()
+    _check_whole(T, d, n, fmt, torch.bfloat16, 8, T)
