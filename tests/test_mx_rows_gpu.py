@@ -289,3 +289,26 @@ def test_random_shapes(cuda_lib, seed):
         rc, rs = mx.quantize(as64(h[:T, :d]), fmt)
         np.testing.assert_array_equal(scales, rs)
         np.testing.assert_array_equal(codes, rc)
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("pad", [0, 8, 3])
+@pytest.mark.parametrize("T,d", [(2403, 2056), (2370, 2050), (18990, 100), (19000, 136), (18944, 256)])
+def test_dequantize_of_four_rows_a_warp(cuda_lib, T, d, pad, dtype, fmt):
+    """Enough rows that a warp takes four of a band: bands of any height, a last group of half its columns, rows of out
+    with and without 16-byte steps, NaN blocks in one of the four rows and in several; nothing beside out is written."""
+    assert -(-mx.padded(d) // 256) * T // 4 >= 148 * 32
+    x = as64(_rows(T + d + pad, T, d, torch.float32))
+    g = np.random.default_rng(T)
+    x[g.integers(0, T, 200), g.integers(0, d, 200)] = np.nan
+    x[5, 3] = x[37, 4] = x[101, 31] = x[T - 1, d - 1] = np.inf
+    codes, scales = mx.quantize(x, fmt)
+    m = to_device(codes, scales, fmt, d)
+    out = torch.full((T + 40, d + pad), 7.0, dtype=dtype, device="cuda")
+    lora.lora_mx_dequantize(out[:T, :d], m)
+    want = torch.from_numpy(mx.values(codes, scales, fmt, d)).to(torch.float32).to(dtype)
+    got = out[:T, :d].cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(want)) and bool(torch.isnan(want).any())
+    assert torch.equal(got.nan_to_num(1.0), want.nan_to_num(1.0))
+    assert (out[T:] == 7).all() and (out[:, d:] == 7).all()
