@@ -312,3 +312,44 @@ def test_dequantize_of_four_rows_a_warp(cuda_lib, T, d, pad, dtype, fmt):
     assert torch.equal(torch.isnan(got), torch.isnan(want)) and bool(torch.isnan(want).any())
     assert torch.equal(got.nan_to_num(1.0), want.nan_to_num(1.0))
     assert (out[T:] == 7).all() and (out[:, d:] == 7).all()
+
+
+# The norm's forms by their rule: registers for 1, 2 or 4 groups of 8 columns a thread, or rows read twice; few rows
+# (fewer than four for each of 148 multiprocessors) or many; 16-byte steps or not.  Widths at and beside each border.
+NORM_FORMS = [(T, d) for T in (3, 700) for d in (256, 264, 408, 512, 520, 2048, 2049, 2184, 4096, 4104, 4108, 8192, 8200, 8215, 16384,
+                                                 16392, 16429, 28672, 32768, 32776, 32783)] + [(591, 408), (592, 408), (591, 8200), (592, 8200)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("res", [False, True])
+@pytest.mark.parametrize("T,d", NORM_FORMS)
+def test_every_form_of_the_norm(cuda_lib, T, d, dtype, res):
+    """h and the sum against 64 bits; the microscaled copies are the quantised h; h is the same with and without them;
+    nothing beside the outputs is written."""
+    g = torch.Generator(device="cuda").manual_seed(T + d)
+    x = (torch.randn(T, d, generator=g, device="cuda") * torch.exp(torch.randn(T, 1, generator=g, device="cuda"))).to(dtype)
+    r = (3 * torch.randn(T, d, generator=g, device="cuda")).to(dtype) if res else None
+    w = torch.randn(d, generator=g, device="cuda").to(dtype)
+    total = (x.double() + r.double()).to(dtype) if res else x
+    v = total.double()
+    ref = v / (v.square().mean(1, keepdim=True) + 1e-5).sqrt() * w.double()
+    h = torch.full((T + 1, d + 8), 9.0, dtype=dtype, device="cuda")
+    s = torch.full((T + 1, d + 8), 9.0, dtype=dtype, device="cuda")
+    out = {"residual": r, "residual_out": s[:T, :d]} if res else {}
+    lora.lora_rms_norm(h[:T, :d], x, w, 1e-5, **out)
+    tol = ref.abs() * ((d / 2 + 6) * 2.0 ** -24 + torch.finfo(dtype).eps / 2) + 1e-37
+    assert ((h[:T, :d].double() - ref).abs() <= tol).all()
+    for t in (h, s):
+        assert (t[T] == 9).all() and (t[:, d:] == 9).all()
+    assert torch.equal(s[:T, :d], total) if res else (s == 9).all()
+    for fmt in FMT:
+        a, b = lora.MxTensor(T + 1, d, fmt), lora.MxTensor(T + 1, d, fmt)
+        for m in (a, b):
+            m.q.fill_(0xA5), m.scales.fill_(0x5A)
+        again = torch.empty(T, d, dtype=dtype, device="cuda")
+        lora.lora_rms_norm(again, x, w, 1e-5, q=a, **out)
+        lora.lora_mx_quantize(b, h[:T, :d])
+        assert torch.equal(again, h[:T, :d])
+        assert torch.equal(a.q, b.q) and torch.equal(a.scales, b.scales)
+        if res:
+            assert torch.equal(s[:T, :d], total)
