@@ -458,7 +458,8 @@ LORA_API int lora_merge_adapter(void *W, int64_t ld_w, int32_t d_out, int32_t d_
  *           columns have e = 0; bytes of rows past the last one are not used.
  * Both are aligned to LORA_MX_ALIGN bytes (LORA_ERR_ALIGN otherwise).  The calls below take the
  * device that is current, need no workspace and may be captured from the first call on.  Where a call takes a
- * row count T beside a matrix, it uses its rows 0..T-1 and leaves the others as they were.
+ * row count T beside a matrix, it uses its rows 0..T-1 and leaves the others as they were.  lora_rms_norm and
+ * lora_mx_linear take T up to LORA_MAX_ROWS (LORA_ERR_SHAPE beyond), the conversions up to the matrix's rows.
  */
 typedef enum { LORA_MXFP8 = 0, LORA_MXFP4 = 1 } lora_mx_format;
 
@@ -504,8 +505,9 @@ LORA_API int lora_mx_dequantize(void *out, int64_t ld_out, const lora_mx *q, int
  * residual and residual_out are both NULL (r = x) or both given, and may be the
  * same array.  h (the x of lora_add_linear) or q (the x of lora_mx_linear; q->cols = d) may
  * be NULL, not both; q is what lora_mx_quantize gives for h, whether h is stored or not.
- * h may be x itself; other outputs overlap nothing (h = residual_out: LORA_ERR_SHAPE).  Sums in fp32.  weight: [d],
- * eps >= 0.
+ * h may be x itself; other outputs overlap nothing (h = residual_out: LORA_ERR_SHAPE).  weight: [d], eps >= 0.  Squares and
+ * their sum in fp32: a finite row whose sum of squares passes fp32's largest number gives h = 0, one whose squares
+ * vanish is scaled by 1 / sqrt(eps).
  */
 LORA_API int lora_rms_norm(void *h, int64_t ld_h, const void *x, int64_t ld_x,
                            const void *residual, int64_t ld_r, void *residual_out, int64_t ld_ro,

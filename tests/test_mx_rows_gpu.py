@@ -353,3 +353,21 @@ def test_every_form_of_the_norm(cuda_lib, T, d, dtype, res):
         assert torch.equal(a.q, b.q) and torch.equal(a.scales, b.scales)
         if res:
             assert torch.equal(s[:T, :d], total)
+
+
+@pytest.mark.parametrize("d", [64, 77, 8200])
+def test_norm_of_rows_past_the_range_of_fp32_squares(cuda_lib, d):
+    """A finite row whose squares pass fp32's largest number gives zeros (no NaN); one whose squares vanish is scaled by
+    1 / sqrt(eps), which the formula gives too (mean r^2 of at most 1e-60 beside eps).  The sums are stored as ever."""
+    x = torch.ones(3, d, device="cuda")
+    x[0] *= 1e30
+    x[1] *= 1e-30
+    w, r = torch.full((d,), 2.0, device="cuda"), torch.zeros(3, d, device="cuda")
+    h, q = torch.empty_like(x), lora.MxTensor(3, d, lora.LORA_MXFP8)
+    lora.lora_rms_norm(h, x, w, 1e-5, residual=r, q=q)
+    assert (h[0] == 0).all() and torch.equal(r, x)
+    ref = as64(x[1:]) / np.sqrt((as64(x[1:]) ** 2).mean(1, keepdims=True) + 1e-5) * 2
+    assert (np.abs(as64(h[1:]) - ref) <= _norm_tol(ref, d, torch.float32)).all()
+    out = torch.empty_like(x)
+    lora.lora_mx_dequantize(out, q)
+    assert (out[0] == 0).all() and not torch.isnan(out).any()
