@@ -228,15 +228,17 @@ __device__ __forceinline__ void drain_ring(Ring r, uint32_t full) {
 // slots.  Roles: one warp copies W and its scales, one x and its, one issues MMAs, four move scales from
 // shared to tensor memory, eight take the finished
 // accumulator.  There are two: one tile's sums are stored while the next one's products go on; or, MT = 2, one for each
-// 128 features, which reads x once for both and may leave a block one tile in place of two (256 x 4096 x 14336 25.4 -> 20.5
+// 128 features, which reads x once for both and may leave a block one tile in place of two (256 x 4096 x 14336 22.3 -> 20.5
 // us; tiles of the height that spreads the features evenly over all SMs took the same time).  S > 1 only where every
 // cluster has one tile: its blocks then add their partial sums, in block order, through distributed shared memory: each owns
 // 1 / S of the rows, and gets the others' sums by plain stores between cluster barriers (st.async, which counts every
 // 16 bytes on a barrier, took 1.4 us per 16 rows).  They land behind the ring (few rows) or, once every
 // block's products are done, in it.
 //
-// Bound: W's bytes from HBM (64 rows, 4096 -> 28672: 66 MB in 18.5 us, 3.6 TB/s; x in MXFP4 15.2 us), or, per SM, filling
-// shared memory (257 x 14336 x 4096: 22.8 us).  What
+// Bound: from about 130 rows on, each SM's copies into shared memory (257 x 14336 x 4096 22.4 us: 34 KB of W and x per 128
+// columns).  For few rows not settled: 64 x 4096 x 28672 moves its 66 MB in 18.8 us (3.5 TB/s, 55 % of HBM's measured
+// rate), with x in MXFP4, when the same bytes of W arrive packed in place of 8-bit cells, in 15.7 (4.2).  HBM is not the
+// bound of the first; whether its 64-byte rows of W or the filling of the cells is was not separated.  What
 // a warp does per slot counts as much: a stage of the MMA warp with a barrier for each 128
 // columns and one for its scales took 1200 clocks per 256 columns, the products 320.
 // warp 0 copies W, 1 MMAs, 2-5 scales, 6-9 and 11-14 sums and stores (every other 16 rows), 10 copies x
@@ -570,10 +572,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 1) mx_linear_few_kernel(const __g
 // Blocks along k and clusters of them, by the time they would take: a scale tile of k costs a block `one`, bound by
 // its latency or its operands' way into shared memory, or `more` where every SM streams; an exchange of partial sums
 // 0.95 us for each doubling of S and 12 ns a row; all 3 us and 8 ns a row and accumulator besides.  Measured (us, S = 1, 2,
-// 4): 1 x 4096 x 4096 7.8, 6.0, 5.6; 64 x 4096 x 4096 9.0, 7.9, 7.3; 64 x 1024 x 4096 4.7, 5.4, 5.4;
-// 257 x 14336 x 4096 38.7, 24.6.  MT = 1 / 2, MXFP8: 1 x 4096 x 28672 16.0 / 16.5, 64 rows 19.1 / 19.2, 128 rows 25.1 / 23.2,
-// 256 x 4096 x 14336 25.4 / 20.5, 64 x 4096 x 50000 28.0 / 34.9; MXFP4: 15.4 / 14.1, 16.5 / 16.2, 18.1 / 17.9, 15.8 / 14.0,
-// 24.5 / 27.7.
+// 4): 1 x 4096 x 4096 7.7, 6.0, 5.5; 64 x 4096 x 4096 9.0, 7.9, 7.1; 64 x 1024 x 4096 4.7, 5.6, 5.4;
+// 257 x 14336 x 4096 25.7, 22.5.  MT = 1 / 2, MXFP8: 1 x 4096 x 28672 15.8 / 16.1, 64 rows 18.6 / 18.8, 128 rows 24.2 / 22.4,
+// 256 x 4096 x 14336 22.3 / 20.5, 64 x 4096 x 50000 27.3 / 34.2; MXFP4: 14.7 / 14.1, 16.0 / 15.6, 17.7 / 17.4, 15.0 / 13.9,
+// 23.5 / 26.9.
 struct FewPlan {
     int split_log2 = 0, clusters = 1;
     int64_t ns = 0;
@@ -645,7 +647,7 @@ struct FewShape {
     FewPlan plan;
 };
 // Scale tiles of a slot: two while three slots fit, else one (MXFP8: KT = 1 from 145 rows on; 257 x 14336 x 4096
-// 24.8 us with one, 22.5 with two).
+// 23.7 us with one, 22.3 with two).
 template <int KIND>
 constexpr int few_kt(bool wide, int mt) { return KIND == MX_A4 || (mt == 1 && !wide) ? 2 : 1; }
 inline bool few_wide(int bn) { return bn > 144; }
@@ -711,10 +713,10 @@ int launch_few(const MxLinArgs &l, const lora_mx *x, const lora_mx *w, int dev, 
 // tensor cores share the halves, so a block moves 32 KB of a stage for 256 x 256 x 32
 // bytes of products, half of what two 128 x 256 tiles would.  At the 4-bit rate that
 // is 64 bytes a clock and SM from L2: the reason for the pair.  8192 x 8192 x 28672 in 4 bits: 715 us (5.4 PFLOP/s) in a short
-// burst, 829 us steady at 1485 MHz under the power cap, 633 us on zeros.  Persistent: pair p
+// burst, 838 us steady at about 1500 MHz under the power cap, 657 us on zeros.  Persistent: pair p
 // takes tiles p, p + pairs, ... of bands of 16 x tiles, x's tiles fastest: concurrent pairs share W's rows and few enough
-// of x's to find both in the nearer half of L2 (8192 x 8192 x 28672 in MXFP8, steady 1650 -> 1510 us;
-// 8192 x 4096 x 4096 in MXFP4 66.6 -> 65.0).
+// of x's to find both in the nearer half of L2 (8192 x 8192 x 28672 in MXFP8, steady 1570 -> 1455 us;
+// 8192 x 4096 x 4096 in MXFP4 68.4 -> 66.0).
 // The fp32 accumulator (256 columns) is drained to registers by eight warps in one
 // go, the next tile's products start, and the rows are stored meanwhile.
 constexpr int BIG_THREADS = 448;      // warp 0 copies, warp 1 MMAs, warps 2-5 scales, warps 6-13 epilogue
@@ -1022,10 +1024,10 @@ int launch_big(const MxLinArgs &l, const lora_mx *x, const lora_mx *w, int sms, 
 }
 
 // Few rows or many, by the time each would take.  The pair kernel: 4.5 us, and per round of its 256 x 256 tiles 3.5 us
-// and 310 (MXFP8) or 165 ns a scale tile of k.  Measured, us few / many, MXFP8 then MXFP4: 128 x 4096 x 28672 24.9 / 31.6,
-// 18.4 / 23.8; 256 x 4096 x 28672 44.4 / 32.2, 27.1 / 24.3; 256 x 14336 x 4096 22.9 / 39.7, 15.8 / 23.9;
-// 512 x 14336 x 4096 43.2 / 40.4, 27.7 / 24.5; 768 x 4096 x 4096 15.9 / 17.4, 10.7 / 12.4; 1024 x 14336 x 1024 25.5 / 39.2,
-// 18.0 / 23.4.
+// and 310 (MXFP8) or 165 ns a scale tile of k.  Measured, us few / many, MXFP8 then MXFP4: 128 x 4096 x 28672 22.9 / 32.1,
+// 17.3 / 23.9; 256 x 4096 x 28672 38.5 / 32.3, 24.8 / 24.0; 256 x 14336 x 4096 21.7 / 39.1, 14.9 / 23.4;
+// 512 x 14336 x 4096 34.2 / 40.2, 20.6 / 24.1; 768 x 14336 x 4096 45.8 / 43.5 (few rows taken), 27.1 / 25.4;
+// 768 x 4096 x 4096 16.2 / 17.3, 10.8 / 12.2; 1024 x 14336 x 1024 21.0 / 38.8, 14.4 / 23.0.
 template <int KIND, typename Y>
 int launch_linear(const MxLinArgs &a, const lora_mx *x, const lora_mx *w, int dev, int sms, cudaStream_t st) {
     const int64_t tiles = (int64_t)((a.T + 255) / 256) * ((a.d_out + 255) / 256), pairs = std::max(1, sms / 2);

@@ -3,7 +3,7 @@
 // type and, optionally, microscaled.  Contracts: lora_delta.h.
 //
 // All three stream rows once and are bound by HBM: norm 8192 x 8192 bf16 with residual and MXFP8 copy 95 us (6.4 TB/s),
-// quantize 28672 x 8192 to MXFP4 91 us (6.6), dequantize 93 us (6.4); one row of 4096 2.2 us.  A lane holds 8 consecutive
+// quantize 28672 x 8192 to MXFP4 91 us (6.5), dequantize 92 us (6.4); one row of 4096 2.2 us.  A lane holds 8 consecutive
 // columns (one 16-byte bf16 access), so 4 lanes hold a scale's block of 32 and a
 // warp 256 columns = two scale tiles; the block's largest magnitude takes two
 // shuffles, the tile's four scale bytes two more.
