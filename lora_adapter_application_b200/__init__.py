@@ -546,6 +546,9 @@ class MxTensor:
     def __setattr__(self, name, value):
         raise LoraError("the fields of an MxTensor are fixed: make another one")
 
+    def __reduce__(self):   # copies and pickles have a struct of their own
+        return MxTensor, (self.rows, self.cols, self.fmt, self.q, self.scales)
+
     def __init__(self, rows, cols, fmt, q=None, scales=None, device=None):
         row_bytes, n_scales = lora_mx_row_bytes(fmt, cols), lora_mx_scale_bytes(rows, cols)
         if row_bytes == 0 or rows < 0 or (rows > 0 and n_scales == 0):

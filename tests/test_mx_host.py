@@ -240,3 +240,15 @@ def test_tensor_memory_is_fenced_after_every_wait():
     for u in uses:
         last = max((w for w in waits if w < u), default=None)
         assert last is None or "tc_fence_after();" in src[last:u], src[last:u]
+
+
+def test_mxtensor_copies(lib):
+    """copy.copy shares the tensors, deepcopy and pickle carry their contents; each has its own struct and addresses."""
+    import copy
+    import pickle
+    m = lora.MxTensor(5, 300, lora.LORA_MXFP4, device="cpu")
+    m.q.fill_(7)
+    for c, shared in ((copy.copy(m), True), (copy.deepcopy(m), False), (pickle.loads(pickle.dumps(m)), False)):
+        assert (c.rows, c.cols, c.fmt) == (5, 300, lora.LORA_MXFP4) and torch.equal(c.q, m.q)
+        assert (c.q.data_ptr() == m.q.data_ptr()) == shared and c.ref != m.ref
+        assert (c.c.q, c.c.scales) == (c.q.data_ptr(), c.scales.data_ptr())
