@@ -237,8 +237,8 @@ __device__ __forceinline__ void drain_ring(Ring r, uint32_t full) {
 //
 // Bound: from about 130 rows on, each SM's copies into shared memory (257 x 14336 x 4096 22.4 us: 34 KB of W and x per 128
 // columns).  For few rows not settled: 64 x 4096 x 28672 moves its 66 MB in 18.8 us (3.5 TB/s, 55 % of HBM's measured
-// rate), with x in MXFP4, when the same bytes of W arrive packed in place of 8-bit cells, in 15.7 (4.2).  HBM is not the
-// bound of the first; whether its 64-byte rows of W or the filling of the cells is was not separated.  What
+// rate), with x in MXFP4, when the same bytes of W arrive packed in place of 8-bit cells, in 15.7 (4.2).  So HBM is
+// not the bound of the first: its 64-byte rows of W are, or the filling of the cells (the two were not timed apart).  What
 // a warp does per slot counts as much: a stage of the MMA warp with a barrier for each 128
 // columns and one for its scales took 1200 clocks per 256 columns, the products 320.
 // warp 0 copies W, 1 MMAs, 2-5 scales, 6-9 and 11-14 sums and stores (every other 16 rows), 10 copies x
