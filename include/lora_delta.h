@@ -14,10 +14,10 @@
  * "LoRA service: multi-adapter dynamic loading", section 2: A_all
  * [N_adapters, r, d] plus a per-request adapter id; page "LoRA hot load and
  * adapter routing": per-request lora_ids where None means the base model).
- * The shared base product W x of dense weights is not part of this library: y
- * arrives holding it and leaves holding it plus the delta (merge step of the page
- * "Multi-LoRA Serving", section 2 flowchart: y_i = base_i + delta_i).  Over weights
- * held in microscaled 4-bit form lora_mx_linear computes it.
+ * y arrives holding the shared base product W x and leaves holding it plus the delta
+ * (merge step of the page "Multi-LoRA Serving", section 2 flowchart: y_i = base_i +
+ * delta_i).  lora_linear computes the base product over dense weights, lora_mx_linear over
+ * weights held in microscaled 4-bit form.
  *
  * Conventions for every entry point
  *   - Pointers named d_* or documented "device" are device memory owned by the
@@ -524,6 +524,86 @@ LORA_API int lora_rms_norm(void *h, int64_t ld_h, const void *x, int64_t ld_x,
  */
 LORA_API int lora_mx_linear(void *y, int64_t ld_y, const lora_mx *x, const lora_mx *w, int32_t T,
                             lora_dtype dtype, int32_t *status, void *stream);
+
+/*
+ * The same product over dense weights, with its epilogue.  No counterpart on the pages, which take W x from the
+ * serving engine: it is the `base` of their y_i = base_i + delta_i.
+ *     z[i][o] = sum_j x[i][j] w[o][j] + bias[o] + addend[i][o]            fp32, o < n_w
+ *     y[i][c] = act(z[i][c]) + residual[i][c]                             n_w = d_out
+ *     y[i][c] = act(z[i][c]) * z[i][d_out + c] + residual[i][c]           gated: n_w = 2 d_out
+ * with fp32 sums in a fixed order and one rounding into y.  The adapters' delta comes in as the addend, ahead of the
+ * activation (lora_add_linear into zeros), or as the residual, behind it.  act, z >= 0 or not, by its formula:
+ *     LORA_ACT_NONE z;  _SILU z / (1 + e^-z);  _GELU z erfc(-z / sqrt 2) / 2;
+ *     _GELU_TANH z / (1 + e^-2u), u = sqrt(2 / pi) (z + 0.044715 z^3);  _RELU 0 below 0, else z
+ * (-infinity gives NaN in all but NONE and RELU).  bf16 rows in steps of 16 bytes run on the tensor cores, others and
+ * fp32 on the ordinary units, with fp32 products.
+ */
+typedef enum { LORA_ACT_NONE = 0, LORA_ACT_SILU = 1, LORA_ACT_GELU = 2, LORA_ACT_GELU_TANH = 3, LORA_ACT_RELU = 4 } lora_act;
+
+typedef struct {
+    const void *bias;       /* [n_w] (lora_expert_linear: [N][n_w]), or NULL */
+    const void *addend;     /* [T][ld_addend], n_w columns used, or NULL */
+    int64_t ld_addend;
+    const void *residual;   /* [T][ld_residual], d_out columns used, or NULL */
+    int64_t ld_residual;
+    int32_t act;            /* lora_act */
+    int32_t gated;          /* 0 or 1 */
+} lora_epilogue;
+
+/*
+ * y ([T][ld_y], d_out columns written) from x ([T][ld_x], d_in columns used) and w ([n_w][ld_w]); all of one dtype.
+ * ep: host memory, NULL = a plain product.  y may be residual itself, or addend itself where not gated (of the same
+ * stride; LORA_ERR_SHAPE otherwise), and overlaps nothing else.  T up to LORA_MAX_ROWS, d_in and n_w up to LORA_MX_MAX.
+ * Needs no workspace, may be captured from the first call on.  status: device int32, receives LORA_DEV_TIMEOUT if a
+ * bounded wait ran out (the call's results are then unreliable).
+ */
+LORA_API int lora_linear(void *y, int64_t ld_y, const void *x, int64_t ld_x, const void *w, int64_t ld_w,
+                         int32_t T, int32_t d_in, int32_t d_out, const lora_epilogue *ep, lora_dtype dtype,
+                         int32_t *status, void *stream);
+
+/*
+ * A feed-forward block of experts: a token's row goes through the k experts that a router chose for it.  Its slots are
+ * grouped by expert as rows are by adapter: ids [T * k], slot t * k + j token t's j-th expert or -1, and a lora_meta of
+ * T * k rows over N experts that lora_build_segments filled from them (any rows_per_tile, min_run).
+ *     lora_expert_route(ids, weights, logits, ...)        the choice
+ *     lora_build_segments(ids, &meta, ...)
+ *     lora_expert_linear(h, x, x_div = k, gated)          gate and up of every slot
+ *     lora_expert_linear(z, h, x_div = 1)                 down
+ *     lora_expert_sum(y, z, ids, weights, residual)       back to the tokens
+ */
+#define LORA_MAX_EXPERTS 1024
+#define LORA_MAX_TOPK      32
+
+typedef enum { LORA_SCORE_SOFTMAX = 0, LORA_SCORE_SIGMOID = 1 } lora_score;
+
+/*
+ * The k largest of a token's n_experts logits ([T][ld], bf16 or fp32), in falling order, ties to the lowest expert:
+ * ids [T][k] and weights [T][k] (fp32).  A weight is the logit's softmax over all experts, or its sigmoid;
+ * renormalize: over the sum of the token's weights; then times scale.  Logits of -infinity or NaN count as closed
+ * experts: never chosen, no part in the softmax; where fewer than k are open, the rest are id -1 and weight 0.
+ * Experts at +infinity share a softmax among them.  1 <= k <= min(n_experts, LORA_MAX_TOPK).
+ */
+LORA_API int lora_expert_route(int32_t *ids, float *weights, const void *logits, int64_t ld, int32_t T,
+                               int32_t n_experts, int32_t k, int32_t score, int32_t renormalize, float scale,
+                               lora_dtype dtype, void *stream);
+
+/*
+ * lora_linear per slot: for every slot i of an expert e (meta's grouping), row i of y (and of addend and residual) from
+ * row i / x_div of x through w[e] ([N][n_w][d_in]) and bias[e].  Rows of y of slots without an expert are left as they
+ * were.  x has x_rows >= ceil(meta->T / x_div) rows.  meta->N up to LORA_MAX_EXPERTS.  The rest as lora_linear.
+ */
+LORA_API int lora_expert_linear(void *y, int64_t ld_y, const void *x, int64_t ld_x, int32_t x_rows, int32_t x_div,
+                                const void *w, int32_t d_in, int32_t d_out, const lora_meta *meta,
+                                const lora_epilogue *ep, lora_dtype dtype, int32_t *status, void *stream);
+
+/*
+ * y[t][c] = residual[t][c] + sum_{j < k} weights[t][j] * x[t * k + j][c] for t < T, c < d, over the slots whose id is in
+ * [0, n_experts) (the rows of the others are not read), fp32 in slot order, one rounding.  residual may be NULL, or y
+ * itself of the same stride; y overlaps nothing else.
+ */
+LORA_API int lora_expert_sum(void *y, int64_t ld_y, const void *x, int64_t ld_x, const int32_t *ids,
+                             const float *weights, int32_t n_experts, int32_t T, int32_t k, int32_t d,
+                             const void *residual, int64_t ld_r, lora_dtype dtype, void *stream);
 
 #ifdef __cplusplus
 }

@@ -33,6 +33,8 @@ __all__ = [
     "lora_slot_cache_key", "lora_slot_cache_evict", "lora_merge_adapter", "lora_segment_plan",
     "LORA_MXFP8", "LORA_MXFP4", "MxTensor", "lora_mx_row_bytes", "lora_mx_scale_bytes",
     "lora_mx_quantize", "lora_mx_dequantize", "lora_rms_norm", "lora_mx_linear",
+    "ACT_NONE", "ACT_SILU", "ACT_GELU", "ACT_GELU_TANH", "ACT_RELU", "lora_linear",
+    "SCORE_SOFTMAX", "SCORE_SIGMOID", "lora_expert_route", "lora_expert_linear", "lora_expert_sum",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -45,6 +47,9 @@ ERR_CUDA = -8   # LORA_ERR_CUDA
 MAX_ROWS, MAX_ADAPTERS, MAX_RANK, MAX_SLICES, LONG_TILE = 131072, 4096, 128, 8, 128
 MAX_TILE_ROWS = 64
 MX_MAX = 1048576   # LORA_MX_MAX: rows, columns of a microscaled matrix
+ACT_NONE, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU = range(5)
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+MAX_EXPERTS, MAX_TOPK = 1024, 32
 
 _P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
@@ -62,6 +67,11 @@ class lora_slice(ctypes.Structure):
 
 class lora_mx(ctypes.Structure):
     _fields_ = [("q", _P), ("scales", _P), ("rows", _I32), ("cols", _I32), ("format", _I32)]
+
+
+class lora_epilogue(ctypes.Structure):
+    _fields_ = [("bias", _P), ("addend", _P), ("ld_addend", _I64), ("residual", _P), ("ld_residual", _I64),
+                ("act", _I32), ("gated", _I32)]
 
 
 class LoraError(RuntimeError):
@@ -106,6 +116,13 @@ _SIGS = {
     "lora_rms_norm": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, ctypes.c_float, _I32,
                                      _I32, _P, ctypes.c_int, _P]),
     "lora_mx_linear": (ctypes.c_int, [_P, _I64, _P, _P, _I32, ctypes.c_int, _P, _P]),
+    "lora_linear": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _I32, _I32, _I32, _P, ctypes.c_int, _P, _P]),
+    "lora_expert_route": (ctypes.c_int, [_P, _P, _P, _I64, _I32, _I32, _I32, _I32, _I32, ctypes.c_float,
+                                         ctypes.c_int, _P]),
+    "lora_expert_linear": (ctypes.c_int, [_P, _I64, _P, _I64, _I32, _I32, _P, _I32, _I32, ctypes.POINTER(lora_meta), _P,
+                                          ctypes.c_int, _P, _P]),
+    "lora_expert_sum": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _I32, _I32, _I32, _I32, _P, _I64, ctypes.c_int,
+                                       _P]),
     "lora_slot_cache_create": (_P, [_I32]),
     "lora_slot_cache_destroy": (None, [_P]),
     "lora_slot_cache_acquire": (ctypes.c_int, [_P, _I64, ctypes.POINTER(_I32), ctypes.POINTER(_I32)]),
@@ -717,3 +734,132 @@ def lora_mx_linear(y, x, w, status, stream=None):
         raise LoraError("status must be an int32 tensor")
     _call_on(x.index, stream, (_lib or load()).lora_mx_linear, _cuda_on(y, "y", x.index), ld, x.ref, w.ref, T,
              _dtype_of(y), _cuda_on(status, "status", x.index))
+
+
+# ---------------------------------------------------------------- dense base, experts
+def _operand(t, what, n, d, index, dtype):
+    """(address, row stride) of an operand that must be [n, d] of x's dtype on CUDA device `index`."""
+    if not isinstance(t, torch.Tensor) or t.shape != (n, d) or t.dtype is not dtype:
+        raise LoraError(f"{what} must be [{n}, {d}] of x's dtype {dtype}")
+    _, _, ld = _matrix(t, what)
+    if t.get_device() != index:
+        raise LoraError(f"{what} must be on cuda:{index}")
+    return t.data_ptr(), ld
+
+
+def _epilogue(T, n_w, n, index, dtype, bias, bias_shape, addend, residual, act, gated):
+    """(address, owner) of the call's lora_epilogue."""
+    if act not in (ACT_NONE, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU):
+        raise LoraError("act is one of ACT_NONE, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU")
+    ep = lora_epilogue(None, None, 0, None, 0, act, 1 if gated else 0)
+    if bias is not None:
+        if not isinstance(bias, torch.Tensor) or bias.shape != bias_shape or bias.dtype is not dtype or \
+                not bias.is_contiguous():
+            raise LoraError(f"bias must be contiguous {list(bias_shape)} of x's dtype")
+        ep.bias = _cuda_on(bias, "bias", index)
+    if addend is not None:
+        ep.addend, ep.ld_addend = _operand(addend, "addend", T, n_w, index, dtype)
+    if residual is not None:
+        ep.residual, ep.ld_residual = _operand(residual, "residual", T, n, index, dtype)
+    return ctypes.addressof(ep), ep
+
+
+def _status_on(status, index):
+    if not isinstance(status, torch.Tensor) or status.dtype != torch.int32 or status.numel() < 1:
+        raise LoraError("status must be an int32 tensor")
+    return _cuda_on(status, "status", index)
+
+
+def lora_linear(y, x, w, status, bias=None, addend=None, residual=None, act=ACT_NONE, gated=False, stream=None):
+    """y [T, n] = act(z) + residual, z = x w^T + bias + addend (x [T, d], w [n, d]); gated: w, bias and addend have 2n
+    rows or columns, the gate's n first, and y = act(z[:, :n]) * z[:, n:] + residual.  One dtype, bf16 or fp32.  y may be
+    residual, or addend where not gated."""
+    T, d, ld_x = _matrix(x, "x")
+    n_w, dw, ld_w = _matrix(w, "w")
+    if T > MAX_ROWS or d > MX_MAX or n_w > MX_MAX or d < 1 or n_w < 1:
+        raise LoraError(f"x has at most {MAX_ROWS} rows, x and w 1 to {MX_MAX} columns, w 1 to {MX_MAX} rows")
+    if dw != d or w.dtype is not x.dtype or (gated and n_w & 1):
+        raise LoraError(f"w must be [n, {d}] of x's dtype, n even where gated")
+    if not x.is_cuda:
+        raise LoraError("x must be a CUDA tensor")
+    code, index, dtype = _dtype_of(x), x.get_device(), x.dtype
+    n = n_w // 2 if gated else n_w
+    py, ld_y = _operand(y, "y", T, n, index, dtype)
+    at = own = None
+    if bias is not None or addend is not None or residual is not None or act or gated:
+        at, own = _epilogue(T, n_w, n, index, dtype, bias, (n_w,), addend, residual, act, gated)
+    _call_on(index, stream, (_lib or load()).lora_linear, py, ld_y, x.data_ptr(), ld_x, _cuda_on(w, "w", index), ld_w, T, d,
+             n, at, code, _status_on(status, index))
+
+
+def lora_expert_linear(y, x, w, meta: Meta, status, x_div=1, bias=None, addend=None, residual=None, act=ACT_NONE,
+                       gated=False, stream=None):
+    """lora_linear of every slot with an expert: row i of y [slots, n] from row i // x_div of x through w[e] of w
+    [N, n (gated: 2n), d] and bias[e] of bias [N, n (2n)]; meta: lora_build_segments of the slots' expert ids (T =
+    slots).  Rows of slots without an expert are left as they were."""
+    R, d, ld_x = _matrix(x, "x")
+    if not isinstance(w, torch.Tensor) or w.dim() != 3 or not w.is_contiguous() or w.dtype is not x.dtype or \
+            w.shape[0] != meta.N or w.shape[2] != d or (gated and w.shape[1] & 1):
+        raise LoraError(f"w must be contiguous [{meta.N}, n, {d}] of x's dtype, n even where gated")
+    n_w = w.shape[1]
+    if R > MX_MAX or d > MX_MAX or n_w > MX_MAX or d < 1 or n_w < 1 or meta.N > MAX_EXPERTS:
+        raise LoraError(f"at most {MX_MAX} rows of x, 1 to {MX_MAX} columns and rows of w, {MAX_EXPERTS} experts")
+    if not 1 <= x_div <= MAX_ROWS or R * x_div < meta.T:
+        raise LoraError("x must hold a row for every slot: ceil(slots / x_div)")
+    if not x.is_cuda:
+        raise LoraError("x must be a CUDA tensor")
+    code, index, dtype = _dtype_of(x), x.get_device(), x.dtype
+    if meta.perm.get_device() != index:
+        raise LoraError(f"meta must be on cuda:{index}")
+    n = n_w // 2 if gated else n_w
+    py, ld_y = _operand(y, "y", meta.T, n, index, dtype)
+    at = own = None
+    if bias is not None or addend is not None or residual is not None or act or gated:
+        at, own = _epilogue(meta.T, n_w, n, index, dtype, bias, (meta.N, n_w), addend, residual, act, gated)
+    _call_on(index, stream, (_lib or load()).lora_expert_linear, py, ld_y, x.data_ptr(), ld_x, R, x_div,
+             _cuda_on(w, "w", index), d, n, ctypes.byref(meta.c), at, code, _status_on(status, index))
+
+
+def _choices(t, what, T, k, dtype, index):
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_contiguous() or t.numel() != T * k:
+        raise LoraError(f"{what} must be contiguous [{T}, {k}] of {dtype}")
+    return _cuda_on(t, what, index)
+
+
+def lora_expert_route(ids, weights, logits, score=SCORE_SOFTMAX, renormalize=True, scale=1.0, stream=None):
+    """The k largest of each token's logits [T, N] (bf16 or fp32): ids int32 [T, k], in falling order, ties to the
+    lowest expert, and weights fp32 [T, k]: softmax over all experts or sigmoid, over the token's sum where
+    renormalize, times scale.  -infinity and NaN close an expert; id -1 and weight 0 where fewer than k are open."""
+    T, n, ld = _matrix(logits, "logits")
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or ids.shape[0] != T:
+        raise LoraError(f"ids must be [{T}, k]")
+    k = ids.shape[1]
+    if T > MAX_ROWS or not 1 <= n <= MAX_EXPERTS or not 1 <= k <= min(n, MAX_TOPK):
+        raise LoraError(f"at most {MAX_ROWS} tokens, {MAX_EXPERTS} experts, k of 1 to {MAX_TOPK} and at most the experts")
+    if score not in (SCORE_SOFTMAX, SCORE_SIGMOID):
+        raise LoraError("score is SCORE_SOFTMAX or SCORE_SIGMOID")
+    if not logits.is_cuda:
+        raise LoraError("logits must be a CUDA tensor")
+    index = logits.get_device()
+    _call_on(index, stream, (_lib or load()).lora_expert_route, _choices(ids, "ids", T, k, torch.int32, index),
+             _choices(weights, "weights", T, k, torch.float32, index), logits.data_ptr(), ld, T, n, k, score,
+             1 if renormalize else 0, float(scale), _dtype_of(logits))
+
+
+def lora_expert_sum(y, x, ids, weights, n_experts, residual=None, stream=None):
+    """y [T, d] = residual + the weighted rows of each token's k slots: x [T k, d], ids int32 and weights fp32 [T, k];
+    slots whose id is outside [0, n_experts) are left out.  y may be residual."""
+    T, d, ld_y = _matrix(y, "y")
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or ids.shape[0] != T:
+        raise LoraError(f"ids must be [{T}, k]")
+    k = ids.shape[1]
+    if T > MAX_ROWS or not 1 <= d <= MX_MAX or not 1 <= k <= MAX_TOPK or not 1 <= n_experts <= MAX_EXPERTS:
+        raise LoraError(f"at most {MAX_ROWS} tokens, 1 to {MX_MAX} columns, {MAX_TOPK} slots a token, {MAX_EXPERTS} experts")
+    if not y.is_cuda:
+        raise LoraError("y must be a CUDA tensor")
+    code, index, dtype = _dtype_of(y), y.get_device(), y.dtype
+    px, ld_x = _operand(x, "x", T * k, d, index, dtype)
+    pr, ld_r = (None, 0) if residual is None else _operand(residual, "residual", T, d, index, dtype)
+    _call_on(index, stream, (_lib or load()).lora_expert_sum, y.data_ptr(), ld_y, px, ld_x,
+             _choices(ids, "ids", T, k, torch.int32, index), _choices(weights, "weights", T, k, torch.float32, index),
+             n_experts, T, k, d, pr, ld_r, code)

@@ -1,0 +1,97 @@
+// What the dense products share (lora_linear, lora_expert_linear): the call's
+// parameters, the epilogue's arithmetic and the way from a row tile to its expert.
+#pragma once
+
+#include "mx.cuh"
+
+namespace lora {
+
+// A call, as the kernels take it.  Rows: of a plain product, 0..T-1 of x and y.  Of the experts', position q of the grouping
+// is slot perm[q] (a row of y) and row perm[q] / x_div of x; expert e has positions seg_start[e] .. seg_start[e + 1] - 1.
+struct LinArgs {
+    void *y;
+    const void *x, *w;
+    const void *bias, *addend, *residual;   // NULL: none
+    int64_t ld_y, ld_x, ld_w, ld_a, ld_r;
+    int T, d_in, d_out;   // d_out: columns of y; W has n_w rows (gated: the gate's d_out, then the up projection's)
+    int n_w;
+    int act;
+    const int32_t *perm, *seg_start;   // experts, else NULL
+    int N, x_div;
+    int32_t *status;
+};
+
+// ------------------------------------------------------------------ epilogue
+// silu and both gelus as quotients or products without cancellation: z / (1 + e^-z) and z erfc(-z / sqrt 2) / 2 keep their
+// relative accuracy where z is far below 0, which z (1 + erf) / 2 and z (1 + tanh) / 2 lose.
+// FAST (results rounded to bf16): __expf and __fdividef, about 2^-20 relative at |z| <= 20, far below bf16's 2^-9; for
+// fp32 results the accurate functions.
+template <bool FAST>
+__device__ __forceinline__ float over_one_plus_exp(float z, float u) {   // z / (1 + e^-u)
+    return FAST ? __fdividef(z, 1.f + __expf(-u)) : z / (1.f + expf(-u));
+}
+template <bool FAST, int N>
+__device__ __forceinline__ void activate(int act, float *z) {
+    switch (act) {
+        case LORA_ACT_SILU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) z[i] = over_one_plus_exp<FAST>(z[i], z[i]);
+            break;
+        case LORA_ACT_GELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) z[i] = 0.5f * z[i] * erfcf(-0.70710678118654752f * z[i]);
+            break;
+        case LORA_ACT_GELU_TANH:   // (1 + tanh u) / 2 = 1 / (1 + e^-2u), u = sqrt(2 / pi) (z + 0.044715 z^3)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                z[i] = over_one_plus_exp<FAST>(z[i], 1.5957691216057308f * (z[i] + 0.044715f * z[i] * z[i] * z[i]));
+            break;
+        case LORA_ACT_RELU:
+#pragma unroll
+            for (int i = 0; i < N; ++i) z[i] = z[i] < 0.f ? 0.f : z[i];   // NaN stays
+            break;
+        default: break;
+    }
+}
+
+// ------------------------------------------------------------------ experts
+// Row tiles (rows positions each) of experts before e, for e in 0..N, to pre[0..N] in shared memory, by a whole block;
+// part: 32 words of shared memory.  Ends with the block's barrier.
+__device__ __forceinline__ void count_tiles(const int32_t *seg_start, int N, int rows, int *pre, int *part) {
+    const int per = (N + (int)blockDim.x - 1) / (int)blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lo = min(N, (int)threadIdx.x * per), hi = min(N, lo + per);
+    int sum = 0;
+    for (int e = lo; e < hi; ++e) sum += (seg_start[e + 1] - seg_start[e] + rows - 1) / rows;
+    int up = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const int v = __shfl_up_sync(FULL, up, d);
+        if (lane >= d) up += v;
+    }
+    if (lane == 31) part[warp] = up;
+    __syncthreads();
+    int at = up - sum;
+    for (int w = 0; w < warp; ++w) at += part[w];
+    if (threadIdx.x == 0) pre[0] = 0;
+    for (int e = lo; e < hi; ++e) {
+        at += (seg_start[e + 1] - seg_start[e] + rows - 1) / rows;
+        pre[e + 1] = at;
+    }
+    __syncthreads();
+}
+// The expert of row tile t: the last e with pre[e] <= t (t < pre[N]).
+__device__ __forceinline__ int expert_of(const int *pre, int N, int t) {
+    int lo = 0, hi = N;   // pre[lo] <= t < pre[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (pre[mid] <= t) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+constexpr int MAX_EXPERTS = LORA_MAX_EXPERTS;
+
+// linear_simt.cu: any type, stride and alignment
+int launch_linear_simt(const LinArgs &a, bool bf16, bool gated, int sms, cudaStream_t st);
+
+}  // namespace lora
