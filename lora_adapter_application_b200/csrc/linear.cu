@@ -27,11 +27,12 @@ int check_dense(LinArgs &a, const lora_epilogue *ep, lora_dtype dtype) {
     return LORA_OK;
 }
 
-int launch_dense(const LinArgs &a, bool gated, lora_dtype dtype, cudaStream_t st) {
+int launch_dense(const LinArgs &a, int64_t x_rows, bool gated, lora_dtype dtype, cudaStream_t st) {
     int dev = 0, sms = 148;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return cuda_rc(e);
+    if (dtype == LORA_BF16 && linear_tc_ok(a, x_rows)) return launch_linear_tc(a, x_rows, gated, dev, sms, st);
     return launch_linear_simt(a, dtype == LORA_BF16, gated, sms, st);
 }
 
@@ -50,7 +51,7 @@ int lora_linear(void *y, int64_t ld_y, const void *x, int64_t ld_x, const void *
     a.T = T, a.d_in = d_in, a.d_out = d_out, a.status = status, a.N = 1, a.x_div = 1;
     const int rc = check_dense(a, ep, dtype);
     if (rc != LORA_OK || T == 0) return rc;
-    return launch_dense(a, ep && ep->gated, dtype, static_cast<cudaStream_t>(stream));
+    return launch_dense(a, T, ep && ep->gated, dtype, static_cast<cudaStream_t>(stream));
 }
 
 int lora_expert_linear(void *y, int64_t ld_y, const void *x, int64_t ld_x, int32_t x_rows, int32_t x_div, const void *w,
@@ -66,7 +67,7 @@ int lora_expert_linear(void *y, int64_t ld_y, const void *x, int64_t ld_x, int32
     a.perm = meta->perm, a.seg_start = meta->seg_start, a.N = meta->N, a.x_div = x_div;
     rc = check_dense(a, ep, dtype);
     if (rc != LORA_OK || a.T == 0) return rc;
-    return launch_dense(a, ep && ep->gated, dtype, static_cast<cudaStream_t>(stream));
+    return launch_dense(a, x_rows, ep && ep->gated, dtype, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,522 @@
+// The dense products on the 5th-generation tensor cores (contract: lora_linear and lora_expert_linear in
+// lora_delta.h): bf16 operands, fp32 sums in tensor memory.
+//
+// W's rows are the MMA's M side: a pair of blocks (cta_group::2) takes 256 features, each block loading its own 128; the
+// rows of x are the N side, any multiple of 32 up to 256, each block loading half.  So a decode batch reads W once and
+// computes no more than it must, a group of an expert's rows wastes at most 31 of a tile, and many rows get 256 x 256
+// tiles, 64 bytes a clock and SM of operands at full rate.  MT = 2: two such feature blocks on one x tile: the gate's and
+// the up projection's columns of a gated product, which then meet in one thread, or twice the features.
+//
+// One persistent kernel for all sizes.  Tile t of cluster c: t = c, c + clusters, ....  Few tiles: a cluster is S pairs that
+// split k, each cluster has one tile, and its blocks add their sums, in rank order, through distributed shared memory.
+//
+// Warp 0 copies W's boxes (and x's, plain product) by TMA; warp 1 of the first block of a pair issues the MMAs; eight warps
+// read the accumulators (lane = feature, column = row of x), apply the epilogue and store.  Experts (GATHER): four more
+// warps copy the group's rows of x, wherever they lie, with cp.async into the same swizzle, 16 bytes a lane (gather4
+// copies of four rows x 128 bytes would be 32 a stage; a TMA copy costs its warp 40-60 ns); they count on the block's own
+// barrier, and warp 1 of the second block passes the word on to the first.
+#include "linear.cuh"
+#include "pipe.cuh"
+
+#include <algorithm>
+#include <cstdlib>
+#include <mutex>
+
+namespace lora {
+
+namespace {
+
+constexpr int PAIR_STAGES = 12;
+constexpr int PAIR_ROWS = 256;    // widest tile of x rows
+constexpr int EPI_WARPS = 8, GATHER_WARPS = 4;
+template <bool GATHER>
+constexpr int pair_threads() { return 32 * (2 + EPI_WARPS + (GATHER ? GATHER_WARPS : 0)); }
+// dynamic shared memory, all that the experts' table of 4 KB or the barriers leave: one block an SM, as its tensor memory asks for
+template <bool GATHER>
+constexpr size_t pair_smem() { return (GATHER ? 221 : 226) * 1024; }
+enum { STALL_MMA = 1, STALL_ROWS = 2, STALL_COPY = 3, STALL_SUMS = 4, STALL_COPY_FIRST = 5 };   // LORA_DEBUG_STALL
+
+struct PairArgs {
+    CUtensorMap tmW, tmX;
+    LinArgs l;
+    int gated;
+    int up;              // rows of W between a tile's two feature blocks
+    int bn;              // rows of a tile
+    int m_tiles, n_tiles;   // tiles along the features; along x (plain product)
+    int n_k;             // 64-column steps of k
+    int stages, bufs;    // ring slots, accumulator buffers
+    int split_log2;      // S
+    int own_red;         // the partial sums' place is behind the ring
+    unsigned limit;
+    int stall;
+};
+
+// Instruction descriptor: as idesc_bf16, with N known at run time
+__device__ __forceinline__ uint32_t pair_idesc(int N) { return idesc_bf16(256, 8) - (1u << 17) + ((uint32_t)(N >> 3) << 17); }
+__device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// 16 bytes, or zeros where bytes is 0
+__device__ __forceinline__ void cp_async16z(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// arrival on a barrier of another block of the cluster; what this thread has seen and fenced is visible to who waits there
+__device__ __forceinline__ void mbar_arrive_release(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+
+// A tile: its features from m0 (MT blocks of 256), its rows q0 .. q0 + cnt - 1 of expert e, n = rows of the MMA.
+struct Tile {
+    int m0, e, q0, cnt, n;
+};
+
+// Rows of a block in the exchange of partial sums: a power of two up to 16, or a multiple of 16, so that 16 rows' owners
+// follow from shifts or are one.
+__host__ __device__ __forceinline__ int own_rows(int rows, int split_log2) {
+    const int fair = (rows + (1 << split_log2) - 1) >> split_log2;
+    if (fair > 16) return (fair + 15) & ~15;
+    int own = 1;
+    while (own < fair) own *= 2;
+    return own;
+}
+
+template <bool GATHER, int MT>
+__global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(const __grid_constant__ PairArgs a) {
+    extern __shared__ __align__(1024) unsigned char lin_sm[];
+    __shared__ uint32_t tmem_sm;
+    __shared__ __align__(8) uint64_t bars[4 * PAIR_STAGES + 5];
+    __shared__ uint32_t stop_sm, used_sm;   // used_sm: ring uses that this block's copies have begun
+    __shared__ int pre[GATHER ? MAX_EXPERTS + 1 : 1], part[GATHER ? 32 : 1];
+    constexpr int FIRST_EPI = GATHER ? 2 + GATHER_WARPS : 2;
+    const int warp = __shfl_sync(FULL, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const uint32_t w_bytes = 16384u * MT, slot_bytes = w_bytes + 64u * (uint32_t)a.bn;
+    const uint32_t base = (smem_u32(lin_sm) + 1023u) & ~1023u, red = base + (a.own_red ? (uint32_t)a.stages * slot_bytes : 0u);
+    const int rank = (int)cluster_rank(), S = 1 << a.split_log2;
+    const uint32_t half = rank & 1, first = rank & ~1;   // this block of the pair; the pair's first block
+    const int cluster = (int)blockIdx.x >> (a.split_log2 + 1), clusters = (int)gridDim.x >> (a.split_log2 + 1);
+    const int k_lo = a.n_k * (rank >> 1) >> a.split_log2, k_hi = a.n_k * ((rank >> 1) + 1) >> a.split_log2;
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    auto full = [&](int s) { return bar(s); };                       // the first block's counts both blocks' TMA bytes
+    auto empty = [&](int s) { return bar(PAIR_STAGES + s); };
+    auto rows_in = [&](int s) { return bar(2 * PAIR_STAGES + s); };      // this block's gathered rows
+    auto peer_rows = [&](int s) { return bar(3 * PAIR_STAGES + s); };    // the first block's: the second's have landed too
+    auto acc_full = [&](int b) { return bar(4 * PAIR_STAGES + b); };
+    auto acc_empty = [&](int b) { return bar(4 * PAIR_STAGES + 2 + b); };   // the first block's: eight warps of each block
+    const uint32_t rest = bar(4 * PAIR_STAGES + 4);   // completes in the teardown after a wait that ran out, else never
+    const Bound bound{smem_u32(&stop_sm), a.limit, a.l.status};
+    bool failed = false;
+
+    if (warp == 0) {
+        for (int i = lane; i < 4 * PAIR_STAGES + 5; i += 32) {
+            const bool rows = i >= 2 * PAIR_STAGES && i < 3 * PAIR_STAGES, drained = i >= 4 * PAIR_STAGES + 2 && i < 4 * PAIR_STAGES + 4;
+            mbar_init(bar(i), rows ? 32 * GATHER_WARPS : drained ? 2 * EPI_WARPS : 1);
+        }
+        if (lane == 0) {
+            stop_sm = 0, used_sm = 0;
+            prefetch_tmap(&a.tmW);
+            if (!GATHER) prefetch_tmap(&a.tmX);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&tmem_sm)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();   // every block's barriers and tensor memory are ready
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(FULL, tmem_sm, 0);
+    pdl_next();
+    pdl_wait();   // all warps: none of the bounded waits below runs while the kernel before this one does
+    int tiles = a.m_tiles * a.n_tiles;
+    if (GATHER) {
+        count_tiles(a.l.seg_start, a.l.N, a.bn, pre, part);
+        tiles = a.m_tiles * pre[a.l.N];
+    }
+
+    // Tiles run along x first: pairs at work at the same time share W's rows (and, in bands of 16 tiles of x, few enough
+    // rows of x to find both in L2).
+    auto place = [&](int t) {
+        Tile p;
+        int mi, rows;
+        if (GATHER) {
+            p.e = expert_of(pre, a.l.N, t / a.m_tiles);
+            const int n = pre[p.e + 1] - pre[p.e], left = t - pre[p.e] * a.m_tiles;
+            mi = left / n;
+            p.q0 = a.l.seg_start[p.e] + (left - mi * n) * a.bn;
+            rows = a.l.seg_start[p.e + 1];
+        } else {
+            constexpr int BAND = 16;
+            const int per = BAND * a.m_tiles, band = t / per, left = t - band * per, high = min(BAND, a.n_tiles - band * BAND);
+            mi = left / high;
+            p.e = 0;
+            p.q0 = (band * BAND + left - mi * high) * a.bn;
+            rows = a.l.T;
+        }
+        p.cnt = min(a.bn, rows - p.q0);
+        p.n = (p.cnt + 31) & ~31;
+        p.m0 = mi * (a.gated ? 256 : 256 * MT);
+        return p;
+    };
+    const uint32_t tx = 2u * (w_bytes + (GATHER ? 0u : 64u * (uint32_t)a.bn));
+
+    if (warp == 0) {
+        Ring ring(a.stages);
+        if (a.stall == (half ? STALL_COPY : STALL_COPY_FIRST)) uniform_wait(rest, 0, bound, failed);
+        for (int t = cluster; t < tiles && !failed; t += clusters) {
+            const Tile p = place(t);
+            const int w0 = p.e * a.l.n_w + p.m0 + 128 * (int)half, x0 = p.q0 + (int)half * (p.n >> 1);
+            for (int k = k_lo; k < k_hi; ++k, ring.next()) {
+                if (ring.reused() && !uniform_wait(empty(ring.slot), ring.parity ^ 1u, bound, failed)) break;
+                const uint32_t slot = base + (uint32_t)ring.slot * slot_bytes, b = map_rank(full(ring.slot), first);
+                if (elect_one()) {
+                    if (half == 0) mbar_expect_tx(full(ring.slot), tx);
+#pragma unroll
+                    for (int u = 0; u < MT; ++u) tma_2d_pair(slot + 16384u * u, &a.tmW, 64 * k, w0 + u * a.up, b);
+                    if (!GATHER) tma_2d_pair(slot + w_bytes, &a.tmX, 64 * k, x0, b);
+                }
+            }
+        }
+        if (elect_one()) used_sm = ring.uses;
+    } else if (warp == 1) {
+        if (half == 0) {
+            Ring ring(a.stages);
+            int n = 0;
+            if (a.stall == STALL_MMA) uniform_wait(rest, 0, bound, failed);
+            for (int t = cluster; t < tiles && !failed; t += clusters, ++n) {
+                const Tile p = place(t);
+                const int b = a.bufs == 2 ? n & 1 : 0, uses = a.bufs == 2 ? n >> 1 : n;
+                if (uses > 0 && !uniform_wait(acc_empty(b), (unsigned)(uses - 1) & 1u, bound, failed)) break;
+                tc_fence_after();
+                const uint32_t d = tmem + (uint32_t)(b * MT * a.bn), idesc = pair_idesc(p.n);
+                for (int k = k_lo; k < k_hi; ++k, ring.next()) {
+                    const int s = ring.slot;
+                    if (!uniform_wait(full(s), ring.parity, bound, failed)) break;
+                    if (GATHER) {
+                        if (!uniform_wait(rows_in(s), ring.parity, bound, failed)) break;
+                        bool ok = false;   // the second block's word: acquire its rows
+                        for (unsigned it = 0; it < bound.limit && !ok && !__any_sync(FULL, stopped(bound.stop)); ++it)
+                            ok = __all_sync(FULL, mbar_try<true>(peer_rows(s), ring.parity));
+                        if (!ok) {
+                            failed = true;
+                            break;
+                        }
+                    }
+                    tc_fence_after();
+                    const uint32_t slot = base + (uint32_t)s * slot_bytes;
+                    if (elect_one()) {
+                        if (GATHER) fence_proxy_async();   // rows came by cp.async (generic proxy), the MMA reads them as operands
+                        const uint64_t dx = desc_sw128(slot + w_bytes);
+#pragma unroll
+                        for (int u = 0; u < MT; ++u) {
+                            const uint64_t dw = desc_sw128(slot + 16384u * u);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                pair_mma(d + (uint32_t)(u * a.bn), dw + 2 * i, dx + 2 * i, idesc, k == k_lo && i == 0 ? 0u : 1u);
+                        }
+                        tc_commit_pair(empty(s), first);
+                    }
+                }
+                if (elect_one()) tc_commit_pair(acc_full(b), first);
+            }
+        } else if (GATHER) {
+            Ring ring(a.stages);
+            for (int t = cluster; t < tiles && !failed; t += clusters)
+                for (int k = k_lo; k < k_hi; ++k, ring.next()) {
+                    if (!uniform_wait(rows_in(ring.slot), ring.parity, bound, failed)) break;
+                    if (elect_one()) {
+                        fence_proxy_async();
+                        mbar_arrive_release(map_rank(peer_rows(ring.slot), first));
+                    }
+                }
+        }
+    } else if (GATHER && warp < FIRST_EPI) {
+        // Lane l of warp w copies columns 8 (l % 8) .. of rows 16 i + 4 (w - 2) + l / 8 of this block's half.  Rows past the
+        // group's last are not read: what the slot holds there only enters columns of the accumulator that no one stores.
+        const int r0 = 4 * (warp - 2) + (lane >> 3), col = 8 * (lane & 7);
+        const uint32_t at = (uint32_t)r0 * 128u + (uint32_t)(((lane & 7) ^ (r0 & 7)) << 4);
+        Ring ring(a.stages);
+        if (a.stall == STALL_ROWS && half && warp == 2) uniform_wait(rest, 0, bound, failed);
+        for (int t = cluster; t < tiles && !failed; t += clusters) {
+            const Tile p = place(t);
+            const int own = p.n >> 1, in = p.cnt - (int)half * own;   // rows of this half, of them there
+            const __nv_bfloat16 *src[PAIR_ROWS / 32];
+#pragma unroll
+            for (int i = 0; i < PAIR_ROWS / 32; ++i) {
+                const int r = 16 * i + r0;
+                src[i] = r < own && r < in ? static_cast<const __nv_bfloat16 *>(a.l.x) +
+                                                 (int64_t)(a.l.perm[p.q0 + (int)half * own + r] / a.l.x_div) * a.l.ld_x + col
+                                           : nullptr;
+            }
+            for (int k = k_lo; k < k_hi; ++k, ring.next()) {
+                if (ring.reused() && !uniform_wait(empty(ring.slot), ring.parity ^ 1u, bound, failed)) break;
+                const uint32_t to = base + (uint32_t)ring.slot * slot_bytes + w_bytes + at;
+                const uint32_t bytes = 64 * k + col < a.l.d_in ? 16u : 0u;   // d_in is a multiple of 8
+#pragma unroll
+                for (int i = 0; i < PAIR_ROWS / 32; ++i)
+                    if (src[i]) cp_async16z(to + 2048u * i, src[i] + (bytes ? 64 * k : 0), bytes);
+                cp_async_arrive(rows_in(ring.slot));
+            }
+        }
+        asm volatile("cp.async.wait_all;\n" ::: "memory");
+    } else {
+        const int q = warp & 3, f = 32 * q + lane;          // this thread's lane of tensor memory: its feature of the block's 128
+        const int from = warp >= FIRST_EPI + 4 ? 16 : 0;    // its first row; then every other 16
+        const LinArgs &l = a.l;
+        __nv_bfloat16 *const y = static_cast<__nv_bfloat16 *>(l.y);
+        const __nv_bfloat16 *const add = static_cast<const __nv_bfloat16 *>(l.addend);
+        const __nv_bfloat16 *const res = static_cast<const __nv_bfloat16 *>(l.residual);
+        const __nv_bfloat16 *const bias = static_cast<const __nv_bfloat16 *>(l.bias);
+        int n = 0;
+        for (int t = cluster; t < tiles && !failed; t += clusters, ++n) {
+            const Tile p = place(t);
+            const int b = a.bufs == 2 ? n & 1 : 0, uses = a.bufs == 2 ? n >> 1 : n;
+            const int m = p.m0 + 128 * (int)half + f;       // its feature: a column of y; the second block's is m + up
+            const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * MT * a.bn);
+            float bz[MT];
+#pragma unroll
+            for (int u = 0; u < MT; ++u) bz[u] = bias && m + u * a.up < l.n_w && m < l.d_out ? load_elem(bias + (int64_t)p.e * l.n_w + m + u * a.up) : 0.f;
+
+            // R rows' sums of one column c of y (gated: and of its up projection) to y; rows from tile row r, stride `by`
+            auto store = [&](auto &z, auto &up, int c, int r, int by, int rows) {
+                constexpr int R = sizeof(z) / sizeof(float);
+                if (c >= l.d_out) return;
+                auto row = [&](int j) -> int64_t { return GATHER ? l.perm[p.q0 + r + j * by] : p.q0 + r + j * by; };
+                if (add) {
+#pragma unroll
+                    for (int j = 0; j < R; ++j)
+                        if (j * by < rows) {
+                            const __nv_bfloat16 *s = add + row(j) * l.ld_a + c;
+                            z[j] += load_elem(s);
+                            if (a.gated) up[j] += load_elem(s + l.d_out);
+                        }
+                }
+                activate<true, R>(l.act, z);
+                if (a.gated)
+#pragma unroll
+                    for (int j = 0; j < R; ++j) z[j] *= up[j];
+                if (res) {
+#pragma unroll
+                    for (int j = 0; j < R; ++j)
+                        if (j * by < rows) z[j] += load_elem(res + row(j) * l.ld_r + c);
+                }
+#pragma unroll
+                for (int j = 0; j < R; ++j)
+                    if (j * by < rows) store_elem(y + row(j) * l.ld_y + c, z[j]);
+            };
+            // S > 1: on to the exchange all the same, which every block of the cluster takes part in
+            const bool stall = a.stall == STALL_SUMS && half == 1 && warp == FIRST_EPI;
+            if (!lanes_wait(stall ? rest : acc_full(b), (unsigned)uses & 1u, bound, failed) && S == 1) break;
+            tc_fence_after();
+            if (S == 1) {
+                for (int c = from; c < p.cnt; c += 32) {
+                    float z[MT][16];
+#pragma unroll
+                    for (int u = 0; u < MT; ++u) tc_ld16(acc + (uint32_t)(u * a.bn + c), z[u]);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int u = 0; u < MT; ++u)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) z[u][j] += bz[u];
+                    if (MT == 2 && !a.gated) store(z[1], z[1], m + a.up, c, 1, p.cnt - c);
+                    store(z[0], z[MT - 1], m, c, 1, p.cnt - c);
+                }
+            } else {
+                const int own = own_rows(p.cnt, a.split_log2), own_log2 = 31 - __clz(own), mine = rank >> 1;
+                // [feature block][source][row of own][128 features], in each owner's shared memory
+                const uint32_t part_bytes = 512u * (uint32_t)own, block_bytes = part_bytes << a.split_log2;
+                const uint32_t to0 = red + (uint32_t)mine * part_bytes + 4u * (uint32_t)f;
+                if (!a.own_red) cluster_sync_all();   // every block's products are done with its ring
+                for (int c = from; c < p.cnt; c += 32) {
+                    float z[MT][16];
+#pragma unroll
+                    for (int u = 0; u < MT; ++u) tc_ld16(acc + (uint32_t)(u * a.bn + c), z[u]);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int owner = own >= 16 ? c / own : (c + j) >> own_log2;
+                        const uint32_t at = map_rank(to0, 2u * (uint32_t)owner + half) + 512u * (uint32_t)(c + j - owner * own);
+                        if (c + j < p.cnt)
+#pragma unroll
+                            for (int u = 0; u < MT; ++u) st_cluster(at + (uint32_t)u * block_bytes, z[u][j]);
+                    }
+                }
+                cluster_sync_all();
+                const int r_lo = mine * own, rows = min(own, p.cnt - r_lo);
+                const uint32_t from0 = red + 4u * (uint32_t)f;
+                for (int r = from >> 4; r < rows; r += 2) {
+                    float z[MT][1];
+#pragma unroll
+                    for (int u = 0; u < MT; ++u) {
+                        z[u][0] = bz[u];
+                        float sum = __uint_as_float(lds32(from0 + (uint32_t)u * block_bytes + 512u * (uint32_t)r));
+                        for (int s = 1; s < S; ++s)
+                            sum += __uint_as_float(lds32(from0 + (uint32_t)u * block_bytes + (uint32_t)s * part_bytes + 512u * (uint32_t)r));
+                        z[u][0] += sum;
+                    }
+                    if (MT == 2 && !a.gated) store(z[1], z[1], m + a.up, r_lo + r, 1, 1);
+                    store(z[0], z[MT - 1], m, r_lo + r, 1, 1);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_rank(acc_empty(b), first));
+        }
+    }
+    // ---------------------------------------------------------------- teardown
+    __syncwarp();
+    leave<true>(bound, failed, first);
+    if (S > 1 && warp < FIRST_EPI && cluster < tiles) {   // the barriers of the exchange, for the warps that take no part in it
+        if (!a.own_red) cluster_sync_all();
+        cluster_sync_all();
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    if (stop_sm) {   // a wait ran out: in both blocks of the pair, which stopped where they were
+        if (warp == 0 && half == 0) {
+            // The first block's barriers count both blocks' bytes.  The uses that one block has begun and the other not (at
+            // most one a slot) complete with the bytes of that one.
+            Ring r(a.stages, used_sm);
+            uint32_t other;
+            asm volatile("ld.shared::cluster.u32 %0, [%1];\n" : "=r"(other) : "r"(map_rank(smem_u32(&used_sm), first + 1)) : "memory");
+            for (uint32_t k = other; k < r.uses; ++k)
+                if (elect_one()) mbar_complete_tx(full((int)(k % (unsigned)a.stages)), tx / 2);
+            for (; r.uses < other; r.next())
+                if (elect_one()) mbar_expect_tx(full(r.slot), tx / 2);
+            drain_ring(r, full(0));
+        } else if (warp == 1) {   // the products read both blocks' memory and tensor memory
+            if (half == 0 && elect_one()) tc_commit_pair(rest, first);
+            rest_wait(rest, 0);
+        }
+    }
+    if (stop_sm) cluster_sync_all();   // of those that are still here: both blocks of the pair
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
+    }
+}
+
+// A shape of the tiles and what the call would take with it.
+struct PairPlan {
+    int mt = 0, bn = 0, split_log2 = 0, clusters = 1;
+    int64_t ns = 0;
+};
+
+// clusters resident at once, of 1, 2, 4 pairs: a property of the device and the kernel, asked for once
+template <bool GATHER, int MT>
+int pair_fit(int dev, const int **fit) {
+    static std::mutex mu;
+    static int table[64][3] = {};
+    std::lock_guard<std::mutex> lock(mu);
+    int *f = table[dev & 63];
+    auto kernel = linear_pair_kernel<GATHER, MT>;
+    if (!f[0]) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pair_smem<GATHER>());
+        for (int i = 2; i >= 0 && e == cudaSuccess; --i) {   // f[0] last: it marks the table as filled
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(2u << i);
+            cfg.blockDim = dim3(pair_threads<GATHER>());
+            cfg.dynamicSmemBytes = pair_smem<GATHER>();
+            cudaLaunchAttribute attr{};
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = 2u << i;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+            if (e == cudaSuccess) f[i] = i ? n : std::max(1, n);
+        }
+        if (e != cudaSuccess) return cuda_rc(e);
+    }
+    *fit = f;
+    return LORA_OK;
+}
+
+int m_tiles_of(const LinArgs &l, bool gated, int mt) { return (l.d_out + (gated ? 256 : 256 * mt) - 1) / (gated ? 256 : 256 * mt); }
+
+// The best split of k for tiles of bn rows; row_tiles: as many as there may be, likely: as many as are expected.
+template <bool GATHER, int MT>
+int consider(const LinArgs &l, bool gated, int bn, int64_t row_tiles, int64_t likely, int dev, PairPlan *best) {
+    const int *fit = nullptr;
+    const int rc = pair_fit<GATHER, MT>(dev, &fit);
+    if (rc != LORA_OK) return rc;
+    const int64_t m = m_tiles_of(l, gated, MT), n_k = (l.d_in + 63) / 64;
+    // a 64-column step: its products, its copies into shared memory, or what a step takes at least (ns)
+    const int64_t step = std::max<int64_t>({(int64_t)MT * bn * 21 / 20, (16384 * MT + 64 * bn) / 110, 100});
+    for (int i = 0; i < 3; ++i) {
+        const int s = 1 << i, rows = std::min(bn, l.T);
+        if (s > n_k) break;
+        const int64_t tiles = m * row_tiles, expect = m * likely;
+        if (i && tiles > fit[i]) break;   // a cluster that splits k has one tile
+        if (i && bn > 32 && (size_t)own_rows(rows, i) * s * 512 * MT > pair_smem<GATHER>() - 1024) continue;
+        const int64_t clusters = std::min<int64_t>(tiles, fit[i]);
+        const int64_t rounds = (expect + clusters - 1) / clusters;
+        const int64_t ns = 4000 + rounds * ((n_k + s - 1) / s * step + 1000) + (i ? 800 * i + 10 * rows * MT : 0);
+        if (!best->mt || ns < best->ns) best->mt = MT, best->bn = bn, best->split_log2 = i, best->clusters = (int)clusters, best->ns = ns;
+    }
+    return LORA_OK;
+}
+
+template <bool GATHER, int MT>
+int launch_pair(PairArgs &a, const PairPlan &plan, cudaStream_t st) {
+    a.bn = plan.bn, a.split_log2 = plan.split_log2;
+    a.up = a.gated ? a.l.d_out : 256;
+    a.m_tiles = m_tiles_of(a.l, a.gated, MT);
+    a.bufs = 2 * MT * plan.bn <= 512 ? 2 : 1;
+    a.own_red = plan.split_log2 > 0 && plan.bn <= 32;
+    const size_t slot = 16384u * MT + 64u * (size_t)plan.bn, red = a.own_red ? (size_t)own_rows(plan.bn, plan.split_log2) * 512 * MT << plan.split_log2 : 0;
+    a.stages = (int)std::min<size_t>(PAIR_STAGES, (pair_smem<GATHER>() - 1024 - red) / slot);
+    return launch_after(linear_pair_kernel<GATHER, MT>, dim3((unsigned)(plan.clusters << (plan.split_log2 + 1))), pair_threads<GATHER>(),
+                        pair_smem<GATHER>(), 2u << plan.split_log2, st, a);
+}
+
+int round32(int64_t n) { return (int)((n + 31) / 32 * 32); }
+
+}  // namespace
+
+bool linear_tc_ok(const LinArgs &a, int64_t x_rows) {
+    return (a.d_in & 7) == 0 && (x_rows <= 1 || (a.ld_x & 7) == 0) && (a.ld_w & 7) == 0 && mx_aligned(a.x, 16) && mx_aligned(a.w, 16);
+}
+
+int launch_linear_tc(const LinArgs &l, int64_t x_rows, bool gated, int dev, int sms, cudaStream_t st) {
+    PairArgs a{};
+    a.l = l;
+    a.gated = gated;
+    a.n_k = (l.d_in + 63) / 64;
+    const char *stall = std::getenv("LORA_DEBUG_STALL");   // test hook: the waits of one role run out, after a short while
+    a.stall = stall ? std::atoi(stall) : 0;
+    a.limit = a.stall ? 64 : WAIT_LIMIT;
+    PairPlan best;
+    int rc = LORA_OK;
+    const bool gather = l.perm != nullptr;
+    if (gather) {
+        const int64_t groups = std::min(l.N, l.T), mean = (l.T + groups - 1) / groups;
+        const int bn = std::min(PAIR_ROWS, round32(mean + mean / 2));
+        const int64_t row_tiles = l.T / bn + groups, likely = std::max<int64_t>(groups, l.T / bn + groups / 2);
+        if (!gated) rc = consider<true, 1>(l, gated, bn, row_tiles, likely, dev, &best);
+        if (rc == LORA_OK) rc = consider<true, 2>(l, gated, bn, row_tiles, likely, dev, &best);
+    } else {
+        const int least = (l.T + PAIR_ROWS - 1) / PAIR_ROWS;
+        for (int nt = least; nt <= least + 2 && rc == LORA_OK; ++nt) {   // the fewest row tiles, or a little more that fill the SMs better
+            const int bn = round32((l.T + nt - 1) / nt), n = (l.T + bn - 1) / bn;
+            if (!gated) rc = consider<false, 1>(l, gated, bn, n, n, dev, &best);
+            if (rc == LORA_OK) rc = consider<false, 2>(l, gated, bn, n, n, dev, &best);
+            if (bn == 32) break;
+        }
+    }
+    if (rc != LORA_OK) return rc;
+    rc = tensor_map_rows(&a.tmW, l.w, (uint64_t)l.d_in, (uint64_t)l.N * l.n_w, (uint64_t)l.ld_w, 128);
+    if (rc == LORA_OK && !gather) rc = tensor_map_rows(&a.tmX, l.x, (uint64_t)l.d_in, (uint64_t)l.T, (uint64_t)(l.T > 1 ? l.ld_x : (l.d_in + 7) / 8 * 8), (uint32_t)best.bn / 2);
+    if (rc != LORA_OK) return rc;
+    a.n_tiles = gather ? 0 : (l.T + best.bn - 1) / best.bn;
+    if (gather) return best.mt == 1 ? launch_pair<true, 1>(a, best, st) : launch_pair<true, 2>(a, best, st);
+    return best.mt == 1 ? launch_pair<false, 1>(a, best, st) : launch_pair<false, 2>(a, best, st);
+}
+
+}  // namespace lora

@@ -17,8 +17,7 @@
 //
 // Two kernels, for few and many rows of x; which one: launch_linear.
 #include "mx.cuh"
-#include "ptx.cuh"
-#include "tc.cuh"
+#include "pipe.cuh"
 
 #include <algorithm>
 #include <cstdlib>
@@ -47,9 +46,6 @@ enum { STALL_MMA = 1, STALL_SCALES = 2, STALL_COPY = 3, STALL_SUMS = 4, STALL_CO
 
 template <int KIND>
 __host__ __device__ constexpr int mx_tiles_per_stage() { return KIND == MX_A8 ? 1 : 2; }
-__host__ __device__ constexpr uint32_t pow2_cols(uint32_t c) {
-    return c <= 32 ? 32 : c <= 64 ? 64 : c <= 128 ? 128 : c <= 256 ? 256 : 512;
-}
 
 // Instruction descriptor of the block-scaled kinds: scale ids at [4,6) (B) and
 // [29,31) (A), element types at [7,10) (A) and [10,13) (B), N >> 3 at [17,23),
@@ -76,73 +72,6 @@ __device__ __forceinline__ void mx_mma(uint32_t d, uint64_t a, uint64_t b, uint3
     if (KIND == MX_A4 && PAIR) MX_MMA("2", "mxf4.block_scale.scale_vec::2X");
 }
 #undef MX_MMA
-// One lane of a full warp, the same at every call.  The tensor-core and copy instructions take
-// their operands from uniform registers.  So the copying and issuing warps run their loops and
-// waits as whole warps, whose counters the compiler then keeps there, and elect a lane around
-// the instructions alone.  Measured: an MMA of N = 16 issued every 59 clocks behind `lane == 0`, every 38 (its
-// own time) behind an election; with the loop inside the elected branch each stage of four still cost
-// about 470 clocks of register moves.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
-    return p != 0;
-}
-
-// A kernel's bounded waits.  The first that runs out says so in `stop`, a word of the block's shared memory (of both
-// blocks' where a pair works together): every wait that goes on ends too, and the teardown, which all warps reach, lets what
-// is under way come to rest before the block goes.
-struct Bound {
-    uint32_t stop;
-    unsigned limit;   // tries
-    int32_t *status;
-};
-__device__ __forceinline__ uint32_t stopped(uint32_t stop) {
-    uint32_t r;
-    asm volatile("ld.relaxed.cluster.shared::cta.u32 %0, [%1];\n" : "=r"(r) : "r"(stop));
-    return r;
-}
-// Wait of a whole warp, uniform for all its lanes: for warps that copy and issue.
-__device__ __forceinline__ bool uniform_wait(uint32_t bar, unsigned parity, const Bound &w, bool &failed) {
-    if (__all_sync(FULL, mbar_try<false>(bar, parity))) return true;
-    for (unsigned it = 1; it < w.limit && !__any_sync(FULL, stopped(w.stop)); ++it)
-        if (__all_sync(FULL, mbar_try<false>(bar, parity))) return true;
-    failed = true;
-    return false;
-}
-// The same, lane by lane: for warps that move scales and sums.  As a uniform_wait theirs took 1 x 4096 x 4096 5.46 -> 5.56 us
-// and 8192 x 4096 x 4096 in MXFP4 65.8 -> 69.0.
-__device__ __forceinline__ bool lanes_wait(uint32_t bar, unsigned parity, const Bound &w, bool &failed) {
-    bool ok = false;
-    for (unsigned it = 0; it < w.limit; ++it) {
-        if ((ok = mbar_try<false>(bar, parity))) break;
-        if (stopped(w.stop)) break;
-    }
-    ok = __all_sync(FULL, ok);
-    if (!ok) failed = true;
-    return ok;
-}
-// A warp's part has ended: after a wait of its own that ran out, or that another's stopped.
-template <bool PAIR>
-__device__ __forceinline__ void leave(const Bound &w, bool failed) {
-    if (failed && elect_one()) {
-        atomicOr(w.status, LORA_DEV_TIMEOUT);
-        if (PAIR) {
-#pragma unroll
-            for (uint32_t k = 0; k < 2; ++k)
-                asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], 1;\n" ::"r"(map_rank(w.stop, k)) : "memory");
-        } else {
-            asm volatile("st.relaxed.cluster.shared::cta.u32 [%0], 1;\n" ::"r"(w.stop) : "memory");
-        }
-    }
-}
-// Wait of the teardown after a wait that ran out: for copies and products in flight, which end by themselves.
-__device__ __forceinline__ void rest_wait(uint32_t bar, unsigned parity) {
-    for (unsigned it = 0; it < 1024 && !__all_sync(FULL, mbar_try<false>(bar, parity)); ++it) {}
-}
-__device__ __forceinline__ void mbar_complete_tx(uint32_t bar, unsigned bytes) {   // as a copy of so many bytes would
-    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");
-}
-
 // 16 bytes to four columns of this thread's tensor-memory lane
 __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint4 v) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(taddr), "r"(v.x), "r"(v.y), "r"(v.z),
@@ -150,12 +79,6 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, uint4 v) {
                  : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-// arrival on a barrier of a block of the cluster (address mapped with map_rank); it orders tensor
-// memory only (through the tcgen05 fences), so it needs no release
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
-}
-
 // The MMAs of one ring stage: n_tiles scale tiles (128 columns of K each) of operands
 // at a, b (shared memory) whose scales lie at columns sa, sb of tensor memory,
 // four (sb_cols) columns a tile.
@@ -182,22 +105,6 @@ __device__ __forceinline__ void y_store(void *y, int64_t at, float v) {
     else static_cast<float *>(y)[at] = v;
 }
 
-// A place in a ring of n slots, after so many uses of slots: the next slot and the parity of its use.  Kept by
-// counting: an integer division costs as much as the MMAs of a stage.
-struct Ring {
-    int slot, n;
-    unsigned uses, parity;
-    __device__ explicit Ring(int n_, unsigned used = 0) : slot((int)(used % (unsigned)n_)), n(n_), uses(used), parity(used / (unsigned)n_ & 1u) {}
-    __device__ void next() {
-        ++uses;
-        if (++slot == n) slot = 0, parity ^= 1u;
-    }
-    __device__ bool reused() const { return uses >= (unsigned)n; }
-};
-
-__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {   // address mapped with map_rank
-    asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(addr), "f"(v) : "memory");
-}
 // Every other row from `from` of a block's `to` rows: the S partial sums at
 // [source][row of own][128 features], in order, to y.
 template <int S, typename Y>
@@ -212,12 +119,6 @@ __device__ __forceinline__ void sum_rows(Y *y, int64_t ld, uint32_t red, int own
         for (int k = 1; k < S; ++k) t += v[k];
         store_elem(y + j * ld, t);
     }
-}
-
-// The last use of each slot of a ring, up to r, is complete on the slots' barriers.
-__device__ __forceinline__ void drain_ring(Ring r, uint32_t full) {
-    for (int j = 0; j < r.n; ++j, r.next())   // oldest first: parity ^ 1 is that of the slot's last use
-        if (r.reused()) rest_wait(full + 8u * (uint32_t)r.slot, r.parity ^ 1u);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -744,35 +645,6 @@ __host__ __device__ constexpr uint32_t big_slot_bytes() {   // x rows, W rows, x
 // rounded up to the 1 KB the swizzle's atoms ask for
 template <int KIND>
 __host__ __device__ constexpr uint32_t big_slot_stride() { return (big_slot_bytes<KIND>() + 1023u) & ~1023u; }
-
-// box copy whose bytes count on a barrier of either block of the pair
-__device__ __forceinline__ void tma_2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, "
-        "{%2, %3}], [%4];\n" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-// arrival on the barrier at this offset in both blocks once the MMAs issued so far are done
-__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(bar),
-        "h"((uint16_t)3)
-        : "memory");
-}
-// 32 consecutive fp32 columns of this thread's tensor-memory lane
-__device__ __forceinline__ void tc_ld32(uint32_t taddr, uint32_t *r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, "
-        "[%32];\n"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr)
-        : "memory");
-}
 
 template <int KIND, bool BF16>
 __global__ void __launch_bounds__(BIG_THREADS, 1) mx_linear_big_kernel(const __grid_constant__ MxBigArgs a) {

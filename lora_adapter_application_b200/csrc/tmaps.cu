@@ -136,6 +136,22 @@ int tensor_map_chunks(CUtensorMap *out, const void *base, uint64_t inner, uint64
     return LORA_OK;
 }
 
+// A bf16 matrix [rows][inner], rows row_stride elements apart: boxes of 64 columns x box_rows rows, 128-byte
+// swizzle.  Encoded afresh on every call.
+int tensor_map_rows(CUtensorMap *out, const void *base, uint64_t inner, uint64_t rows, uint64_t row_stride,
+                    uint32_t box_rows) {
+    auto fn = encoder();
+    if (!fn) return cuda_fail("cuTensorMapEncodeTiled: driver entry point not found");
+    const cuuint64_t dims[2] = {inner, rows};
+    const cuuint64_t strides[1] = {row_stride * 2};
+    const cuuint32_t box[2] = {64, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = fn(out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? LORA_OK : cuda_fail("cuTensorMapEncodeTiled failed");
+}
+
 // A byte matrix [rows][inner] with rows `pitch` bytes apart, 128-byte swizzle, boxes of
 // 128 bytes x box_rows rows; packed4: the bytes hold two 4-bit elements and arrive
 // in shared memory 8 bytes in each 16 (16 elements, then padding: the form the
