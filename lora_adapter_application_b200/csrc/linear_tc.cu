@@ -28,6 +28,7 @@ namespace {
 
 constexpr int PAIR_STAGES = 12;
 constexpr int PAIR_ROWS = 256;    // widest tile of x rows
+constexpr int MAX_S = 4;          // most pairs that split k: clusters of eight blocks
 constexpr int EPI_WARPS = 8, GATHER_WARPS = 4;
 template <bool GATHER>
 constexpr int pair_threads() { return 32 * (2 + EPI_WARPS + (GATHER ? GATHER_WARPS : 0)); }
@@ -43,9 +44,9 @@ struct PairArgs {
     int up;              // rows of W between a tile's two feature blocks
     int bn;              // rows of a tile
     int m_tiles, n_tiles;   // tiles along the features; along x (plain product)
-    int n_k;             // 64-column steps of k
+    int n_k;             // ring slots of k (KT steps of 64 columns each)
     int stages, bufs;    // ring slots, accumulator buffers
-    int split_log2;      // S
+    int S;               // pairs that split k
     int own_red;         // the partial sums' place is behind the ring
     unsigned limit;
     int stall;
@@ -64,9 +65,10 @@ __device__ __forceinline__ void pair_mma(uint32_t d, uint64_t a, uint64_t b, uin
 __device__ __forceinline__ void cp_async16z(uint32_t dst, const void *src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-// arrival on a barrier of another block of the cluster; what this thread has seen and fenced is visible to who waits there
-__device__ __forceinline__ void mbar_arrive_release(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
+// Arrival on a barrier of another block of the cluster.  The rows it speaks for are read by the tensor core of this thread's
+// own SM, for which its proxy fence has made them visible.  (A release and an acquire of the cluster's scope took 1.2 us a stage.)
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
 
 // A tile: its features from m0 (MT blocks of 256), its rows q0 .. q0 + cnt - 1 of expert e, n = rows of the MMA.
@@ -74,31 +76,39 @@ struct Tile {
     int m0, e, q0, cnt, n;
 };
 
+// What the epilogue adds to R rows' sums of a thread's MT features: bf16 bits, a register each (two in one would wait for
+// both loads where they are packed).
+template <int MT, int R>
+struct Operands {
+    uint32_t add[MT][R], res[MT][R];
+};
+__device__ __forceinline__ uint32_t bf16_bits(const __nv_bfloat16 *p) { return *reinterpret_cast<const unsigned short *>(p); }
+
 // Rows of a block in the exchange of partial sums: a power of two up to 16, or a multiple of 16, so that 16 rows' owners
 // follow from shifts or are one.
-__host__ __device__ __forceinline__ int own_rows(int rows, int split_log2) {
-    const int fair = (rows + (1 << split_log2) - 1) >> split_log2;
+__host__ __device__ __forceinline__ int own_rows(int rows, int S) {
+    const int fair = (rows + S - 1) / S;
     if (fair > 16) return (fair + 15) & ~15;
     int own = 1;
     while (own < fair) own *= 2;
     return own;
 }
 
-template <bool GATHER, int MT>
+template <bool GATHER, int MT, int KT>
 __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(const __grid_constant__ PairArgs a) {
     extern __shared__ __align__(1024) unsigned char lin_sm[];
     __shared__ uint32_t tmem_sm;
-    __shared__ __align__(8) uint64_t bars[4 * PAIR_STAGES + 5];
+    __shared__ __align__(8) uint64_t bars[4 * PAIR_STAGES + 6];
     __shared__ uint32_t stop_sm, used_sm;   // used_sm: ring uses that this block's copies have begun
     __shared__ int pre[GATHER ? MAX_EXPERTS + 1 : 1], part[GATHER ? 32 : 1];
     constexpr int FIRST_EPI = GATHER ? 2 + GATHER_WARPS : 2;
     const int warp = __shfl_sync(FULL, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const uint32_t w_bytes = 16384u * MT, slot_bytes = w_bytes + 64u * (uint32_t)a.bn;
+    const uint32_t w_bytes = 16384u * MT * KT, x_bytes = 64u * (uint32_t)a.bn, slot_bytes = w_bytes + x_bytes * KT;
     const uint32_t base = (smem_u32(lin_sm) + 1023u) & ~1023u, red = base + (a.own_red ? (uint32_t)a.stages * slot_bytes : 0u);
-    const int rank = (int)cluster_rank(), S = 1 << a.split_log2;
+    const int rank = (int)cluster_rank(), S = a.S;
     const uint32_t half = rank & 1, first = rank & ~1;   // this block of the pair; the pair's first block
-    const int cluster = (int)blockIdx.x >> (a.split_log2 + 1), clusters = (int)gridDim.x >> (a.split_log2 + 1);
-    const int k_lo = a.n_k * (rank >> 1) >> a.split_log2, k_hi = a.n_k * ((rank >> 1) + 1) >> a.split_log2;
+    const int cluster = (int)blockIdx.x / (2 * S), clusters = (int)gridDim.x / (2 * S);
+    const int k_lo = a.n_k * (rank >> 1) / S, k_hi = a.n_k * ((rank >> 1) + 1) / S;
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     auto full = [&](int s) { return bar(s); };                       // the first block's counts both blocks' TMA bytes
     auto empty = [&](int s) { return bar(PAIR_STAGES + s); };
@@ -106,12 +116,13 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
     auto peer_rows = [&](int s) { return bar(3 * PAIR_STAGES + s); };    // the first block's: the second's have landed too
     auto acc_full = [&](int b) { return bar(4 * PAIR_STAGES + b); };
     auto acc_empty = [&](int b) { return bar(4 * PAIR_STAGES + 2 + b); };   // the first block's: eight warps of each block
+    const uint32_t ready = bar(4 * PAIR_STAGES + 5);   // the first block's: the second has its tensor memory
     const uint32_t rest = bar(4 * PAIR_STAGES + 4);   // completes in the teardown after a wait that ran out, else never
     const Bound bound{smem_u32(&stop_sm), a.limit, a.l.status};
     bool failed = false;
 
     if (warp == 0) {
-        for (int i = lane; i < 4 * PAIR_STAGES + 5; i += 32) {
+        for (int i = lane; i < 4 * PAIR_STAGES + 6; i += 32) {
             const bool rows = i >= 2 * PAIR_STAGES && i < 3 * PAIR_STAGES, drained = i >= 4 * PAIR_STAGES + 2 && i < 4 * PAIR_STAGES + 4;
             mbar_init(bar(i), rows ? 32 * GATHER_WARPS : drained ? 2 * EPI_WARPS : 1);
         }
@@ -122,17 +133,24 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
         }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
+    // The warps that copy need no more than the barriers of the cluster's blocks; tensor memory is got meanwhile.
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(smem_u32(&tmem_sm)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
     }
-    tc_fence_before();
-    __syncthreads();
-    cluster_sync_all();   // every block's barriers and tensor memory are ready
-    tc_fence_after();
-    const uint32_t tmem = __shfl_sync(FULL, tmem_sm, 0);
     pdl_next();
     pdl_wait();   // all warps: none of the bounded waits below runs while the kernel before this one does
+    asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+    uint32_t tmem = 0;
+    if (warp == 1 || warp >= FIRST_EPI) {
+        tc_fence_before();
+        asm volatile("bar.sync 1, %0;\n" ::"n"(32 * (1 + EPI_WARPS)) : "memory");
+        tc_fence_after();
+        tmem = __shfl_sync(FULL, tmem_sm, 0);
+        if (warp == 1 && half == 1 && elect_one()) mbar_arrive_peer(map_rank(ready, first));
+    }
     int tiles = a.m_tiles * a.n_tiles;
     if (GATHER) {
         count_tiles(a.l.seg_start, a.l.N, a.bn, pre, part);
@@ -163,7 +181,7 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
         p.m0 = mi * (a.gated ? 256 : 256 * MT);
         return p;
     };
-    const uint32_t tx = 2u * (w_bytes + (GATHER ? 0u : 64u * (uint32_t)a.bn));
+    const uint32_t tx = 2u * (GATHER ? w_bytes : slot_bytes);
 
     if (warp == 0) {
         Ring ring(a.stages);
@@ -177,8 +195,12 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
                 if (elect_one()) {
                     if (half == 0) mbar_expect_tx(full(ring.slot), tx);
 #pragma unroll
-                    for (int u = 0; u < MT; ++u) tma_2d_pair(slot + 16384u * u, &a.tmW, 64 * k, w0 + u * a.up, b);
-                    if (!GATHER) tma_2d_pair(slot + w_bytes, &a.tmX, 64 * k, x0, b);
+                    for (int u = 0; u < MT; ++u)
+#pragma unroll
+                        for (int i = 0; i < KT; ++i) tma_2d_pair(slot + 16384u * (u + MT * i), &a.tmW, 64 * (k * KT + i), w0 + u * a.up, b);
+                    if (!GATHER)
+#pragma unroll
+                        for (int i = 0; i < KT; ++i) tma_2d_pair(slot + w_bytes + x_bytes * i, &a.tmX, 64 * (k * KT + i), x0, b);
                 }
             }
         }
@@ -187,7 +209,7 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
         if (half == 0) {
             Ring ring(a.stages);
             int n = 0;
-            if (a.stall == STALL_MMA) uniform_wait(rest, 0, bound, failed);
+            uniform_wait(a.stall == STALL_MMA ? rest : ready, 0, bound, failed);
             for (int t = cluster; t < tiles && !failed; t += clusters, ++n) {
                 const Tile p = place(t);
                 const int b = a.bufs == 2 ? n & 1 : 0, uses = a.bufs == 2 ? n >> 1 : n;
@@ -198,26 +220,23 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
                     const int s = ring.slot;
                     if (!uniform_wait(full(s), ring.parity, bound, failed)) break;
                     if (GATHER) {
-                        if (!uniform_wait(rows_in(s), ring.parity, bound, failed)) break;
-                        bool ok = false;   // the second block's word: acquire its rows
-                        for (unsigned it = 0; it < bound.limit && !ok && !__any_sync(FULL, stopped(bound.stop)); ++it)
-                            ok = __all_sync(FULL, mbar_try<true>(peer_rows(s), ring.parity));
-                        if (!ok) {
-                            failed = true;
+                        if (!uniform_wait(rows_in(s), ring.parity, bound, failed) || !uniform_wait(peer_rows(s), ring.parity, bound, failed))
                             break;
-                        }
                     }
                     tc_fence_after();
                     const uint32_t slot = base + (uint32_t)s * slot_bytes;
                     if (elect_one()) {
                         if (GATHER) fence_proxy_async();   // rows came by cp.async (generic proxy), the MMA reads them as operands
-                        const uint64_t dx = desc_sw128(slot + w_bytes);
 #pragma unroll
-                        for (int u = 0; u < MT; ++u) {
-                            const uint64_t dw = desc_sw128(slot + 16384u * u);
+                        for (int x = 0; x < KT; ++x) {
+                            const uint64_t dx = desc_sw128(slot + w_bytes + x_bytes * x);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                pair_mma(d + (uint32_t)(u * a.bn), dw + 2 * i, dx + 2 * i, idesc, k == k_lo && i == 0 ? 0u : 1u);
+                            for (int u = 0; u < MT; ++u) {
+                                const uint64_t dw = desc_sw128(slot + 16384u * (u + MT * x));
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    pair_mma(d + (uint32_t)(u * a.bn), dw + 2 * i, dx + 2 * i, idesc, k == k_lo && x == 0 && i == 0 ? 0u : 1u);
+                            }
                         }
                         tc_commit_pair(empty(s), first);
                     }
@@ -231,7 +250,7 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
                     if (!uniform_wait(rows_in(ring.slot), ring.parity, bound, failed)) break;
                     if (elect_one()) {
                         fence_proxy_async();
-                        mbar_arrive_release(map_rank(peer_rows(ring.slot), first));
+                        mbar_arrive_peer(map_rank(peer_rows(ring.slot), first));
                     }
                 }
         }
@@ -256,17 +275,23 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
             for (int k = k_lo; k < k_hi; ++k, ring.next()) {
                 if (ring.reused() && !uniform_wait(empty(ring.slot), ring.parity ^ 1u, bound, failed)) break;
                 const uint32_t to = base + (uint32_t)ring.slot * slot_bytes + w_bytes + at;
-                const uint32_t bytes = 64 * k + col < a.l.d_in ? 16u : 0u;   // d_in is a multiple of 8
 #pragma unroll
-                for (int i = 0; i < PAIR_ROWS / 32; ++i)
-                    if (src[i]) cp_async16z(to + 2048u * i, src[i] + (bytes ? 64 * k : 0), bytes);
+                for (int x = 0; x < KT; ++x) {
+                    const int at_k = 64 * (k * KT + x);
+                    const uint32_t bytes = at_k + col < a.l.d_in ? 16u : 0u;   // d_in is a multiple of 8
+#pragma unroll
+                    for (int i = 0; i < PAIR_ROWS / 32; ++i)
+                        if (src[i]) cp_async16z(to + x_bytes * x + 2048u * i, src[i] + (bytes ? at_k : 0), bytes);
+                }
                 cp_async_arrive(rows_in(ring.slot));
             }
         }
         asm volatile("cp.async.wait_all;\n" ::: "memory");
     } else {
         const int q = warp & 3, f = 32 * q + lane;          // this thread's lane of tensor memory: its feature of the block's 128
-        const int from = warp >= FIRST_EPI + 4 ? 16 : 0;    // its first row; then every other 16
+        const int half_warps = warp >= FIRST_EPI + 4;       // which of the two warps of these lanes
+        constexpr int CHUNK = MT == 2 ? 8 : 16;   // rows at a time (8: 16 spill registers)
+        constexpr int OWN_CHUNK = 4;                        // of those that a block owns after an exchange
         const LinArgs &l = a.l;
         __nv_bfloat16 *const y = static_cast<__nv_bfloat16 *>(l.y);
         const __nv_bfloat16 *const add = static_cast<const __nv_bfloat16 *>(l.addend);
@@ -282,85 +307,144 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
 #pragma unroll
             for (int u = 0; u < MT; ++u) bz[u] = bias && m + u * a.up < l.n_w && m < l.d_out ? load_elem(bias + (int64_t)p.e * l.n_w + m + u * a.up) : 0.f;
 
-            // R rows' sums of one column c of y (gated: and of its up projection) to y; rows from tile row r, stride `by`
-            auto store = [&](auto &z, auto &up, int c, int r, int by, int rows) {
-                constexpr int R = sizeof(z) / sizeof(float);
-                if (c >= l.d_out) return;
-                auto row = [&](int j) -> int64_t { return GATHER ? l.perm[p.q0 + r + j * by] : p.q0 + r + j * by; };
+            // R rows from tile row r: what the epilogue adds to them, fetched ahead of their sums (rows past the last: the
+            // last one again), for this thread's columns of y
+            auto row = [&](int r) -> int64_t {
+                const int q = p.q0 + min(r, p.cnt - 1);
+                return GATHER ? l.perm[q] : q;
+            };
+            const int cols = MT == 2 && !a.gated ? (m + a.up < l.d_out ? 2 : m < l.d_out) : (m < l.d_out ? 1 : 0);
+            auto fetch = [&](auto &ops, int r) {
+                constexpr int R = sizeof(ops.res[0]) / sizeof(uint32_t);
+                if (cols == 0 || !(add || res)) return;
+                int64_t at[R];
+#pragma unroll
+                for (int j = 0; j < R; ++j) at[j] = row(r + j);
                 if (add) {
 #pragma unroll
-                    for (int j = 0; j < R; ++j)
-                        if (j * by < rows) {
-                            const __nv_bfloat16 *s = add + row(j) * l.ld_a + c;
-                            z[j] += load_elem(s);
-                            if (a.gated) up[j] += load_elem(s + l.d_out);
-                        }
-                }
-                activate<true, R>(l.act, z);
-                if (a.gated)
+                    for (int j = 0; j < R; ++j) ops.add[0][j] = bf16_bits(add + at[j] * l.ld_a + m);
+                    if (MT == 2 && (a.gated || cols == 2))
 #pragma unroll
-                    for (int j = 0; j < R; ++j) z[j] *= up[j];
+                        for (int j = 0; j < R; ++j) ops.add[MT - 1][j] = bf16_bits(add + at[j] * l.ld_a + m + a.up);
+                }
                 if (res) {
 #pragma unroll
-                    for (int j = 0; j < R; ++j)
-                        if (j * by < rows) z[j] += load_elem(res + row(j) * l.ld_r + c);
+                    for (int j = 0; j < R; ++j) ops.res[0][j] = bf16_bits(res + at[j] * l.ld_r + m);
+                    if (MT == 2 && cols == 2)
+#pragma unroll
+                        for (int j = 0; j < R; ++j) ops.res[MT - 1][j] = bf16_bits(res + at[j] * l.ld_r + m + a.up);
                 }
+            };
+            // the epilogue of R rows' sums, in z
+            auto finish = [&](auto &z, auto &ops) {
+                constexpr int R = sizeof(z[0]) / sizeof(float);
+#pragma unroll
+                for (int u = 0; u < MT; ++u)
+#pragma unroll
+                    for (int j = 0; j < R; ++j) z[u][j] += bz[u];
+                if (add)
+#pragma unroll
+                    for (int u = 0; u < MT; ++u)
+#pragma unroll
+                        for (int j = 0; j < R; ++j) z[u][j] += bf16_lo(ops.add[u][j]);
+                activate<true, R>(l.act, z[0]);
+                if (MT == 2) {
+                    if (a.gated) {
+#pragma unroll
+                        for (int j = 0; j < R; ++j) z[0][j] *= z[MT - 1][j];
+                    } else {
+                        activate<true, R>(l.act, z[MT - 1]);
+                    }
+                }
+                if (res)
+#pragma unroll
+                    for (int u = 0; u < MT; ++u)
+#pragma unroll
+                        for (int j = 0; j < R; ++j) z[u][j] += bf16_lo(ops.res[u][j]);
+            };
+            auto put = [&](auto &z, int r, int rows) {
+                constexpr int R = sizeof(z[0]) / sizeof(float);
 #pragma unroll
                 for (int j = 0; j < R; ++j)
-                    if (j * by < rows) store_elem(y + row(j) * l.ld_y + c, z[j]);
+                    if (j < rows && cols) {
+                        __nv_bfloat16 *to = y + row(r + j) * l.ld_y + m;
+                        store_elem(to, z[0][j]);
+                        if (MT == 2 && cols == 2) store_elem(to + a.up, z[MT - 1][j]);
+                    }
             };
+            // a few rows at a time, the two halves of the warps in turn
+            Operands<MT, CHUNK> ops;
+            Operands<MT, OWN_CHUNK> mine_ops;
+            const int first_row = half_warps * CHUNK, own = own_rows(p.cnt, S), mine = rank >> 1, r_lo = mine * own;
+            if (S > 1) fetch(mine_ops, r_lo + half_warps * OWN_CHUNK);
+            else if (first_row < p.cnt) fetch(ops, first_row);
             // S > 1: on to the exchange all the same, which every block of the cluster takes part in
             const bool stall = a.stall == STALL_SUMS && half == 1 && warp == FIRST_EPI;
             if (!lanes_wait(stall ? rest : acc_full(b), (unsigned)uses & 1u, bound, failed) && S == 1) break;
             tc_fence_after();
             if (S == 1) {
-                for (int c = from; c < p.cnt; c += 32) {
-                    float z[MT][16];
+                for (int c = first_row; c < p.cnt; c += 2 * CHUNK) {
+                    float z[MT][CHUNK];
 #pragma unroll
-                    for (int u = 0; u < MT; ++u) tc_ld16(acc + (uint32_t)(u * a.bn + c), z[u]);
+                    for (int u = 0; u < MT; ++u) {
+                        if (CHUNK == 8) tc_ld8(acc + (uint32_t)(u * a.bn + c), z[u]);
+                        else tc_ld16(acc + (uint32_t)(u * a.bn + c), z[u]);
+                    }
                     tc_wait_ld();
-#pragma unroll
-                    for (int u = 0; u < MT; ++u)
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) z[u][j] += bz[u];
-                    if (MT == 2 && !a.gated) store(z[1], z[1], m + a.up, c, 1, p.cnt - c);
-                    store(z[0], z[MT - 1], m, c, 1, p.cnt - c);
+                    finish(z, ops);
+                    if (c + 2 * CHUNK < p.cnt) fetch(ops, c + 2 * CHUNK);
+                    put(z, c, p.cnt - c);
                 }
             } else {
-                const int own = own_rows(p.cnt, a.split_log2), own_log2 = 31 - __clz(own), mine = rank >> 1;
+                const int own_log2 = 31 - __clz(own);
                 // [feature block][source][row of own][128 features], in each owner's shared memory
-                const uint32_t part_bytes = 512u * (uint32_t)own, block_bytes = part_bytes << a.split_log2;
+                const uint32_t part_bytes = 512u * (uint32_t)own, block_bytes = part_bytes * (uint32_t)S;
                 const uint32_t to0 = red + (uint32_t)mine * part_bytes + 4u * (uint32_t)f;
                 if (!a.own_red) cluster_sync_all();   // every block's products are done with its ring
-                for (int c = from; c < p.cnt; c += 32) {
+                for (int c = 16 * half_warps; c < p.cnt; c += 32) {
                     float z[MT][16];
 #pragma unroll
                     for (int u = 0; u < MT; ++u) tc_ld16(acc + (uint32_t)(u * a.bn + c), z[u]);
                     tc_wait_ld();
+                    // 16 rows have one owner, or owners that follow from shifts
+                    if (own >= 16) {
+                        const int owner = c / own;
+                        const uint32_t at = map_rank(to0, 2u * (uint32_t)owner + half) + 512u * (uint32_t)(c - owner * own);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int owner = own >= 16 ? c / own : (c + j) >> own_log2;
-                        const uint32_t at = map_rank(to0, 2u * (uint32_t)owner + half) + 512u * (uint32_t)(c + j - owner * own);
-                        if (c + j < p.cnt)
+                        for (int u = 0; u < MT; ++u)
 #pragma unroll
-                            for (int u = 0; u < MT; ++u) st_cluster(at + (uint32_t)u * block_bytes, z[u][j]);
+                            for (int j = 0; j < 16; ++j)
+                                if (c + j < p.cnt) st_cluster(at + (uint32_t)u * block_bytes + 512u * j, z[u][j]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const uint32_t at = map_rank(to0, 2u * ((uint32_t)(c + j) >> own_log2) + half) + 512u * ((c + j) & (own - 1));
+                            if (c + j < p.cnt)
+#pragma unroll
+                                for (int u = 0; u < MT; ++u) st_cluster(at + (uint32_t)u * block_bytes, z[u][j]);
+                        }
                     }
                 }
                 cluster_sync_all();
-                const int r_lo = mine * own, rows = min(own, p.cnt - r_lo);
+                const int rows = min(own, p.cnt - r_lo);
                 const uint32_t from0 = red + 4u * (uint32_t)f;
-                for (int r = from >> 4; r < rows; r += 2) {
-                    float z[MT][1];
+                for (int r = half_warps * OWN_CHUNK; r < rows; r += 2 * OWN_CHUNK) {
+                    float z[MT][OWN_CHUNK];
 #pragma unroll
-                    for (int u = 0; u < MT; ++u) {
-                        z[u][0] = bz[u];
-                        float sum = __uint_as_float(lds32(from0 + (uint32_t)u * block_bytes + 512u * (uint32_t)r));
-                        for (int s = 1; s < S; ++s)
-                            sum += __uint_as_float(lds32(from0 + (uint32_t)u * block_bytes + (uint32_t)s * part_bytes + 512u * (uint32_t)r));
-                        z[u][0] += sum;
-                    }
-                    if (MT == 2 && !a.gated) store(z[1], z[1], m + a.up, r_lo + r, 1, 1);
-                    store(z[0], z[MT - 1], m, r_lo + r, 1, 1);
+                    for (int u = 0; u < MT; ++u)
+#pragma unroll
+                        for (int j = 0; j < OWN_CHUNK; ++j)   // rows past the last: whatever lies there, not stored
+                            z[u][j] = __uint_as_float(lds32(from0 + (uint32_t)u * block_bytes + 512u * (uint32_t)min(r + j, rows - 1)));
+                    for (int s = 1; s < S; ++s)
+#pragma unroll
+                        for (int u = 0; u < MT; ++u)
+#pragma unroll
+                            for (int j = 0; j < OWN_CHUNK; ++j)
+                                z[u][j] += __uint_as_float(lds32(from0 + (uint32_t)u * block_bytes + (uint32_t)s * part_bytes +
+                                                                 512u * (uint32_t)min(r + j, rows - 1)));
+                    finish(z, mine_ops);
+                    if (r + 2 * OWN_CHUNK < rows) fetch(mine_ops, r_lo + r + 2 * OWN_CHUNK);
+                    put(z, r_lo + r, rows - r);
                 }
             }
             tc_fence_before();
@@ -403,28 +487,28 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
 
 // A shape of the tiles and what the call would take with it.
 struct PairPlan {
-    int mt = 0, bn = 0, split_log2 = 0, clusters = 1;
+    int mt = 0, bn = 0, kt = 0, S = 1, clusters = 1;
     int64_t ns = 0;
 };
 
-// clusters resident at once, of 1, 2, 4 pairs: a property of the device and the kernel, asked for once
-template <bool GATHER, int MT>
+// clusters resident at once, of 1 to 4 pairs: a property of the device and the kernel, asked for once
+template <bool GATHER, int MT, int KT>
 int pair_fit(int dev, const int **fit) {
     static std::mutex mu;
-    static int table[64][3] = {};
+    static int table[64][MAX_S] = {};
     std::lock_guard<std::mutex> lock(mu);
     int *f = table[dev & 63];
-    auto kernel = linear_pair_kernel<GATHER, MT>;
+    auto kernel = linear_pair_kernel<GATHER, MT, KT>;
     if (!f[0]) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pair_smem<GATHER>());
-        for (int i = 2; i >= 0 && e == cudaSuccess; --i) {   // f[0] last: it marks the table as filled
+        for (int i = MAX_S - 1; i >= 0 && e == cudaSuccess; --i) {   // f[0] last: it marks the table as filled
             cudaLaunchConfig_t cfg{};
-            cfg.gridDim = dim3(2u << i);
+            cfg.gridDim = dim3(2u * (i + 1));
             cfg.blockDim = dim3(pair_threads<GATHER>());
             cfg.dynamicSmemBytes = pair_smem<GATHER>();
             cudaLaunchAttribute attr{};
             attr.id = cudaLaunchAttributeClusterDimension;
-            attr.val.clusterDim.x = 2u << i;
+            attr.val.clusterDim.x = 2u * (i + 1);
             attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
             cfg.attrs = &attr;
             cfg.numAttrs = 1;
@@ -440,40 +524,60 @@ int pair_fit(int dev, const int **fit) {
 
 int m_tiles_of(const LinArgs &l, bool gated, int mt) { return (l.d_out + (gated ? 256 : 256 * mt) - 1) / (gated ? 256 : 256 * mt); }
 
+// Two 64-column steps to a ring slot while three slots fit.
+bool two_steps(int mt, int bn) { return mt == 1 ? bn <= 160 : bn <= 64; }
+
 // The best split of k for tiles of bn rows; row_tiles: as many as there may be, likely: as many as are expected.
-template <bool GATHER, int MT>
+template <bool GATHER, int MT, int KT>
 int consider(const LinArgs &l, bool gated, int bn, int64_t row_tiles, int64_t likely, int dev, PairPlan *best) {
     const int *fit = nullptr;
-    const int rc = pair_fit<GATHER, MT>(dev, &fit);
+    const int rc = pair_fit<GATHER, MT, KT>(dev, &fit);
     if (rc != LORA_OK) return rc;
-    const int64_t m = m_tiles_of(l, gated, MT), n_k = (l.d_in + 63) / 64;
+    const int64_t m = m_tiles_of(l, gated, MT), n_k = (l.d_in + 64 * KT - 1) / (64 * KT);
     // a 64-column step: its products, its copies into shared memory, or what a step takes at least (ns)
     const int64_t step = std::max<int64_t>({(int64_t)MT * bn * 21 / 20, (16384 * MT + 64 * bn) / 110, 100});
-    for (int i = 0; i < 3; ++i) {
-        const int s = 1 << i, rows = std::min(bn, l.T);
-        if (s > n_k) break;
+    const int rows = std::min(bn, l.T);
+    for (int s = 1; s <= MAX_S && s <= n_k; ++s) {
         const int64_t tiles = m * row_tiles, expect = m * likely;
-        if (i && tiles > fit[i]) break;   // a cluster that splits k has one tile
-        if (i && bn > 32 && (size_t)own_rows(rows, i) * s * 512 * MT > pair_smem<GATHER>() - 1024) continue;
-        const int64_t clusters = std::min<int64_t>(tiles, fit[i]);
+        if (s > 1 && tiles > fit[s - 1]) break;   // a cluster that splits k has one tile
+        if (s > 1 && bn > 32 && (size_t)own_rows(rows, s) * s * 512 * MT > pair_smem<GATHER>() - 1024) continue;
+        const int64_t clusters = std::min<int64_t>(tiles, fit[s - 1]);
         const int64_t rounds = (expect + clusters - 1) / clusters;
-        const int64_t ns = 4000 + rounds * ((n_k + s - 1) / s * step + 1000) + (i ? 800 * i + 10 * rows * MT : 0);
-        if (!best->mt || ns < best->ns) best->mt = MT, best->bn = bn, best->split_log2 = i, best->clusters = (int)clusters, best->ns = ns;
+        const int64_t sums = 500 + 17 * rows * MT, k_ns = (n_k + s - 1) / s * KT * step;   // a tile's epilogue, its products
+        const int64_t tile_ns = 2 * MT * bn <= 512 ? std::max(k_ns, sums) : k_ns + sums;   // two accumulator buffers or one
+        const int64_t ns = 3500 + rounds * tile_ns + sums + (s > 1 ? 600 + 12 * rows * MT : 0);
+        if (!best->mt || ns < best->ns) best->mt = MT, best->kt = KT, best->bn = bn, best->S = s, best->clusters = (int)clusters, best->ns = ns;
     }
     return LORA_OK;
 }
 
-template <bool GATHER, int MT>
+template <bool GATHER, int MT, int KT>
 int launch_pair(PairArgs &a, const PairPlan &plan, cudaStream_t st) {
-    a.bn = plan.bn, a.split_log2 = plan.split_log2;
+    a.bn = plan.bn, a.S = plan.S;
     a.up = a.gated ? a.l.d_out : 256;
     a.m_tiles = m_tiles_of(a.l, a.gated, MT);
     a.bufs = 2 * MT * plan.bn <= 512 ? 2 : 1;
-    a.own_red = plan.split_log2 > 0 && plan.bn <= 32;
-    const size_t slot = 16384u * MT + 64u * (size_t)plan.bn, red = a.own_red ? (size_t)own_rows(plan.bn, plan.split_log2) * 512 * MT << plan.split_log2 : 0;
+    a.own_red = plan.S > 1 && plan.bn <= 32;
+    a.n_k = (a.l.d_in + 64 * KT - 1) / (64 * KT);
+    const size_t slot = (16384u * MT + 64u * (size_t)plan.bn) * KT, red = a.own_red ? (size_t)own_rows(plan.bn, plan.S) * 512 * MT * plan.S : 0;
     a.stages = (int)std::min<size_t>(PAIR_STAGES, (pair_smem<GATHER>() - 1024 - red) / slot);
-    return launch_after(linear_pair_kernel<GATHER, MT>, dim3((unsigned)(plan.clusters << (plan.split_log2 + 1))), pair_threads<GATHER>(),
-                        pair_smem<GATHER>(), 2u << plan.split_log2, st, a);
+    return launch_after(linear_pair_kernel<GATHER, MT, KT>, dim3((unsigned)(plan.clusters * 2 * plan.S)), pair_threads<GATHER>(),
+                        pair_smem<GATHER>(), 2u * plan.S, st, a);
+}
+
+template <bool GATHER>
+int consider_all(const LinArgs &l, bool gated, int bn, int64_t row_tiles, int64_t likely, int dev, PairPlan *best) {
+    int rc = LORA_OK;
+    if (!gated) rc = two_steps(1, bn) ? consider<GATHER, 1, 2>(l, gated, bn, row_tiles, likely, dev, best)
+                                      : consider<GATHER, 1, 1>(l, gated, bn, row_tiles, likely, dev, best);
+    if (rc != LORA_OK) return rc;
+    return two_steps(2, bn) ? consider<GATHER, 2, 2>(l, gated, bn, row_tiles, likely, dev, best)
+                            : consider<GATHER, 2, 1>(l, gated, bn, row_tiles, likely, dev, best);
+}
+template <bool GATHER>
+int launch_plan(PairArgs &a, const PairPlan &p, cudaStream_t st) {
+    if (p.mt == 1) return p.kt == 1 ? launch_pair<GATHER, 1, 1>(a, p, st) : launch_pair<GATHER, 1, 2>(a, p, st);
+    return p.kt == 1 ? launch_pair<GATHER, 2, 1>(a, p, st) : launch_pair<GATHER, 2, 2>(a, p, st);
 }
 
 int round32(int64_t n) { return (int)((n + 31) / 32 * 32); }
@@ -488,7 +592,6 @@ int launch_linear_tc(const LinArgs &l, int64_t x_rows, bool gated, int dev, int 
     PairArgs a{};
     a.l = l;
     a.gated = gated;
-    a.n_k = (l.d_in + 63) / 64;
     const char *stall = std::getenv("LORA_DEBUG_STALL");   // test hook: the waits of one role run out, after a short while
     a.stall = stall ? std::atoi(stall) : 0;
     a.limit = a.stall ? 64 : WAIT_LIMIT;
@@ -499,14 +602,12 @@ int launch_linear_tc(const LinArgs &l, int64_t x_rows, bool gated, int dev, int 
         const int64_t groups = std::min(l.N, l.T), mean = (l.T + groups - 1) / groups;
         const int bn = std::min(PAIR_ROWS, round32(mean + mean / 2));
         const int64_t row_tiles = l.T / bn + groups, likely = std::max<int64_t>(groups, l.T / bn + groups / 2);
-        if (!gated) rc = consider<true, 1>(l, gated, bn, row_tiles, likely, dev, &best);
-        if (rc == LORA_OK) rc = consider<true, 2>(l, gated, bn, row_tiles, likely, dev, &best);
+        rc = consider_all<true>(l, gated, bn, row_tiles, likely, dev, &best);
     } else {
         const int least = (l.T + PAIR_ROWS - 1) / PAIR_ROWS;
         for (int nt = least; nt <= least + 2 && rc == LORA_OK; ++nt) {   // the fewest row tiles, or a little more that fill the SMs better
             const int bn = round32((l.T + nt - 1) / nt), n = (l.T + bn - 1) / bn;
-            if (!gated) rc = consider<false, 1>(l, gated, bn, n, n, dev, &best);
-            if (rc == LORA_OK) rc = consider<false, 2>(l, gated, bn, n, n, dev, &best);
+            rc = consider_all<false>(l, gated, bn, n, n, dev, &best);
             if (bn == 32) break;
         }
     }
@@ -515,8 +616,7 @@ int launch_linear_tc(const LinArgs &l, int64_t x_rows, bool gated, int dev, int 
     if (rc == LORA_OK && !gather) rc = tensor_map_rows(&a.tmX, l.x, (uint64_t)l.d_in, (uint64_t)l.T, (uint64_t)(l.T > 1 ? l.ld_x : (l.d_in + 7) / 8 * 8), (uint32_t)best.bn / 2);
     if (rc != LORA_OK) return rc;
     a.n_tiles = gather ? 0 : (l.T + best.bn - 1) / best.bn;
-    if (gather) return best.mt == 1 ? launch_pair<true, 1>(a, best, st) : launch_pair<true, 2>(a, best, st);
-    return best.mt == 1 ? launch_pair<false, 1>(a, best, st) : launch_pair<false, 2>(a, best, st);
+    return gather ? launch_plan<true>(a, best, st) : launch_plan<false>(a, best, st);
 }
 
 }  // namespace lora
