@@ -24,11 +24,15 @@ struct LinArgs {
 // ------------------------------------------------------------------ epilogue
 // silu and both gelus as quotients or products without cancellation: z / (1 + e^-z) and z erfc(-z / sqrt 2) / 2 keep their
 // relative accuracy where z is far below 0, which z (1 + erf) / 2 and z (1 + tanh) / 2 lose.
-// FAST (results rounded to bf16): __expf and __fdividef, about 2^-20 relative at |z| <= 20, far below bf16's 2^-9; for
-// fp32 results the accurate functions.
+// FAST (results rounded to bf16): the approximate base-2 exponential and reciprocal, about 2^-20 relative at |z| <= 20, far below
+// bf16's 2^-9; for fp32 results the accurate functions.
 template <bool FAST>
 __device__ __forceinline__ float over_one_plus_exp(float z, float u) {   // z / (1 + e^-u)
-    return FAST ? __fdividef(z, 1.f + __expf(-u)) : z / (1.f + expf(-u));
+    if (!FAST) return z / (1.f + expf(-u));
+    float e, r;   // where e^-u passes fp32's range, the quotient is z times 0
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e) : "f"(-1.4426950408889634f * u));
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(1.f + e));
+    return z * r;
 }
 template <bool FAST, int N>
 __device__ __forceinline__ void activate(int act, float *z) {

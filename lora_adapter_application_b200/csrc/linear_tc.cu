@@ -45,9 +45,11 @@ struct PairArgs {
     int bn;              // rows of a tile
     int m_tiles, n_tiles;   // tiles along the features; along x (plain product)
     int n_k;             // ring slots of k (KT steps of 64 columns each)
-    int stages, bufs;    // ring slots, accumulator buffers
+    int stages;          // ring slots
     int S;               // pairs that split k
     int own_red;         // the partial sums' place is behind the ring
+    uint32_t epi_at;     // the epilogue's, behind both
+    int vec;             // y, addend, residual and bias in 16-byte steps
     unsigned limit;
     int stall;
 };
@@ -76,13 +78,35 @@ struct Tile {
     int m0, e, q0, cnt, n;
 };
 
-// What the epilogue adds to R rows' sums of a thread's MT features: bf16 bits, a register each (two in one would wait for
-// both loads where they are packed).
-template <int MT, int R>
+// What the epilogue adds to a thread's eight columns of a row (of MT feature blocks), and where the row lies.
+template <int MT>
 struct Operands {
-    uint32_t add[MT][R], res[MT][R];
+    uint4 add[MT], res[MT];
+    int64_t row;
 };
-__device__ __forceinline__ uint32_t bf16_bits(const __nv_bfloat16 *p) { return *reinterpret_cast<const unsigned short *>(p); }
+// n (0 to 8) elements at p; vec: 16-byte steps, n is 0 or 8
+__device__ __forceinline__ uint4 load_cols(const __nv_bfloat16 *p, int n, bool vec) {
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (vec) {
+        if (n > 0) u = *reinterpret_cast<const uint4 *>(p);
+    } else {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = i < n ? __bfloat16_as_ushort(p[i]) : 0u;
+        u = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+    }
+    return u;
+}
+__device__ __forceinline__ void store_cols(__nv_bfloat16 *p, const uint4 &u, int n, bool vec) {
+    if (vec) {
+        if (n > 0) *reinterpret_cast<uint4 *>(p) = u;
+    } else {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = __ushort_as_bfloat16((unsigned short)(w[i >> 1] >> (16 * (i & 1))));
+    }
+}
 
 // Rows of a block in the exchange of partial sums: a power of two up to 16, or a multiple of 16, so that 16 rows' owners
 // follow from shifts or are one.
@@ -212,7 +236,7 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
             uniform_wait(a.stall == STALL_MMA ? rest : ready, 0, bound, failed);
             for (int t = cluster; t < tiles && !failed; t += clusters, ++n) {
                 const Tile p = place(t);
-                const int b = a.bufs == 2 ? n & 1 : 0, uses = a.bufs == 2 ? n >> 1 : n;
+                const int b = n & 1, uses = n >> 1;   // accumulator buffer, its earlier uses
                 if (uses > 0 && !uniform_wait(acc_empty(b), (unsigned)(uses - 1) & 1u, bound, failed)) break;
                 tc_fence_after();
                 const uint32_t d = tmem + (uint32_t)(b * MT * a.bn), idesc = pair_idesc(p.n);
@@ -288,120 +312,130 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
         }
         asm volatile("cp.async.wait_all;\n" ::: "memory");
     } else {
-        const int q = warp & 3, f = 32 * q + lane;          // this thread's lane of tensor memory: its feature of the block's 128
-        const int half_warps = warp >= FIRST_EPI + 4;       // which of the two warps of these lanes
-        constexpr int CHUNK = MT == 2 ? 8 : 16;   // rows at a time (8: 16 spill registers)
-        constexpr int OWN_CHUNK = 4;                        // of those that a block owns after an exchange
+        // A warp reads 32 lanes of tensor memory: features f, a row of x in each column.  Through shared memory of its own, eight
+        // rows at a time, a thread gets eight columns of one row, four neighbours the warp's 32: one 16-byte access of each
+        // operand and of y where there were eight of two bytes, each with its address.  (As they lie in tensor memory: 256 rows
+        // 5.5 us for 256 features, and a chunk's operands, loaded one after the other, up to 0.5 us a row.)
+        const int q = warp & 3, f = 32 * q + lane;
+        const int side = warp >= FIRST_EPI + 4;             // which of the two warps of these lanes
+        const int l_row = lane >> 2, l_col = 32 * q + 8 * (lane & 3);   // this thread's row of eight and columns
+        const uint32_t buf = base + a.epi_at + (uint32_t)(warp - FIRST_EPI) * (1024u * MT);
         const LinArgs &l = a.l;
         __nv_bfloat16 *const y = static_cast<__nv_bfloat16 *>(l.y);
         const __nv_bfloat16 *const add = static_cast<const __nv_bfloat16 *>(l.addend);
         const __nv_bfloat16 *const res = static_cast<const __nv_bfloat16 *>(l.residual);
         const __nv_bfloat16 *const bias = static_cast<const __nv_bfloat16 *>(l.bias);
+        const bool vec = a.vec;
         int n = 0;
         for (int t = cluster; t < tiles && !failed; t += clusters, ++n) {
             const Tile p = place(t);
-            const int b = a.bufs == 2 ? n & 1 : 0, uses = a.bufs == 2 ? n >> 1 : n;
-            const int m = p.m0 + 128 * (int)half + f;       // its feature: a column of y; the second block's is m + up
+            const int b = n & 1, uses = n >> 1;   // accumulator buffer, its earlier uses
+            const int m = p.m0 + 128 * (int)half + l_col;   // this thread's columns of y; the second block's are m + up
+            const int n0 = min(8, max(0, l.d_out - m)), n1 = MT == 1 ? 0 : a.gated ? n0 : min(8, max(0, l.d_out - m - a.up));
             const uint32_t acc = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(b * MT * a.bn);
-            float bz[MT];
+            uint4 bz[MT];
 #pragma unroll
-            for (int u = 0; u < MT; ++u) bz[u] = bias && m + u * a.up < l.n_w && m < l.d_out ? load_elem(bias + (int64_t)p.e * l.n_w + m + u * a.up) : 0.f;
+            for (int u = 0; u < MT; ++u)
+                bz[u] = bias ? load_cols(bias + (int64_t)p.e * l.n_w + m + u * a.up, u ? n1 : n0, vec) : make_uint4(0, 0, 0, 0);
 
-            // R rows from tile row r: what the epilogue adds to them, fetched ahead of their sums (rows past the last: the
-            // last one again), for this thread's columns of y
-            auto row = [&](int r) -> int64_t {
-                const int q = p.q0 + min(r, p.cnt - 1);
-                return GATHER ? l.perm[q] : q;
-            };
-            const int cols = MT == 2 && !a.gated ? (m + a.up < l.d_out ? 2 : m < l.d_out) : (m < l.d_out ? 1 : 0);
-            auto fetch = [&](auto &ops, int r) {
-                constexpr int R = sizeof(ops.res[0]) / sizeof(uint32_t);
-                if (cols == 0 || !(add || res)) return;
-                int64_t at[R];
-#pragma unroll
-                for (int j = 0; j < R; ++j) at[j] = row(r + j);
+            auto fetch = [&](Operands<MT> &o, int r) {   // for tile row r (past the last: the last one again)
+                const int at = p.q0 + min(r, p.cnt - 1);
+                o.row = GATHER ? l.perm[at] : at;
                 if (add) {
-#pragma unroll
-                    for (int j = 0; j < R; ++j) ops.add[0][j] = bf16_bits(add + at[j] * l.ld_a + m);
-                    if (MT == 2 && (a.gated || cols == 2))
-#pragma unroll
-                        for (int j = 0; j < R; ++j) ops.add[MT - 1][j] = bf16_bits(add + at[j] * l.ld_a + m + a.up);
+                    o.add[0] = load_cols(add + o.row * l.ld_a + m, n0, vec);
+                    if (MT == 2) o.add[MT - 1] = load_cols(add + o.row * l.ld_a + m + a.up, n1, vec);
                 }
                 if (res) {
-#pragma unroll
-                    for (int j = 0; j < R; ++j) ops.res[0][j] = bf16_bits(res + at[j] * l.ld_r + m);
-                    if (MT == 2 && cols == 2)
-#pragma unroll
-                        for (int j = 0; j < R; ++j) ops.res[MT - 1][j] = bf16_bits(res + at[j] * l.ld_r + m + a.up);
+                    o.res[0] = load_cols(res + o.row * l.ld_r + m, n0, vec);
+                    if (MT == 2 && !a.gated) o.res[MT - 1] = load_cols(res + o.row * l.ld_r + m + a.up, n1, vec);
                 }
             };
-            // the epilogue of R rows' sums, in z
-            auto finish = [&](auto &z, auto &ops) {
-                constexpr int R = sizeof(z[0]) / sizeof(float);
+            auto plus = [](float *z, const uint4 &u) {
+                float v[8];
+                raw_values(u, v);
 #pragma unroll
-                for (int u = 0; u < MT; ++u)
+                for (int i = 0; i < 8; ++i) z[i] += v[i];
+            };
+            auto finish = [&](float (&z)[MT][8], const Operands<MT> &o, bool there) {   // sums of eight columns to y
 #pragma unroll
-                    for (int j = 0; j < R; ++j) z[u][j] += bz[u];
-                if (add)
-#pragma unroll
-                    for (int u = 0; u < MT; ++u)
-#pragma unroll
-                        for (int j = 0; j < R; ++j) z[u][j] += bf16_lo(ops.add[u][j]);
-                activate<true, R>(l.act, z[0]);
+                for (int u = 0; u < MT; ++u) {
+                    if (bias) plus(z[u], bz[u]);
+                    if (add) plus(z[u], o.add[u]);
+                }
+                activate<true, 8>(l.act, z[0]);
+                uint4 out;
+                __nv_bfloat16 *to = y + o.row * l.ld_y + m;
                 if (MT == 2) {
                     if (a.gated) {
 #pragma unroll
-                        for (int j = 0; j < R; ++j) z[0][j] *= z[MT - 1][j];
+                        for (int i = 0; i < 8; ++i) z[0][i] *= z[MT - 1][i];
                     } else {
-                        activate<true, R>(l.act, z[MT - 1]);
+                        activate<true, 8>(l.act, z[MT - 1]);
+                        if (res) plus(z[MT - 1], o.res[MT - 1]);
+                        raw_round(z[MT - 1], out);
+                        if (there) store_cols(to + a.up, out, n1, vec);
                     }
                 }
-                if (res)
-#pragma unroll
-                    for (int u = 0; u < MT; ++u)
-#pragma unroll
-                        for (int j = 0; j < R; ++j) z[u][j] += bf16_lo(ops.res[u][j]);
+                if (res) plus(z[0], o.res[0]);
+                raw_round(z[0], out);
+                if (there) store_cols(to, out, n0, vec);
             };
-            auto put = [&](auto &z, int r, int rows) {
-                constexpr int R = sizeof(z[0]) / sizeof(float);
-#pragma unroll
-                for (int j = 0; j < R; ++j)
-                    if (j < rows && cols) {
-                        __nv_bfloat16 *to = y + row(r + j) * l.ld_y + m;
-                        store_elem(to, z[0][j]);
-                        if (MT == 2 && cols == 2) store_elem(to + a.up, z[MT - 1][j]);
-                    }
+            // eight floats of a row of 128 bytes (buf) or 512 (partial sums); odd rows take their halves the other way round, so
+            // that eight threads meet no bank twice
+            auto load_row = [&](float *z, uint32_t at) {
+                const float4 x = lds128f(at + 16u * (l_row & 1)), w = lds128f(at + 16u * (~l_row & 1));
+                const float4 lo = l_row & 1 ? w : x, hi = l_row & 1 ? x : w;
+                z[0] = lo.x, z[1] = lo.y, z[2] = lo.z, z[3] = lo.w, z[4] = hi.x, z[5] = hi.y, z[6] = hi.z, z[7] = hi.w;
             };
-            // a few rows at a time, the two halves of the warps in turn
-            Operands<MT, CHUNK> ops;
-            Operands<MT, OWN_CHUNK> mine_ops;
-            const int first_row = half_warps * CHUNK, own = own_rows(p.cnt, S), mine = rank >> 1, r_lo = mine * own;
-            if (S > 1) fetch(mine_ops, r_lo + half_warps * OWN_CHUNK);
-            else if (first_row < p.cnt) fetch(ops, first_row);
+            auto drained = [&] {   // this warp's part of the accumulator is in registers
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(map_rank(acc_empty(b), first));
+            };
+            // the two warps of the same lanes take half of the columns each; after an exchange, every other eight rows of the
+            // block's own.  Operands are fetched 16 rows ahead (8: 8192 x 1024 x 4096 with a residual 81 us, without 68), the first before
+            // the sums are there.
+            const int own = own_rows(p.cnt, S), mine = rank >> 1, r_lo = mine * own, rows = min(own, p.cnt - r_lo);
+            const int c_lo = side * (p.n >> 1), c_hi = min(c_lo + (p.n >> 1), p.cnt);
+            Operands<MT> o[2];
+            fetch(o[0], S > 1 ? r_lo + 8 * side + l_row : c_lo + l_row);
+            if (S == 1) fetch(o[1], c_lo + 8 + l_row);
             // S > 1: on to the exchange all the same, which every block of the cluster takes part in
             const bool stall = a.stall == STALL_SUMS && half == 1 && warp == FIRST_EPI;
             if (!lanes_wait(stall ? rest : acc_full(b), (unsigned)uses & 1u, bound, failed) && S == 1) break;
             tc_fence_after();
             if (S == 1) {
-                for (int c = first_row; c < p.cnt; c += 2 * CHUNK) {
-                    float z[MT][CHUNK];
+                for (int c = c_lo; c < c_hi; c += 16) {
+                    float v[MT][16];
 #pragma unroll
-                    for (int u = 0; u < MT; ++u) {
-                        if (CHUNK == 8) tc_ld8(acc + (uint32_t)(u * a.bn + c), z[u]);
-                        else tc_ld16(acc + (uint32_t)(u * a.bn + c), z[u]);
-                    }
+                    for (int u = 0; u < MT; ++u) tc_ld16(acc + (uint32_t)(u * a.bn + c), v[u]);
                     tc_wait_ld();
-                    finish(z, ops);
-                    if (c + 2 * CHUNK < p.cnt) fetch(ops, c + 2 * CHUNK);
-                    put(z, c, p.cnt - c);
+                    if (c + 16 >= c_hi) drained();
+#pragma unroll
+                    for (int h = 0; h < 16; h += 8)
+                        if (c + h < c_hi) {
+                            __syncwarp();
+#pragma unroll
+                            for (int u = 0; u < MT; ++u)
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) sts32(buf + 1024u * u + 128u * j + 4u * lane, __float_as_uint(v[u][h + j]));
+                            __syncwarp();
+                            float z[MT][8];
+#pragma unroll
+                            for (int u = 0; u < MT; ++u) load_row(z[u], buf + 1024u * u + 128u * (uint32_t)l_row + 32u * (lane & 3));
+                            const Operands<MT> now = o[h / 8];
+                            if (c + h + 16 < c_hi) fetch(o[h / 8], c + h + 16 + l_row);
+                            finish(z, now, c + h + l_row < c_hi);
+                        }
                 }
+                if (c_lo >= c_hi) drained();
             } else {
                 const int own_log2 = 31 - __clz(own);
                 // [feature block][source][row of own][128 features], in each owner's shared memory
                 const uint32_t part_bytes = 512u * (uint32_t)own, block_bytes = part_bytes * (uint32_t)S;
                 const uint32_t to0 = red + (uint32_t)mine * part_bytes + 4u * (uint32_t)f;
                 if (!a.own_red) cluster_sync_all();   // every block's products are done with its ring
-                for (int c = 16 * half_warps; c < p.cnt; c += 32) {
+                for (int c = 16 * side; c < p.cnt; c += 32) {
                     float z[MT][16];
 #pragma unroll
                     for (int u = 0; u < MT; ++u) tc_ld16(acc + (uint32_t)(u * a.bn + c), z[u]);
@@ -426,30 +460,25 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
                     }
                 }
                 cluster_sync_all();
-                const int rows = min(own, p.cnt - r_lo);
-                const uint32_t from0 = red + 4u * (uint32_t)f;
-                for (int r = half_warps * OWN_CHUNK; r < rows; r += 2 * OWN_CHUNK) {
-                    float z[MT][OWN_CHUNK];
+                for (int r = 8 * side; r < rows; r += 16) {
+                    const uint32_t at = red + 512u * (uint32_t)min(r + l_row, rows - 1) + 4u * (uint32_t)l_col;
+                    float z[MT][8];
 #pragma unroll
-                    for (int u = 0; u < MT; ++u)
-#pragma unroll
-                        for (int j = 0; j < OWN_CHUNK; ++j)   // rows past the last: whatever lies there, not stored
-                            z[u][j] = __uint_as_float(lds32(from0 + (uint32_t)u * block_bytes + 512u * (uint32_t)min(r + j, rows - 1)));
+                    for (int u = 0; u < MT; ++u) load_row(z[u], at + (uint32_t)u * block_bytes);
                     for (int s = 1; s < S; ++s)
 #pragma unroll
-                        for (int u = 0; u < MT; ++u)
+                        for (int u = 0; u < MT; ++u) {
+                            float v[8];
+                            load_row(v, at + (uint32_t)u * block_bytes + (uint32_t)s * part_bytes);
 #pragma unroll
-                            for (int j = 0; j < OWN_CHUNK; ++j)
-                                z[u][j] += __uint_as_float(lds32(from0 + (uint32_t)u * block_bytes + (uint32_t)s * part_bytes +
-                                                                 512u * (uint32_t)min(r + j, rows - 1)));
-                    finish(z, mine_ops);
-                    if (r + 2 * OWN_CHUNK < rows) fetch(mine_ops, r_lo + r + 2 * OWN_CHUNK);
-                    put(z, r_lo + r, rows - r);
+                            for (int i = 0; i < 8; ++i) z[u][i] += v[i];
+                        }
+                    const Operands<MT> now = o[0];
+                    if (r + 16 < rows) fetch(o[0], r_lo + r + 16 + l_row);
+                    finish(z, now, r + l_row < rows);
                 }
+                drained();
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_rank(acc_empty(b), first));
         }
     }
     // ---------------------------------------------------------------- teardown
@@ -525,7 +554,7 @@ int pair_fit(int dev, const int **fit) {
 int m_tiles_of(const LinArgs &l, bool gated, int mt) { return (l.d_out + (gated ? 256 : 256 * mt) - 1) / (gated ? 256 : 256 * mt); }
 
 // Two 64-column steps to a ring slot while three slots fit.
-bool two_steps(int mt, int bn) { return mt == 1 ? bn <= 160 : bn <= 64; }
+bool two_steps(int mt, int bn) { return mt == 1 ? bn <= 160 : bn <= 32; }
 
 // The best split of k for tiles of bn rows; row_tiles: as many as there may be, likely: as many as are expected.
 template <bool GATHER, int MT, int KT>
@@ -535,7 +564,9 @@ int consider(const LinArgs &l, bool gated, int bn, int64_t row_tiles, int64_t li
     if (rc != LORA_OK) return rc;
     const int64_t m = m_tiles_of(l, gated, MT), n_k = (l.d_in + 64 * KT - 1) / (64 * KT);
     // a 64-column step: its products, its copies into shared memory, or what a step takes at least (ns)
-    const int64_t step = std::max<int64_t>({(int64_t)MT * bn * 21 / 20, (16384 * MT + 64 * bn) / 110, 100});
+    const int64_t step = std::max<int64_t>({(int64_t)MT * bn * 8 / 7, (16384 * MT + 64 * bn) / 112, 90});
+    const int64_t sums = 500 + 25 * bn * MT;   // a tile's epilogue, beside the next tile's products
+    const int64_t hbm = ((int64_t)std::min<int64_t>(l.N, likely) * l.n_w * l.d_in + (int64_t)l.T * (l.d_in + l.d_out)) * 2 / 6400;
     const int rows = std::min(bn, l.T);
     for (int s = 1; s <= MAX_S && s <= n_k; ++s) {
         const int64_t tiles = m * row_tiles, expect = m * likely;
@@ -543,9 +574,8 @@ int consider(const LinArgs &l, bool gated, int bn, int64_t row_tiles, int64_t li
         if (s > 1 && bn > 32 && (size_t)own_rows(rows, s) * s * 512 * MT > pair_smem<GATHER>() - 1024) continue;
         const int64_t clusters = std::min<int64_t>(tiles, fit[s - 1]);
         const int64_t rounds = (expect + clusters - 1) / clusters;
-        const int64_t sums = 500 + 17 * rows * MT, k_ns = (n_k + s - 1) / s * KT * step;   // a tile's epilogue, its products
-        const int64_t tile_ns = 2 * MT * bn <= 512 ? std::max(k_ns, sums) : k_ns + sums;   // two accumulator buffers or one
-        const int64_t ns = 3500 + rounds * tile_ns + sums + (s > 1 ? 600 + 12 * rows * MT : 0);
+        const int64_t k_ns = (n_k + s - 1) / s * KT * step;
+        const int64_t ns = 3500 + std::max(hbm, rounds * std::max(k_ns, sums)) + 14 * rows * MT + (s > 1 ? 500 + 8 * rows * MT : 0);
         if (!best->mt || ns < best->ns) best->mt = MT, best->kt = KT, best->bn = bn, best->S = s, best->clusters = (int)clusters, best->ns = ns;
     }
     return LORA_OK;
@@ -556,21 +586,22 @@ int launch_pair(PairArgs &a, const PairPlan &plan, cudaStream_t st) {
     a.bn = plan.bn, a.S = plan.S;
     a.up = a.gated ? a.l.d_out : 256;
     a.m_tiles = m_tiles_of(a.l, a.gated, MT);
-    a.bufs = 2 * MT * plan.bn <= 512 ? 2 : 1;
-    a.own_red = plan.S > 1 && plan.bn <= 32;
+        a.own_red = plan.S > 1 && plan.bn <= 32;
     a.n_k = (a.l.d_in + 64 * KT - 1) / (64 * KT);
+    a.vec = mx_vec(a.l.y, a.l.ld_y, a.l.d_out, 2) && (!a.l.addend || mx_vec(a.l.addend, a.l.ld_a, a.l.d_out, 2)) &&
+            (!a.l.residual || mx_vec(a.l.residual, a.l.ld_r, a.l.d_out, 2)) && (!a.l.bias || mx_aligned(a.l.bias, 16));
     const size_t slot = (16384u * MT + 64u * (size_t)plan.bn) * KT, red = a.own_red ? (size_t)own_rows(plan.bn, plan.S) * 512 * MT * plan.S : 0;
-    a.stages = (int)std::min<size_t>(PAIR_STAGES, (pair_smem<GATHER>() - 1024 - red) / slot);
+    a.stages = (int)std::min<size_t>(PAIR_STAGES, (pair_smem<GATHER>() - 1024 - EPI_WARPS * 1024 * MT - red) / slot);
+    a.epi_at = (uint32_t)(a.stages * slot + red);
     return launch_after(linear_pair_kernel<GATHER, MT, KT>, dim3((unsigned)(plan.clusters * 2 * plan.S)), pair_threads<GATHER>(),
                         pair_smem<GATHER>(), 2u * plan.S, st, a);
 }
 
 template <bool GATHER>
-int consider_all(const LinArgs &l, bool gated, int bn, int64_t row_tiles, int64_t likely, int dev, PairPlan *best) {
-    int rc = LORA_OK;
-    if (!gated) rc = two_steps(1, bn) ? consider<GATHER, 1, 2>(l, gated, bn, row_tiles, likely, dev, best)
-                                      : consider<GATHER, 1, 1>(l, gated, bn, row_tiles, likely, dev, best);
-    if (rc != LORA_OK) return rc;
+int consider_mt(int mt, const LinArgs &l, bool gated, int bn, int64_t row_tiles, int64_t likely, int dev, PairPlan *best) {
+    if (mt == 1)
+        return two_steps(1, bn) ? consider<GATHER, 1, 2>(l, gated, bn, row_tiles, likely, dev, best)
+                                : consider<GATHER, 1, 1>(l, gated, bn, row_tiles, likely, dev, best);
     return two_steps(2, bn) ? consider<GATHER, 2, 2>(l, gated, bn, row_tiles, likely, dev, best)
                             : consider<GATHER, 2, 1>(l, gated, bn, row_tiles, likely, dev, best);
 }
@@ -598,16 +629,19 @@ int launch_linear_tc(const LinArgs &l, int64_t x_rows, bool gated, int dev, int 
     PairPlan best;
     int rc = LORA_OK;
     const bool gather = l.perm != nullptr;
-    if (gather) {
-        const int64_t groups = std::min(l.N, l.T), mean = (l.T + groups - 1) / groups;
-        const int bn = std::min(PAIR_ROWS, round32(mean + mean / 2));
-        const int64_t row_tiles = l.T / bn + groups, likely = std::max<int64_t>(groups, l.T / bn + groups / 2);
-        rc = consider_all<true>(l, gated, bn, row_tiles, likely, dev, &best);
-    } else {
-        const int least = (l.T + PAIR_ROWS - 1) / PAIR_ROWS;
+    for (int mt = gated ? 2 : 1; mt <= 2 && rc == LORA_OK; ++mt) {
+        // rows that two accumulator buffers hold: with one (MT = 2, 256 rows) 8192 x 4096 x 2 x 14336 took 1380 us for 1200
+        const int most = PAIR_ROWS / mt;
+        if (gather) {   // tiles that most groups fit in
+            const int64_t groups = std::min(l.N, l.T), mean = (l.T + groups - 1) / groups;
+            const int bn = std::min(most, round32(mean + mean / 2));
+            rc = consider_mt<true>(mt, l, gated, bn, l.T / bn + groups, std::max<int64_t>(groups, l.T / bn + groups / 2), dev, &best);
+            continue;
+        }
+        const int least = (l.T + most - 1) / most;
         for (int nt = least; nt <= least + 2 && rc == LORA_OK; ++nt) {   // the fewest row tiles, or a little more that fill the SMs better
             const int bn = round32((l.T + nt - 1) / nt), n = (l.T + bn - 1) / bn;
-            rc = consider_all<false>(l, gated, bn, n, n, dev, &best);
+            rc = consider_mt<false>(mt, l, gated, bn, n, n, dev, &best);
             if (bn == 32) break;
         }
     }
