@@ -32,8 +32,7 @@ int launch_dense(const LinArgs &a, int64_t x_rows, bool gated, lora_dtype dtype,
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return cuda_rc(e);
-    if (dtype == LORA_BF16 && linear_tc_ok(a, x_rows)) return launch_linear_tc(a, x_rows, gated, dev, sms, st);
-    return launch_linear_simt(a, dtype == LORA_BF16, gated, sms, st);
+    return dtype == LORA_BF16 ? launch_linear_tc(a, x_rows, gated, dev, st) : launch_linear_simt(a, gated, sms, st);
 }
 
 }  // namespace

@@ -99,11 +99,10 @@ constexpr int MAX_EXPERTS = LORA_MAX_EXPERTS;
 int tensor_map_rows(CUtensorMap *out, const void *base, uint64_t inner, uint64_t rows, uint64_t row_stride,
                     uint32_t box_rows);
 
-// linear_tc.cu: bf16, rows of x and W in steps of 16 bytes, any y; x_rows: rows that x has
-bool linear_tc_ok(const LinArgs &a, int64_t x_rows);
-int launch_linear_tc(const LinArgs &a, int64_t x_rows, bool gated, int dev, int sms, cudaStream_t st);
+// linear_tc.cu: bf16, any stride and alignment; x_rows: rows that x has
+int launch_linear_tc(const LinArgs &a, int64_t x_rows, bool gated, int dev, cudaStream_t st);
 
-// linear_simt.cu: any type, stride and alignment
-int launch_linear_simt(const LinArgs &a, bool bf16, bool gated, int sms, cudaStream_t st);
+// linear_simt.cu: fp32, any stride and alignment
+int launch_linear_simt(const LinArgs &a, bool gated, int sms, cudaStream_t st);
 
 }  // namespace lora

@@ -11,7 +11,7 @@
 // split k, each cluster has one tile, and its blocks add their sums, in rank order, through distributed shared memory.
 //
 // Warp 0 copies W's boxes (and x's, plain product) by TMA; warp 1 of the first block of a pair issues the MMAs; eight warps
-// read the accumulators (lane = feature, column = row of x), apply the epilogue and store.  Experts (GATHER): four more
+// read the accumulators (lane = feature, column = row of x), apply the epilogue and store.  Experts (GATHERED): four more
 // warps copy the group's rows of x, wherever they lie, with cp.async into the same swizzle, 16 bytes a lane (gather4
 // copies of four rows x 128 bytes would be 32 a stage; a TMA copy costs its warp 40-60 ns); they count on the block's own
 // barrier, and warp 1 of the second block passes the word on to the first.
@@ -29,12 +29,17 @@ namespace {
 constexpr int PAIR_STAGES = 12;
 constexpr int PAIR_ROWS = 256;    // widest tile of x rows
 constexpr int MAX_S = 4;          // most pairs that split k: clusters of eight blocks
-constexpr int EPI_WARPS = 8, GATHER_WARPS = 4;
-template <bool GATHER>
-constexpr int pair_threads() { return 32 * (2 + EPI_WARPS + (GATHER ? GATHER_WARPS : 0)); }
+// How a kernel's operands come: W and x by TMA; the experts' W by TMA, their rows of x by cp.async; both through registers
+// (rows off 16-byte steps, with or without experts).
+enum { PLAIN = 0, GATHERED = 1, LOADED = 2 };
+constexpr int EPI_WARPS = 8;
+template <int MODE>
+constexpr int load_warps() { return MODE == PLAIN ? 0 : MODE == GATHERED ? 4 : 8; }
+template <int MODE>
+constexpr int pair_threads() { return 32 * (2 + EPI_WARPS + load_warps<MODE>()); }
 // dynamic shared memory, all that the experts' table of 4 KB or the barriers leave: one block an SM, as its tensor memory asks for
-template <bool GATHER>
-constexpr size_t pair_smem() { return (GATHER ? 221 : 226) * 1024; }
+template <int MODE>
+constexpr size_t pair_smem() { return (MODE == PLAIN ? 226 : 221) * 1024; }
 enum { STALL_MMA = 1, STALL_ROWS = 2, STALL_COPY = 3, STALL_SUMS = 4, STALL_COPY_FIRST = 5 };   // LORA_DEBUG_STALL
 
 struct PairArgs {
@@ -118,14 +123,32 @@ __host__ __device__ __forceinline__ int own_rows(int rows, int S) {
     return own;
 }
 
-template <bool GATHER, int MT, int KT>
-__global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(const __grid_constant__ PairArgs a) {
+// 16 bytes from byte o (even) of 32: a, then b
+__device__ __forceinline__ uint4 shift_bytes(const uint4 &a, const uint4 &b, uint32_t o) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = o & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = o & 4 ? w[i + 1] : w[i];
+    const uint32_t s = (o & 2) * 8;
+    return make_uint4(__funnelshift_r(w[0], w[1], s), __funnelshift_r(w[1], w[2], s), __funnelshift_r(w[2], w[3], s),
+                      __funnelshift_r(w[3], w[4], s));
+}
+__device__ __forceinline__ uint4 shfl4(const uint4 &v, int from) {
+    return make_uint4(__shfl_sync(FULL, v.x, from), __shfl_sync(FULL, v.y, from), __shfl_sync(FULL, v.z, from),
+                      __shfl_sync(FULL, v.w, from));
+}
+
+template <int MODE, int MT, int KT>
+__global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(const __grid_constant__ PairArgs a) {
+    constexpr bool ROWS = MODE != PLAIN;   // x comes by warps
     extern __shared__ __align__(1024) unsigned char lin_sm[];
     __shared__ uint32_t tmem_sm;
     __shared__ __align__(8) uint64_t bars[4 * PAIR_STAGES + 6];
     __shared__ uint32_t stop_sm, used_sm;   // used_sm: ring uses that this block's copies have begun
-    __shared__ int pre[GATHER ? MAX_EXPERTS + 1 : 1], part[GATHER ? 32 : 1];
-    constexpr int FIRST_EPI = GATHER ? 2 + GATHER_WARPS : 2;
+    __shared__ int pre[ROWS ? MAX_EXPERTS + 1 : 1], part[ROWS ? 32 : 1];
+    constexpr int FIRST_EPI = 2 + load_warps<MODE>();
+    const bool grouped = MODE == GATHERED || (MODE == LOADED && a.l.perm);
     const int warp = __shfl_sync(FULL, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t w_bytes = 16384u * MT * KT, x_bytes = 64u * (uint32_t)a.bn, slot_bytes = w_bytes + x_bytes * KT;
     const uint32_t base = (smem_u32(lin_sm) + 1023u) & ~1023u, red = base + (a.own_red ? (uint32_t)a.stages * slot_bytes : 0u);
@@ -148,12 +171,12 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
     if (warp == 0) {
         for (int i = lane; i < 4 * PAIR_STAGES + 6; i += 32) {
             const bool rows = i >= 2 * PAIR_STAGES && i < 3 * PAIR_STAGES, drained = i >= 4 * PAIR_STAGES + 2 && i < 4 * PAIR_STAGES + 4;
-            mbar_init(bar(i), rows ? 32 * GATHER_WARPS : drained ? 2 * EPI_WARPS : 1);
+            mbar_init(bar(i), rows ? (MODE == GATHERED ? 32 : 1) * max(1, load_warps<MODE>()) : drained ? 2 * EPI_WARPS : 1);
         }
         if (lane == 0) {
             stop_sm = 0, used_sm = 0;
-            prefetch_tmap(&a.tmW);
-            if (!GATHER) prefetch_tmap(&a.tmX);
+            if (MODE != LOADED) prefetch_tmap(&a.tmW);
+            if (MODE == PLAIN) prefetch_tmap(&a.tmX);
         }
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
@@ -176,7 +199,7 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
         if (warp == 1 && half == 1 && elect_one()) mbar_arrive_peer(map_rank(ready, first));
     }
     int tiles = a.m_tiles * a.n_tiles;
-    if (GATHER) {
+    if (grouped) {
         count_tiles(a.l.seg_start, a.l.N, a.bn, pre, part);
         tiles = a.m_tiles * pre[a.l.N];
     }
@@ -186,7 +209,7 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
     auto place = [&](int t) {
         Tile p;
         int mi, rows;
-        if (GATHER) {
+        if (grouped) {
             p.e = expert_of(pre, a.l.N, t / a.m_tiles);
             const int n = pre[p.e + 1] - pre[p.e], left = t - pre[p.e] * a.m_tiles;
             mi = left / n;
@@ -205,9 +228,9 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
         p.m0 = mi * (a.gated ? 256 : 256 * MT);
         return p;
     };
-    const uint32_t tx = 2u * (GATHER ? w_bytes : slot_bytes);
+    const uint32_t tx = 2u * (MODE == GATHERED ? w_bytes : slot_bytes);
 
-    if (warp == 0) {
+    if (MODE != LOADED && warp == 0) {
         Ring ring(a.stages);
         if (a.stall == (half ? STALL_COPY : STALL_COPY_FIRST)) uniform_wait(rest, 0, bound, failed);
         for (int t = cluster; t < tiles && !failed; t += clusters) {
@@ -222,7 +245,7 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
                     for (int u = 0; u < MT; ++u)
 #pragma unroll
                         for (int i = 0; i < KT; ++i) tma_2d_pair(slot + 16384u * (u + MT * i), &a.tmW, 64 * (k * KT + i), w0 + u * a.up, b);
-                    if (!GATHER)
+                    if (MODE == PLAIN)
 #pragma unroll
                         for (int i = 0; i < KT; ++i) tma_2d_pair(slot + w_bytes + x_bytes * i, &a.tmX, 64 * (k * KT + i), x0, b);
                 }
@@ -242,15 +265,15 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
                 const uint32_t d = tmem + (uint32_t)(b * MT * a.bn), idesc = pair_idesc(p.n);
                 for (int k = k_lo; k < k_hi; ++k, ring.next()) {
                     const int s = ring.slot;
-                    if (!uniform_wait(full(s), ring.parity, bound, failed)) break;
-                    if (GATHER) {
+                    if (MODE != LOADED && !uniform_wait(full(s), ring.parity, bound, failed)) break;
+                    if (ROWS) {
                         if (!uniform_wait(rows_in(s), ring.parity, bound, failed) || !uniform_wait(peer_rows(s), ring.parity, bound, failed))
                             break;
                     }
                     tc_fence_after();
                     const uint32_t slot = base + (uint32_t)s * slot_bytes;
                     if (elect_one()) {
-                        if (GATHER) fence_proxy_async();   // rows came by cp.async (generic proxy), the MMA reads them as operands
+                        if (MODE == GATHERED) fence_proxy_async();   // rows came by cp.async (generic proxy), the MMA reads them as operands
 #pragma unroll
                         for (int x = 0; x < KT; ++x) {
                             const uint64_t dx = desc_sw128(slot + w_bytes + x_bytes * x);
@@ -267,18 +290,18 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
                 }
                 if (elect_one()) tc_commit_pair(acc_full(b), first);
             }
-        } else if (GATHER) {
+        } else if (ROWS) {
             Ring ring(a.stages);
             for (int t = cluster; t < tiles && !failed; t += clusters)
                 for (int k = k_lo; k < k_hi; ++k, ring.next()) {
                     if (!uniform_wait(rows_in(ring.slot), ring.parity, bound, failed)) break;
                     if (elect_one()) {
-                        fence_proxy_async();
+                        if (MODE == GATHERED) fence_proxy_async();
                         mbar_arrive_peer(map_rank(peer_rows(ring.slot), first));
                     }
                 }
         }
-    } else if (GATHER && warp < FIRST_EPI) {
+    } else if (MODE == GATHERED && warp >= 2 && warp < FIRST_EPI) {
         // Lane l of warp w copies columns 8 (l % 8) .. of rows 16 i + 4 (w - 2) + l / 8 of this block's half.  Rows past the
         // group's last are not read: what the slot holds there only enters columns of the accumulator that no one stores.
         const int r0 = 4 * (warp - 2) + (lane >> 3), col = 8 * (lane & 7);
@@ -311,7 +334,72 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
             }
         }
         asm volatile("cp.async.wait_all;\n" ::: "memory");
-    } else {
+    } else if (MODE == LOADED && warp >= 2 && warp < FIRST_EPI) {
+        // Rows at any (even) address: eight lanes read the aligned 16-byte pieces around 64 columns of a row, a ninth piece comes
+        // from a load that a warp makes once for all its rows, and each lane shifts two neighbouring pieces into the 16 bytes
+        // that the operand's swizzle wants.  Pieces that hold no column of the row are not read.  Loads go out ahead of the
+        // wait for the slot; a slot's 32 KB in flight bound it.
+        constexpr int W_IT = 4 * MT, X_IT = PAIR_ROWS / MT / 2 / 32, ITS = W_IT + X_IT, EXTRA = (ITS + 7) / 8;
+        const int lw = warp - 2, lr = lane >> 3, c = lane & 7;   // rows 4 (lw + 8 i) + lr of W's, then of x's
+        Ring ring(a.stages);
+        if (a.stall == STALL_ROWS && half && warp == 2) uniform_wait(rest, 0, bound, failed);
+        for (int t = cluster; t < tiles && !failed; t += clusters) {
+            const Tile p = place(t);
+            const int own = p.n >> 1, in = min(own, p.cnt - (int)half * own);   // rows of this half, of them there
+            const char *src[ITS];   // rows' first bytes; what is not there reads a row that is
+#pragma unroll
+            for (int i = 0; i < ITS; ++i) {
+                if (i < W_IT) {
+                    const int f = 4 * (lw + 8 * (i & 3)) + lr;
+                    const int64_t row = (int64_t)p.e * a.l.n_w + p.m0 + 128 * (int)half + f + (i >> 2) * a.up;
+                    src[i] = reinterpret_cast<const char *>(static_cast<const __nv_bfloat16 *>(a.l.w) +
+                                                            min(row, (int64_t)a.l.N * a.l.n_w - 1) * a.l.ld_w);
+                } else {
+                    const int r = 4 * (lw + 8 * (i - W_IT)) + lr, q = p.q0 + (in > 0 ? (int)half * own + min(r, in - 1) : 0);
+                    src[i] = reinterpret_cast<const char *>(static_cast<const __nv_bfloat16 *>(a.l.x) +
+                                                            (int64_t)(grouped ? a.l.perm[q] / a.l.x_div : q) * a.l.ld_x);
+                }
+            }
+            const char *more[EXTRA];   // lane 4 i + r: row r of turn i (then i + 8)
+#pragma unroll
+            for (int x = 0; x < EXTRA; ++x) {
+                more[x] = nullptr;
+#pragma unroll
+                for (int i = 8 * x; i < (ITS < 8 * x + 8 ? ITS : 8 * x + 8); ++i) {
+                    const uint64_t got = __shfl_sync(FULL, reinterpret_cast<uint64_t>(src[i]), 8 * (lane & 3));
+                    if (lane >> 2 == (i & 7)) more[x] = reinterpret_cast<const char *>(got);
+                }
+            }
+            const int64_t row_bytes = 2 * (int64_t)a.l.d_in;
+            auto piece = [&](const char *row, int64_t at) {   // the aligned 16 bytes around byte `at` of a row
+                const char *s = reinterpret_cast<const char *>(reinterpret_cast<uint64_t>(row + at) & ~15ull);
+                return row && s < row + row_bytes ? *reinterpret_cast<const uint4 *>(s) : make_uint4(0, 0, 0, 0);
+            };
+            for (int k = k_lo; k < k_hi; ++k, ring.next()) {
+                uint4 v[ITS], ninth[EXTRA];
+#pragma unroll
+                for (int i = 0; i < ITS; ++i)
+                    if (i < W_IT || 32 * (i - W_IT) < own) v[i] = piece(src[i], 128 * (int64_t)k + 16 * c);
+#pragma unroll
+                for (int x = 0; x < EXTRA; ++x) ninth[x] = piece(more[x], 128 * (int64_t)k + 128);
+                if (ring.reused() && !uniform_wait(empty(ring.slot), ring.parity ^ 1u, bound, failed)) break;
+                const uint32_t slot = base + (uint32_t)ring.slot * slot_bytes;
+                const int keep = max(0, min(8, a.l.d_in - 64 * k - 8 * c));   // columns past d_in: zeros on both sides
+#pragma unroll
+                for (int i = 0; i < ITS; ++i)
+                    if (i < W_IT || 32 * (i - W_IT) < own) {
+                        const uint4 up = shfl4(v[i], (lane + 1) & 31), last = shfl4(ninth[i >> 3], 4 * (i & 7) + lr);
+                        const uint4 out = keep8(shift_bytes(v[i], c == 7 ? last : up, (uint32_t)reinterpret_cast<uint64_t>(src[i]) & 15u), keep);
+                        const int r = 4 * (lw + 8 * (i < W_IT ? i & 3 : i - W_IT)) + lr;
+                        const uint32_t at = slot + (i < W_IT ? 16384u * (i >> 2) : w_bytes) + 128u * (uint32_t)r;
+                        if (i < W_IT || r < own) sts128(at + (uint32_t)((c ^ (r & 7)) << 4), out);
+                    }
+                fence_proxy_async();   // the MMA reads what these stores wrote
+                __syncwarp();
+                if (elect_one()) mbar_arrive(rows_in(ring.slot));
+            }
+        }
+    } else if (warp >= FIRST_EPI) {
         // A warp reads 32 lanes of tensor memory: features f, a row of x in each column.  Through shared memory of its own, eight
         // rows at a time, a thread gets eight columns of one row, four neighbours the warp's 32: one 16-byte access of each
         // operand and of y where there were eight of two bytes, each with its address.  (As they lie in tensor memory: 256 rows
@@ -340,7 +428,7 @@ __global__ void __launch_bounds__(pair_threads<GATHER>(), 1) linear_pair_kernel(
 
             auto fetch = [&](Operands<MT> &o, int r) {   // for tile row r (past the last: the last one again)
                 const int at = p.q0 + min(r, p.cnt - 1);
-                o.row = GATHER ? l.perm[at] : at;
+                o.row = grouped ? l.perm[at] : at;
                 if (add) {
                     o.add[0] = load_cols(add + o.row * l.ld_a + m, n0, vec);
                     if (MT == 2) o.add[MT - 1] = load_cols(add + o.row * l.ld_a + m + a.up, n1, vec);
@@ -521,20 +609,20 @@ struct PairPlan {
 };
 
 // clusters resident at once, of 1 to 4 pairs: a property of the device and the kernel, asked for once
-template <bool GATHER, int MT, int KT>
+template <int MODE, int MT, int KT>
 int pair_fit(int dev, const int **fit) {
     static std::mutex mu;
     static int table[64][MAX_S] = {};
     std::lock_guard<std::mutex> lock(mu);
     int *f = table[dev & 63];
-    auto kernel = linear_pair_kernel<GATHER, MT, KT>;
+    auto kernel = linear_pair_kernel<MODE, MT, KT>;
     if (!f[0]) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pair_smem<GATHER>());
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pair_smem<MODE>());
         for (int i = MAX_S - 1; i >= 0 && e == cudaSuccess; --i) {   // f[0] last: it marks the table as filled
             cudaLaunchConfig_t cfg{};
             cfg.gridDim = dim3(2u * (i + 1));
-            cfg.blockDim = dim3(pair_threads<GATHER>());
-            cfg.dynamicSmemBytes = pair_smem<GATHER>();
+            cfg.blockDim = dim3(pair_threads<MODE>());
+            cfg.dynamicSmemBytes = pair_smem<MODE>();
             cudaLaunchAttribute attr{};
             attr.id = cudaLaunchAttributeClusterDimension;
             attr.val.clusterDim.x = 2u * (i + 1);
@@ -557,21 +645,21 @@ int m_tiles_of(const LinArgs &l, bool gated, int mt) { return (l.d_out + (gated 
 bool two_steps(int mt, int bn) { return mt == 1 ? bn <= 160 : bn <= 32; }
 
 // The best split of k for tiles of bn rows; row_tiles: as many as there may be, likely: as many as are expected.
-template <bool GATHER, int MT, int KT>
+template <int MODE, int MT, int KT>
 int consider(const LinArgs &l, bool gated, int bn, int64_t row_tiles, int64_t likely, int dev, PairPlan *best) {
     const int *fit = nullptr;
-    const int rc = pair_fit<GATHER, MT, KT>(dev, &fit);
+    const int rc = pair_fit<MODE, MT, KT>(dev, &fit);
     if (rc != LORA_OK) return rc;
     const int64_t m = m_tiles_of(l, gated, MT), n_k = (l.d_in + 64 * KT - 1) / (64 * KT);
     // a 64-column step: its products, its copies into shared memory, or what a step takes at least (ns)
-    const int64_t step = std::max<int64_t>({(int64_t)MT * bn * 8 / 7, (16384 * MT + 64 * bn) / 112, 90});
+    const int64_t step = std::max<int64_t>({(int64_t)MT * bn * 8 / 7, (16384 * MT + 64 * bn) / 112, MODE == LOADED ? 1000 : 90});
     const int64_t sums = 500 + 25 * bn * MT;   // a tile's epilogue, beside the next tile's products
     const int64_t hbm = ((int64_t)std::min<int64_t>(l.N, likely) * l.n_w * l.d_in + (int64_t)l.T * (l.d_in + l.d_out)) * 2 / 6400;
     const int rows = std::min(bn, l.T);
     for (int s = 1; s <= MAX_S && s <= n_k; ++s) {
         const int64_t tiles = m * row_tiles, expect = m * likely;
         if (s > 1 && tiles > fit[s - 1]) break;   // a cluster that splits k has one tile
-        if (s > 1 && bn > 32 && (size_t)own_rows(rows, s) * s * 512 * MT > pair_smem<GATHER>() - 1024) continue;
+        if (s > 1 && bn > 32 && (size_t)own_rows(rows, s) * s * 512 * MT > pair_smem<MODE>() - 1024) continue;
         const int64_t clusters = std::min<int64_t>(tiles, fit[s - 1]);
         const int64_t rounds = (expect + clusters - 1) / clusters;
         const int64_t k_ns = (n_k + s - 1) / s * KT * step;
@@ -581,7 +669,7 @@ int consider(const LinArgs &l, bool gated, int bn, int64_t row_tiles, int64_t li
     return LORA_OK;
 }
 
-template <bool GATHER, int MT, int KT>
+template <int MODE, int MT, int KT>
 int launch_pair(PairArgs &a, const PairPlan &plan, cudaStream_t st) {
     a.bn = plan.bn, a.S = plan.S;
     a.up = a.gated ? a.l.d_out : 256;
@@ -591,35 +679,49 @@ int launch_pair(PairArgs &a, const PairPlan &plan, cudaStream_t st) {
     a.vec = mx_vec(a.l.y, a.l.ld_y, a.l.d_out, 2) && (!a.l.addend || mx_vec(a.l.addend, a.l.ld_a, a.l.d_out, 2)) &&
             (!a.l.residual || mx_vec(a.l.residual, a.l.ld_r, a.l.d_out, 2)) && (!a.l.bias || mx_aligned(a.l.bias, 16));
     const size_t slot = (16384u * MT + 64u * (size_t)plan.bn) * KT, red = a.own_red ? (size_t)own_rows(plan.bn, plan.S) * 512 * MT * plan.S : 0;
-    a.stages = (int)std::min<size_t>(PAIR_STAGES, (pair_smem<GATHER>() - 1024 - EPI_WARPS * 1024 * MT - red) / slot);
+    a.stages = (int)std::min<size_t>(PAIR_STAGES, (pair_smem<MODE>() - 1024 - EPI_WARPS * 1024 * MT - red) / slot);
     a.epi_at = (uint32_t)(a.stages * slot + red);
-    return launch_after(linear_pair_kernel<GATHER, MT, KT>, dim3((unsigned)(plan.clusters * 2 * plan.S)), pair_threads<GATHER>(),
-                        pair_smem<GATHER>(), 2u * plan.S, st, a);
+    return launch_after(linear_pair_kernel<MODE, MT, KT>, dim3((unsigned)(plan.clusters * 2 * plan.S)), pair_threads<MODE>(),
+                        pair_smem<MODE>(), 2u * plan.S, st, a);
 }
 
-template <bool GATHER>
+template <int MODE>
 int consider_mt(int mt, const LinArgs &l, bool gated, int bn, int64_t row_tiles, int64_t likely, int dev, PairPlan *best) {
-    if (mt == 1)
-        return two_steps(1, bn) ? consider<GATHER, 1, 2>(l, gated, bn, row_tiles, likely, dev, best)
-                                : consider<GATHER, 1, 1>(l, gated, bn, row_tiles, likely, dev, best);
-    return two_steps(2, bn) ? consider<GATHER, 2, 2>(l, gated, bn, row_tiles, likely, dev, best)
-                            : consider<GATHER, 2, 1>(l, gated, bn, row_tiles, likely, dev, best);
+    if constexpr (MODE == LOADED) {
+        return mt == 1 ? consider<MODE, 1, 1>(l, gated, bn, row_tiles, likely, dev, best)
+                       : consider<MODE, 2, 1>(l, gated, bn, row_tiles, likely, dev, best);
+    } else {
+        if (mt == 1)
+            return two_steps(1, bn) ? consider<MODE, 1, 2>(l, gated, bn, row_tiles, likely, dev, best)
+                                    : consider<MODE, 1, 1>(l, gated, bn, row_tiles, likely, dev, best);
+        return two_steps(2, bn) ? consider<MODE, 2, 2>(l, gated, bn, row_tiles, likely, dev, best)
+                                : consider<MODE, 2, 1>(l, gated, bn, row_tiles, likely, dev, best);
+    }
 }
-template <bool GATHER>
+template <int MODE>
 int launch_plan(PairArgs &a, const PairPlan &p, cudaStream_t st) {
-    if (p.mt == 1) return p.kt == 1 ? launch_pair<GATHER, 1, 1>(a, p, st) : launch_pair<GATHER, 1, 2>(a, p, st);
-    return p.kt == 1 ? launch_pair<GATHER, 2, 1>(a, p, st) : launch_pair<GATHER, 2, 2>(a, p, st);
+    if constexpr (MODE == LOADED) {
+        return p.mt == 1 ? launch_pair<MODE, 1, 1>(a, p, st) : launch_pair<MODE, 2, 1>(a, p, st);
+    } else {
+        if (p.mt == 1) return p.kt == 1 ? launch_pair<MODE, 1, 1>(a, p, st) : launch_pair<MODE, 1, 2>(a, p, st);
+        return p.kt == 1 ? launch_pair<MODE, 2, 1>(a, p, st) : launch_pair<MODE, 2, 2>(a, p, st);
+    }
 }
 
 int round32(int64_t n) { return (int)((n + 31) / 32 * 32); }
 
 }  // namespace
 
-bool linear_tc_ok(const LinArgs &a, int64_t x_rows) {
+namespace {
+
+// Rows of x and W in the 16-byte steps that TMA and 16-byte copies take.
+bool whole_steps(const LinArgs &a, int64_t x_rows) {
     return (a.d_in & 7) == 0 && (x_rows <= 1 || (a.ld_x & 7) == 0) && (a.ld_w & 7) == 0 && mx_aligned(a.x, 16) && mx_aligned(a.w, 16);
 }
 
-int launch_linear_tc(const LinArgs &l, int64_t x_rows, bool gated, int dev, int sms, cudaStream_t st) {
+}  // namespace
+
+int launch_linear_tc(const LinArgs &l, int64_t x_rows, bool gated, int dev, cudaStream_t st) {
     PairArgs a{};
     a.l = l;
     a.gated = gated;
@@ -629,28 +731,36 @@ int launch_linear_tc(const LinArgs &l, int64_t x_rows, bool gated, int dev, int 
     PairPlan best;
     int rc = LORA_OK;
     const bool gather = l.perm != nullptr;
+    const int mode = !whole_steps(l, x_rows) ? LOADED : gather ? GATHERED : PLAIN;
+    auto consider_tiles = [&](int mt, int bn, int64_t tiles, int64_t likely) {
+        if (mode == LOADED) return consider_mt<LOADED>(mt, l, gated, bn, tiles, likely, dev, &best);
+        return mode == GATHERED ? consider_mt<GATHERED>(mt, l, gated, bn, tiles, likely, dev, &best)
+                                : consider_mt<PLAIN>(mt, l, gated, bn, tiles, likely, dev, &best);
+    };
     for (int mt = gated ? 2 : 1; mt <= 2 && rc == LORA_OK; ++mt) {
         // rows that two accumulator buffers hold: with one (MT = 2, 256 rows) 8192 x 4096 x 2 x 14336 took 1380 us for 1200
         const int most = PAIR_ROWS / mt;
         if (gather) {   // tiles that most groups fit in
             const int64_t groups = std::min(l.N, l.T), mean = (l.T + groups - 1) / groups;
             const int bn = std::min(most, round32(mean + mean / 2));
-            rc = consider_mt<true>(mt, l, gated, bn, l.T / bn + groups, std::max<int64_t>(groups, l.T / bn + groups / 2), dev, &best);
+            rc = consider_tiles(mt, bn, l.T / bn + groups, std::max<int64_t>(groups, l.T / bn + groups / 2));
             continue;
         }
         const int least = (l.T + most - 1) / most;
         for (int nt = least; nt <= least + 2 && rc == LORA_OK; ++nt) {   // the fewest row tiles, or a little more that fill the SMs better
             const int bn = round32((l.T + nt - 1) / nt), n = (l.T + bn - 1) / bn;
-            rc = consider_mt<false>(mt, l, gated, bn, n, n, dev, &best);
+            rc = consider_tiles(mt, bn, n, n);
             if (bn == 32) break;
         }
     }
     if (rc != LORA_OK) return rc;
-    rc = tensor_map_rows(&a.tmW, l.w, (uint64_t)l.d_in, (uint64_t)l.N * l.n_w, (uint64_t)l.ld_w, 128);
-    if (rc == LORA_OK && !gather) rc = tensor_map_rows(&a.tmX, l.x, (uint64_t)l.d_in, (uint64_t)l.T, (uint64_t)(l.T > 1 ? l.ld_x : (l.d_in + 7) / 8 * 8), (uint32_t)best.bn / 2);
+    if (mode != LOADED) rc = tensor_map_rows(&a.tmW, l.w, (uint64_t)l.d_in, (uint64_t)l.N * l.n_w, (uint64_t)l.ld_w, 128);
+    if (rc == LORA_OK && mode == PLAIN)   // one row's stride is of no use, and need not be one that a map takes
+        rc = tensor_map_rows(&a.tmX, l.x, (uint64_t)l.d_in, (uint64_t)l.T, (uint64_t)(l.T > 1 ? l.ld_x : l.d_in), (uint32_t)best.bn / 2);
     if (rc != LORA_OK) return rc;
     a.n_tiles = gather ? 0 : (l.T + best.bn - 1) / best.bn;
-    return gather ? launch_plan<true>(a, best, st) : launch_plan<false>(a, best, st);
+    if (mode == LOADED) return launch_plan<LOADED>(a, best, st);
+    return mode == GATHERED ? launch_plan<GATHERED>(a, best, st) : launch_plan<PLAIN>(a, best, st);
 }
 
 }  // namespace lora

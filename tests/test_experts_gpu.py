@@ -152,7 +152,8 @@ def _experts_check(seed, slots, N, d, n, dtype, kind="spread", x_div=1, gated=Fa
 
 SHAPES = [(1, 1, 8, 8), (1, 8, 64, 128), (2, 3, 72, 136), (16, 8, 4096, 512), (33, 4, 256, 264), (64, 64, 128, 128), (100, 7, 200, 40),
           (128, 2, 1024, 256), (200, 1, 512, 384), (257, 3, 264, 520), (300, 5, 1003, 77), (512, 128, 256, 136),
-          (1000, 16, 128, 1000), (777, 1024, 64, 24), (2000, 8, 512, 512), (4096, 64, 264, 128), (3001, 2, 72, 2056)]
+          (1000, 16, 128, 1000), (777, 1024, 64, 24), (2000, 8, 512, 512), (4096, 64, 264, 128), (3001, 2, 72, 2056), (2000, 9, 333, 257),
+          (1200, 2, 1001, 600), (50, 6, 2047, 130)]
 
 
 @pytest.mark.parametrize("gated", [False, True])

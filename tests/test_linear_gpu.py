@@ -50,7 +50,8 @@ SHAPES = [(1, 1, 1), (1, 8, 8), (1, 64, 128), (1, 4096, 4096), (2, 72, 136), (3,
           (129, 4096, 128), (144, 320, 648), (160, 512, 3000), (176, 640, 8), (191, 128, 264), (192, 256, 256),
           (193, 128, 128), (224, 4096, 4096), (240, 72, 4104), (255, 264, 264), (256, 256, 256), (257, 1408, 384),
           (300, 264, 520), (384, 1024, 2048), (500, 3000, 704), (512, 64, 64), (513, 8, 8), (1000, 1152, 1000),
-          (1024, 512, 2304), (2049, 128, 40), (4096, 256, 512), (5000, 304, 3000), (8192, 64, 264)]
+          (1024, 512, 2304), (2049, 128, 40), (4096, 256, 512), (5000, 304, 3000), (8192, 64, 264),
+          (40, 4097, 1001), (300, 1003, 520), (520, 65, 257), (1030, 777, 1001), (2100, 129, 4099), (260, 8191, 129)]
 
 
 @pytest.mark.parametrize("gated", [False, True])
