@@ -1,7 +1,7 @@
 // The dense products of fp32 data (contract: lora_linear and lora_expert_linear in lora_delta.h), on the ordinary
 // arithmetic units: fp32 products, no tf32; any stride and alignment.
 //
-//   few rows    a warp takes four features (gated: two of each half) x eight rows, its lanes split k: W is read once for
+//   few rows    a warp takes two features (gated: one of each half) x eight rows, its lanes split k: W is read once for
 //               eight rows, bound by HBM
 //   many rows   a block takes a tile of rows x features, 8 x 8 or 4 x 4 sums a thread, both operands through shared memory;
 //               bound by the arithmetic units (128 fused multiply-adds a clock and SM)
@@ -62,7 +62,7 @@ __device__ __forceinline__ void load4(const float *p, int n, bool vec, float *v)
 }
 
 // ---------------------------------------------------------------- few rows
-constexpr int DOT_ROWS = 8, DOT_FEATURES = 4, DOT_WARPS = 8;
+constexpr int DOT_ROWS = 8, DOT_FEATURES = 2, DOT_WARPS = 8;
 
 template <bool GATED>
 __global__ void __launch_bounds__(32 * DOT_WARPS) linear_dot_kernel(const LinArgs a, int vec) {
@@ -90,20 +90,25 @@ __global__ void __launch_bounds__(32 * DOT_WARPS) linear_dot_kernel(const LinArg
         xp[i] = static_cast<const float *>(a.x) + (int64_t)(a.perm ? slot[i] / a.x_div : q) * a.ld_x;
     }
     float acc[DOT_ROWS][DOT_FEATURES] = {};
-#pragma unroll 2
-    for (int k = 4 * lane; k < a.d_in; k += 128) {
-        const int n = a.d_in - k;
-        float wv[DOT_FEATURES][4], xv[4];
+    constexpr int STEPS = 4;   // of 128 columns, whose W is under way at once
+    for (int k0 = 4 * lane; k0 < a.d_in; k0 += 128 * STEPS) {
+        float wv[STEPS][DOT_FEATURES][4];
 #pragma unroll
-        for (int f = 0; f < DOT_FEATURES; ++f) load4(wp[f] + k, n, vec, wv[f]);
+        for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+            for (int f = 0; f < DOT_FEATURES; ++f) load4(wp[f] + (k0 + 128 * s), a.d_in - k0 - 128 * s, vec, wv[s][f]);
 #pragma unroll
         for (int i = 0; i < DOT_ROWS; ++i) {
             if (i >= r.cnt) break;
-            load4(xp[i] + k, n, vec, xv);
 #pragma unroll
-            for (int f = 0; f < DOT_FEATURES; ++f)
+            for (int s = 0; s < STEPS; ++s) {
+                float xv[4];
+                load4(xp[i] + (k0 + 128 * s), a.d_in - k0 - 128 * s, vec, xv);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][f] = fmaf(wv[f][j], xv[j], acc[i][f]);
+                for (int f = 0; f < DOT_FEATURES; ++f)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[i][f] = fmaf(wv[s][f][j], xv[j], acc[i][f]);
+            }
         }
     }
 #pragma unroll
@@ -124,16 +129,25 @@ __global__ void __launch_bounds__(32 * DOT_WARPS) linear_dot_kernel(const LinArg
 }
 
 // --------------------------------------------------------------- many rows
-// BM rows x BN features of W (gated: BN / 2 of each half), TM x TN sums a thread, k in tiles of 32 that cp.async brings into
+// BM rows x BN features of W (gated: BN / 2 of each half), TM x TN sums a thread, KG groups of threads that take a part of each
+// k tile each (where tiles are few: more warps on an SM) and add their sums at the end, in order; k in tiles of 32 that cp.async brings into
 // a ring of STAGES: 16 bytes a copy, or 4 where rows are off 16-byte steps.  Rows lie 36 floats apart: a thread reads four
 // k of a row at once, eight neighbours eight rows of W in eight different bank groups.  A thread's features are BN / TN
 // apart, so a gated tile's gate and up sums of a column meet in one thread, and neighbours store neighbouring columns.
 constexpr int TILE_K = 32, TILE_LD = 36;
 
-template <bool GATED, int BM, int BN, int TM, int TN, int STAGES>
-__global__ void __launch_bounds__((BM / TM) * (BN / TN)) linear_tile_kernel(const LinArgs a, int vec) {
-    constexpr int THREADS = (BM / TM) * (BN / TN), ROWS = BM + BN, TX = BN / TN, H = BN / 2;
-    static_assert(TN % 2 == 0 && 32 % TX == 0, "gate and up in one thread, whole rows of threads in a warp");
+// two fused multiply-adds in one instruction, each rounded as its own
+__device__ __forceinline__ void fma2(uint64_t &acc, uint64_t x, uint64_t w) {
+    asm("fma.rn.f32x2 %0, %1, %2, %0;\n" : "+l"(acc) : "l"(x), "l"(w));
+}
+__device__ __forceinline__ float sum2(uint64_t v) {
+    return __uint_as_float((uint32_t)v) + __uint_as_float((uint32_t)(v >> 32));
+}
+
+template <bool GATED, int BM, int BN, int TM, int TN, int KG, int STAGES>
+__global__ void __launch_bounds__(KG * (BM / TM) * (BN / TN)) linear_tile_kernel(const LinArgs a, int vec) {
+    constexpr int GROUP = (BM / TM) * (BN / TN), THREADS = KG * GROUP, ROWS = BM + BN, TX = BN / TN, H = BN / 2;
+    static_assert(TN % 2 == 0 && TX % 8 == 0 && GROUP % 32 == 0 && BM / TM % 4 == 0, "gate and up in one thread, whole warps");
     extern __shared__ __align__(16) float lin_tiles[];   // [STAGES][ROWS][TILE_LD]
     __shared__ int pre[MAX_EXPERTS + 1], part[32];
     __shared__ const float *src[ROWS];   // rows of x, then of W
@@ -143,7 +157,8 @@ __global__ void __launch_bounds__((BM / TM) * (BN / TN)) linear_tile_kernel(cons
     if (!block_rows(a, (int)blockIdx.x, BM, pre, part, &r)) return;
     constexpr int COLS = GATED ? H : BN;                    // columns of y of this block
     const int c0 = (int)blockIdx.y * COLS, tid = threadIdx.x;
-    const int tx = tid % TX, ty = tid / TX;
+    // a warp is 8 threads along the features x 4 along the rows: 8 + 4 rows of 16 bytes a step where 16 + 2 would be more
+    const int group = tid / GROUP, g_warp = tid % GROUP / 32, tx = tid % 8 + g_warp % (TX / 8) * 8, ty = tid % 32 / 8 + g_warp / (TX / 8) * 4;
     for (int i = tid; i < ROWS; i += THREADS) {   // rows past the last read the last one
         if (i < BM) {
             const int q = r.q0 + min(i, r.cnt - 1);
@@ -180,31 +195,48 @@ __global__ void __launch_bounds__((BM / TM) * (BN / TN)) linear_tile_kernel(cons
         }
         asm volatile("cp.async.commit_group;\n" ::: "memory");
     };
-    float acc[TM][TN] = {};
+    uint64_t acc[TM][TN] = {};   // pairs of sums, of the even and the odd k
 #pragma unroll
     for (int k = 0; k < STAGES - 1; ++k) fetch(k);
     for (int k = 0; k < n_k; ++k) {
         asm volatile("cp.async.wait_group %0;\n" ::"n"(STAGES - 2) : "memory");
         __syncthreads();   // tile k is there for all, and all are done with tile k - 1, whose place the next one takes
         fetch(k + STAGES - 1);
-        const float *xs = lin_tiles + (k % STAGES) * ROWS * TILE_LD, *ws = xs + BM * TILE_LD;
+        const float *xs = lin_tiles + (k % STAGES) * ROWS * TILE_LD + group * (TILE_K / KG), *ws = xs + BM * TILE_LD;
+#pragma unroll 4
+        for (int kk = 0; kk < TILE_K / KG; kk += 4) {
+            ulonglong2 xf[TM], wf[TN];
 #pragma unroll
-        for (int kk = 0; kk < TILE_K; kk += 4) {
-            float4 xf[TM], wf[TN];
+            for (int i = 0; i < TM; ++i) xf[i] = *reinterpret_cast<const ulonglong2 *>(xs + (ty + i * (BM / TM)) * TILE_LD + kk);
 #pragma unroll
-            for (int i = 0; i < TM; ++i) xf[i] = *reinterpret_cast<const float4 *>(xs + (ty + i * (BM / TM)) * TILE_LD + kk);
-#pragma unroll
-            for (int j = 0; j < TN; ++j) wf[j] = *reinterpret_cast<const float4 *>(ws + (tx + j * TX) * TILE_LD + kk);
+            for (int j = 0; j < TN; ++j) wf[j] = *reinterpret_cast<const ulonglong2 *>(ws + (tx + j * TX) * TILE_LD + kk);
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int j = 0; j < TN; ++j) {
-                    acc[i][j] = fmaf(xf[i].x, wf[j].x, acc[i][j]);
-                    acc[i][j] = fmaf(xf[i].y, wf[j].y, acc[i][j]);
-                    acc[i][j] = fmaf(xf[i].z, wf[j].z, acc[i][j]);
-                    acc[i][j] = fmaf(xf[i].w, wf[j].w, acc[i][j]);
-                }
+                for (int j = 0; j < TN; ++j) fma2(acc[i][j], xf[i].x, wf[j].x);
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) fma2(acc[i][j], xf[i].y, wf[j].y);
         }
+    }
+    float sum[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) sum[i][j] = sum2(acc[i][j]);
+    if (KG > 1) {
+        static_assert((KG - 1) * GROUP * TM * TN <= STAGES * ROWS * TILE_LD, "the groups' sums fit the ring");
+        asm volatile("cp.async.wait_all;\n" ::: "memory");
+        __syncthreads();   // all are done with the ring
+        if (group > 0)
+#pragma unroll
+            for (int i = 0; i < TM * TN; ++i) lin_tiles[((group - 1) * TM * TN + i) * GROUP + tid % GROUP] = sum[i / TN][i % TN];
+        __syncthreads();
+        if (group > 0) return;
+        for (int g = 0; g < KG - 1; ++g)
+#pragma unroll
+            for (int i = 0; i < TM * TN; ++i) sum[i / TN][i % TN] += lin_tiles[(g * TM * TN + i) * GROUP + tid];
     }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -214,19 +246,19 @@ __global__ void __launch_bounds__((BM / TM) * (BN / TN)) linear_tile_kernel(cons
 #pragma unroll
         for (int j = 0; j < (GATED ? TN / 2 : TN); ++j) {
             const int c = c0 + tx + j * TX;
-            if (c < a.d_out) finish<GATED>(a, row, r.e, c, acc[i][j], GATED ? acc[i][TN / 2 + j] : 0.f);
+            if (c < a.d_out) finish<GATED>(a, row, r.e, c, sum[i][j], GATED ? sum[i][TN / 2 + j] : 0.f);
         }
     }
 }
 
-template <bool GATED, int BM, int BN, int TM, int TN, int STAGES>
+template <bool GATED, int BM, int BN, int TM, int TN, int KG, int STAGES>
 int launch_tile(const LinArgs &a, int vec, int row_tiles, cudaStream_t st) {
     constexpr int COLS = GATED ? BN / 2 : BN;
     constexpr size_t SMEM = (size_t)STAGES * (BM + BN) * TILE_LD * sizeof(float);
-    auto kernel = linear_tile_kernel<GATED, BM, BN, TM, TN, STAGES>;
+    auto kernel = linear_tile_kernel<GATED, BM, BN, TM, TN, KG, STAGES>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
     if (e != cudaSuccess) return cuda_rc(e);
-    return launch_after(kernel, dim3(row_tiles, (a.d_out + COLS - 1) / COLS), (BM / TM) * (BN / TN), SMEM, 0, st, a, vec);
+    return launch_after(kernel, dim3(row_tiles, (a.d_out + COLS - 1) / COLS), KG * (BM / TM) * (BN / TN), SMEM, 0, st, a, vec);
 }
 
 template <bool GATED>
@@ -242,9 +274,9 @@ int launch_as(const LinArgs &a, int sms, cudaStream_t st) {
     }
     // the largest tile that gives every SM one
     auto tiles = [&](int bm, int bn) { return (int64_t)row_tiles(bm) * ((a.n_w + bn - 1) / bn); };
-    if (per_group > 64 && tiles(128, 128) >= sms) return launch_tile<GATED, 128, 128, 8, 8, 3>(a, vec, row_tiles(128), st);
-    if (per_group > 32 && tiles(64, 64) >= sms) return launch_tile<GATED, 64, 64, 4, 4, 4>(a, vec, row_tiles(64), st);
-    return launch_tile<GATED, 32, 64, 4, 4, 4>(a, vec, row_tiles(32), st);
+    if (per_group > 64 && tiles(128, 64) >= sms) return launch_tile<GATED, 128, 64, 8, 4, 1, 3>(a, vec, row_tiles(128), st);
+    if (per_group > 32 && tiles(64, 64) >= sms) return launch_tile<GATED, 64, 64, 4, 4, 1, 3>(a, vec, row_tiles(64), st);
+    return launch_tile<GATED, 32, 64, 4, 4, 4, 4>(a, vec, row_tiles(32), st);
 }
 
 }  // namespace
