@@ -84,7 +84,10 @@
  *                       context stays usable).  In lora_mx_linear (1 to 5) one warp waits
  *                       for what never comes, in place of its first wait: the products'
  *                       (1), one of the scales' (2), one of the sums' (4), either of two
- *                       that copy (3, 5); its other waits are as short.
+ *                       that copy (3, 5); its other waits are as short.  In lora_linear and
+ *                       lora_expert_linear over bf16: the products' (1), one that brings rows
+ *                       of x where warps do (2), one of the sums' (4), either of two that copy
+ *                       boxes (3, 5).
  */
 #ifndef LORA_DELTA_H
 #define LORA_DELTA_H

@@ -10,9 +10,10 @@ namespace {
 
 // ------------------------------------------------------------------ route
 // A warp takes a token; its lanes hold the logits, expert 32 i + lane in key[i], as whole numbers that order as the logits
-// do, 0 for those that cannot be chosen.  A pick is two warp reductions in hardware: the largest key, and the first
-// expert that holds it.  The weights come from the picks' logits, so that ids depend on comparisons alone.
-// Bound: latency (1 token), then the picks' reductions.
+// do, 0 for those that cannot be chosen.  A pick is one warp reduction in hardware for bf16 logits, whose 16 bits share a
+// key with the expert's complement (the largest key is the first expert's of the largest logit), two for fp32: the largest
+// key, and the first expert that holds it.  The weights come from the picks' logits, so that ids depend on comparisons
+// alone.  Bound: latency (1 token), then the picks' instructions (8192 x 256 bf16, 8 of them: KERNEL_US).
 constexpr int ROUTE_WARPS = 4;
 
 __device__ __forceinline__ uint32_t order_key(float l) {
@@ -32,24 +33,27 @@ __device__ __forceinline__ float warp_sum(float v) {
 template <typename E, int VPL>
 __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_kernel(int32_t *ids, float *weights, const E *logits, int64_t ld, int T,
                                                                  int n, int k, int sigmoid, int renorm, float scale) {
+    constexpr bool SHARED_KEY = sizeof(E) == 2;
     pdl_next();
     pdl_wait();
     const int t = (int)blockIdx.x * ROUTE_WARPS + (int)(threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (t >= T) return;
     const E *row = logits + t * ld;
-    uint32_t key[VPL];
+    // the logit of a key: its high 16 bits, the rest as order_key leaves it for a bf16 value
+    auto value = [](uint32_t key) { return key_value(SHARED_KEY ? (key & 0xffff0000u) | (key >> 31 ? 0u : 0xffffu) : key); };
+    uint32_t key[VPL], top = 0;   // top: the largest of this lane's
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) key[i] = 32 * i + lane < n ? order_key(load_elem(row + 32 * i + lane)) : 0u;
-    uint32_t top = 0;   // the largest key of this lane's
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) top = max(top, key[i]);
-    const uint32_t first = __reduce_max_sync(FULL, top);
-    const float most = key_value(first);   // of no use where first is 0: then nothing is chosen
+    for (int i = 0; i < VPL; ++i) {
+        key[i] = 32 * i + lane < n ? order_key(load_elem(row + 32 * i + lane)) : 0u;
+        if (SHARED_KEY && key[i]) key[i] = (key[i] & 0xffff0000u) | (0xffffu ^ (uint32_t)(32 * i + lane));
+        top = max(top, key[i]);
+    }
+    const float most = value(__reduce_max_sync(FULL, top));   // of no use where no expert is open: then nothing is chosen
     float all = 0.f;
     if (!sigmoid && !renorm) {   // the softmax's sum over all experts
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            if (key[i]) all += exp_below(key_value(key[i]), most);
+            if (key[i]) all += exp_below(value(key[i]), most);
         all = warp_sum(all);
     }
     uint32_t my_key = 0;   // lane j: the j-th pick
@@ -57,11 +61,16 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_kernel(int32_t *ids, f
     for (int j = 0; j < k; ++j) {
         const uint32_t best = __reduce_max_sync(FULL, top);
         if (best == 0) break;
-        int at = VPL;
+        int id;
+        if (SHARED_KEY) {
+            id = (int)(0xffffu ^ (best & 0xffffu));
+        } else {
+            int at = VPL;
 #pragma unroll
-        for (int i = VPL - 1; i >= 0; --i)
-            if (key[i] == best) at = i;
-        const int id = (int)__reduce_min_sync(FULL, at < VPL ? (unsigned)(32 * at + lane) : 0xffffffffu);
+            for (int i = VPL - 1; i >= 0; --i)
+                if (key[i] == best) at = i;
+            id = (int)__reduce_min_sync(FULL, at < VPL ? (unsigned)(32 * at + lane) : 0xffffffffu);
+        }
         if (lane == j) my_key = best, my_id = id;
         if ((id & 31) == lane) {
             top = 0;
@@ -72,7 +81,7 @@ __global__ void __launch_bounds__(32 * ROUTE_WARPS) route_kernel(int32_t *ids, f
             }
         }
     }
-    const float l = key_value(my_key);
+    const float l = value(my_key);
     float w = 0.f;
     if (my_id >= 0) {
         if (!sigmoid) {
@@ -106,63 +115,73 @@ int launch_route(int32_t *ids, float *weights, const void *logits, int64_t ld, i
 }
 
 // -------------------------------------------------------------------- sum
-// A thread takes eight columns of a token (VEC: 16-byte accesses; else columns a block apart) and adds the slots' rows
-// in slot order, fp32, one rounding.  Four rows' loads are in flight at a time.  Bound: HBM.
-constexpr int SUM_THREADS = 128;
+// A warp takes 256 columns of a few tokens, eight a lane (VEC: 16-byte accesses; else 32 columns apart), and adds the slots'
+// rows in slot order, fp32, one rounding.  The tokens' ids and weights come in one load of the warp, ahead of all; four
+// rows' loads are in flight at a time.  Bound: HBM.
+constexpr int SUM_WARPS = 4, SUM_TOKENS = 4;
 
 template <typename E, bool VEC>
-__global__ void __launch_bounds__(SUM_THREADS) sum_kernel(E *y, int64_t ld_y, const E *x, int64_t ld_x, const int32_t *ids,
-                                                          const float *weights, int n, int k, int d, const E *res, int64_t ld_r) {
+__global__ void __launch_bounds__(32 * SUM_WARPS) sum_kernel(E *y, int64_t ld_y, const E *x, int64_t ld_x, const int32_t *ids,
+                                                             const float *weights, int n, int T, int k, int tokens, int d, const E *res,
+                                                             int64_t ld_r) {
     pdl_next();
     pdl_wait();
     using Raw = typename RawOf<E>::type;
-    const int64_t t = blockIdx.x;
+    const int64_t t0 = (int64_t)blockIdx.x * tokens;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c0 = ((int)blockIdx.y * (SUM_THREADS / 32) + warp) * 256;   // the warp's 256 columns
+    const int c0 = ((int)blockIdx.y * SUM_WARPS + warp) * 256;   // the warp's 256 columns
     if (c0 >= d) return;
-    float acc[8], v[8];
-    if (res) {
-        Raw u;
-        load8<VEC>(res + t * ld_r, c0, d, lane, u);
-        raw_values(u, acc);
-    } else {
+    const int here = min(tokens, (int)(T - t0));
+    // tokens * k <= 32, or one token of up to 32 slots: lane l has slot l
+    const int my_id = lane < here * k ? ids[t0 * k + lane] : -1;
+    const float my_w = lane < here * k ? weights[t0 * k + lane] : 0.f;
+    for (int i = 0; i < here; ++i) {
+        const int64_t t = t0 + i;
+        float acc[8], v[8];
+        if (res) {
+            Raw u;
+            load8<VEC>(res + t * ld_r, c0, d, lane, u);
+            raw_values(u, acc);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = 0.f;
-    }
-    for (int j = 0; j < k; j += 4) {
-        Raw u[4];
-        float w[4];
-        bool there[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t slot = t * k + j + i;
-            const int id = j + i < k ? ids[slot] : -1;
-            there[i] = id >= 0 && id < n;
-            if (there[i]) {   // the rows of slots without an expert hold nothing of use: not read
-                w[i] = weights[slot];
-                load8<VEC>(x + slot * ld_x, c0, d, lane, u[i]);
-            }
+            for (int c = 0; c < 8; ++c) acc[c] = 0.f;
         }
+        for (int j = 0; j < k; j += 4) {
+            Raw u[4];
+            float w[4];
+            bool there[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (there[i]) {
-                raw_values(u[i], v);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) acc[c] = fmaf(w[i], v[c], acc[c]);
+            for (int s = 0; s < 4; ++s) {
+                const int at = min(i * k + j + s, 31);
+                const int id = __shfl_sync(FULL, my_id, at);
+                w[s] = __shfl_sync(FULL, my_w, at);
+                there[s] = j + s < k && id >= 0 && id < n;
+                // the rows of slots without an expert hold nothing of use: not read
+                if (there[s]) load8<VEC>(x + (t * k + j + s) * ld_x, c0, d, lane, u[s]);
             }
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+                if (there[s]) {
+                    raw_values(u[s], v);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) acc[c] = fmaf(w[s], v[c], acc[c]);
+                }
+        }
+        Raw u;
+        raw_round(acc, u);
+        store8<VEC>(y + t * ld_y, c0, d, lane, u);
     }
-    Raw u;
-    raw_round(acc, u);
-    store8<VEC>(y + t * ld_y, c0, d, lane, u);
 }
 
 template <typename E>
 int launch_sum(void *y, int64_t ld_y, const void *x, int64_t ld_x, const int32_t *ids, const float *weights, int n, int T, int k,
                int d, const void *res, int64_t ld_r, cudaStream_t st) {
     const bool vec = mx_vec(x, ld_x, d, sizeof(E)) && mx_vec(y, ld_y, d, sizeof(E)) && (!res || mx_vec(res, ld_r, d, sizeof(E)));
-    const dim3 grid((unsigned)T, (unsigned)((d + 8 * SUM_THREADS - 1) / (8 * SUM_THREADS)));
-    return launch_after(vec ? sum_kernel<E, true> : sum_kernel<E, false>, grid, SUM_THREADS, 0, 0, st, static_cast<E *>(y), ld_y,
-                        static_cast<const E *>(x), ld_x, ids, weights, n, k, d, static_cast<const E *>(res), ld_r);
+    // several tokens a warp only where many: a block of one token lives mostly for the latency of its ids
+    const int tokens = T >= 4096 ? std::max(1, std::min(SUM_TOKENS, 32 / k)) : 1;
+    const dim3 grid((unsigned)((T + tokens - 1) / tokens), (unsigned)((d + 256 * SUM_WARPS - 1) / (256 * SUM_WARPS)));
+    return launch_after(vec ? sum_kernel<E, true> : sum_kernel<E, false>, grid, 32 * SUM_WARPS, 0, 0, st, static_cast<E *>(y), ld_y,
+                        static_cast<const E *>(x), ld_x, ids, weights, n, T, k, tokens, d, static_cast<const E *>(res), ld_r);
 }
 
 }  // namespace

@@ -65,15 +65,16 @@ __device__ __forceinline__ void load4(const float *p, int n, bool vec, float *v)
 constexpr int DOT_ROWS = 8, DOT_FEATURES = 2, DOT_WARPS = 8;
 
 template <bool GATED>
-__global__ void __launch_bounds__(32 * DOT_WARPS) linear_dot_kernel(const LinArgs a, int vec) {
+__global__ void __launch_bounds__(32 * DOT_WARPS) linear_dot_kernel(const LinArgs a, int vec, int row_tiles) {
     __shared__ int pre[MAX_EXPERTS + 1], part[32];
     pdl_next();
     pdl_wait();
     Rows r;
-    if (!block_rows(a, (int)blockIdx.x, DOT_ROWS, pre, part, &r)) return;
+    const int block = (int)blockIdx.x / row_tiles;   // row tiles of the same features beside each other
+    if (!block_rows(a, (int)blockIdx.x - block * row_tiles, DOT_ROWS, pre, part, &r)) return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int COLS = GATED ? DOT_FEATURES / 2 : DOT_FEATURES;   // of y, a warp
-    const int c0 = ((int)blockIdx.y * DOT_WARPS + warp) * COLS;
+    const int c0 = (block * DOT_WARPS + warp) * COLS;
     if (c0 >= a.d_out) return;
     const float *w = static_cast<const float *>(a.w) + (int64_t)r.e * a.n_w * a.ld_w;
     const float *wp[DOT_FEATURES], *xp[DOT_ROWS];
@@ -131,11 +132,9 @@ __global__ void __launch_bounds__(32 * DOT_WARPS) linear_dot_kernel(const LinArg
 // --------------------------------------------------------------- many rows
 // BM rows x BN features of W (gated: BN / 2 of each half), TM x TN sums a thread, KG groups of threads that take a part of each
 // k tile each (where tiles are few: more warps on an SM) and add their sums at the end, in order; k in tiles of 32 that cp.async brings into
-// a ring of STAGES: 16 bytes a copy, or 4 where rows are off 16-byte steps.  Rows lie 36 floats apart: a thread reads four
+// a ring of STAGES: 16 bytes a copy, or 4 where rows are off 16-byte steps.  Rows lie TILE_K + 4 floats apart: a thread reads four
 // k of a row at once, eight neighbours eight rows of W in eight different bank groups.  A thread's features are BN / TN
 // apart, so a gated tile's gate and up sums of a column meet in one thread, and neighbours store neighbouring columns.
-constexpr int TILE_K = 32, TILE_LD = 36;
-
 // two fused multiply-adds in one instruction, each rounded as its own
 __device__ __forceinline__ void fma2(uint64_t &acc, uint64_t x, uint64_t w) {
     asm("fma.rn.f32x2 %0, %1, %2, %0;\n" : "+l"(acc) : "l"(x), "l"(w));
@@ -144,9 +143,9 @@ __device__ __forceinline__ float sum2(uint64_t v) {
     return __uint_as_float((uint32_t)v) + __uint_as_float((uint32_t)(v >> 32));
 }
 
-template <bool GATED, int BM, int BN, int TM, int TN, int KG, int STAGES>
+template <bool GATED, int BM, int BN, int TM, int TN, int KG, int TILE_K, int STAGES>
 __global__ void __launch_bounds__(KG * (BM / TM) * (BN / TN)) linear_tile_kernel(const LinArgs a, int vec) {
-    constexpr int GROUP = (BM / TM) * (BN / TN), THREADS = KG * GROUP, ROWS = BM + BN, TX = BN / TN, H = BN / 2;
+    constexpr int GROUP = (BM / TM) * (BN / TN), THREADS = KG * GROUP, ROWS = BM + BN, TX = BN / TN, H = BN / 2, TILE_LD = TILE_K + 4;
     static_assert(TN % 2 == 0 && TX % 8 == 0 && GROUP % 32 == 0 && BM / TM % 4 == 0, "gate and up in one thread, whole warps");
     extern __shared__ __align__(16) float lin_tiles[];   // [STAGES][ROWS][TILE_LD]
     __shared__ int pre[MAX_EXPERTS + 1], part[32];
@@ -251,11 +250,11 @@ __global__ void __launch_bounds__(KG * (BM / TM) * (BN / TN)) linear_tile_kernel
     }
 }
 
-template <bool GATED, int BM, int BN, int TM, int TN, int KG, int STAGES>
+template <bool GATED, int BM, int BN, int TM, int TN, int KG, int TILE_K, int STAGES>
 int launch_tile(const LinArgs &a, int vec, int row_tiles, cudaStream_t st) {
     constexpr int COLS = GATED ? BN / 2 : BN;
-    constexpr size_t SMEM = (size_t)STAGES * (BM + BN) * TILE_LD * sizeof(float);
-    auto kernel = linear_tile_kernel<GATED, BM, BN, TM, TN, KG, STAGES>;
+    constexpr size_t SMEM = (size_t)STAGES * (BM + BN) * (TILE_K + 4) * sizeof(float);
+    auto kernel = linear_tile_kernel<GATED, BM, BN, TM, TN, KG, TILE_K, STAGES>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
     if (e != cudaSuccess) return cuda_rc(e);
     return launch_after(kernel, dim3(row_tiles, (a.d_out + COLS - 1) / COLS), KG * (BM / TM) * (BN / TN), SMEM, 0, st, a, vec);
@@ -269,14 +268,14 @@ int launch_as(const LinArgs &a, int sms, cudaStream_t st) {
     const int per_group = a.perm ? (a.T + a.N - 1) / a.N : a.T;
     if (per_group <= 2 * DOT_ROWS) {
         const int cols = DOT_WARPS * DOT_FEATURES / (GATED ? 2 : 1);
-        return launch_after(linear_dot_kernel<GATED>, dim3(row_tiles(DOT_ROWS), (a.d_out + cols - 1) / cols), 32 * DOT_WARPS, 0, 0, st,
-                            a, vec);
+        const int tiles = row_tiles(DOT_ROWS);   // at most 3072 of them, and 65536 blocks of features
+        return launch_after(linear_dot_kernel<GATED>, dim3(tiles * ((a.d_out + cols - 1) / cols)), 32 * DOT_WARPS, 0, 0, st, a, vec, tiles);
     }
     // the largest tile that gives every SM one
     auto tiles = [&](int bm, int bn) { return (int64_t)row_tiles(bm) * ((a.n_w + bn - 1) / bn); };
-    if (per_group > 64 && tiles(128, 64) >= sms) return launch_tile<GATED, 128, 64, 8, 4, 1, 3>(a, vec, row_tiles(128), st);
-    if (per_group > 32 && tiles(64, 64) >= sms) return launch_tile<GATED, 64, 64, 4, 4, 1, 3>(a, vec, row_tiles(64), st);
-    return launch_tile<GATED, 32, 64, 4, 4, 4, 4>(a, vec, row_tiles(32), st);
+    if (per_group > 64 && tiles(128, 64) >= sms) return launch_tile<GATED, 128, 64, 8, 4, 1, 32, 3>(a, vec, row_tiles(128), st);
+    if (per_group > 32 && tiles(64, 64) >= sms) return launch_tile<GATED, 64, 64, 8, 4, 2, 32, 3>(a, vec, row_tiles(64), st);
+    return launch_tile<GATED, 32, 64, 4, 4, 4, 64, 3>(a, vec, row_tiles(32), st);
 }
 
 }  // namespace

@@ -308,17 +308,23 @@ __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(co
         const uint32_t at = (uint32_t)r0 * 128u + (uint32_t)(((lane & 7) ^ (r0 & 7)) << 4);
         Ring ring(a.stages);
         if (a.stall == STALL_ROWS && half && warp == 2) uniform_wait(rest, 0, bound, failed);
-        for (int t = cluster; t < tiles && !failed; t += clusters) {
+        // The slots of the next tile are asked for while this one's rows are copied.
+        int slots[PAIR_ROWS / 32];
+        auto ask = [&](int t) {
             const Tile p = place(t);
-            const int own = p.n >> 1, in = p.cnt - (int)half * own;   // rows of this half, of them there
+            const int own = p.n >> 1, in = min(own, p.cnt - (int)half * own);   // rows of this half, of them there
+#pragma unroll
+            for (int i = 0; i < PAIR_ROWS / 32; ++i) slots[i] = 16 * i + r0 < in ? a.l.perm[p.q0 + (int)half * own + 16 * i + r0] : -1;
+        };
+        if (cluster < tiles) ask(cluster);
+        const float per = 1.f / (float)a.l.x_div;   // slots are below 2^17: (slot + 1/2) / x_div is off a whole number by far more than fp32's error
+        for (int t = cluster; t < tiles && !failed; t += clusters) {
             const __nv_bfloat16 *src[PAIR_ROWS / 32];
 #pragma unroll
-            for (int i = 0; i < PAIR_ROWS / 32; ++i) {
-                const int r = 16 * i + r0;
-                src[i] = r < own && r < in ? static_cast<const __nv_bfloat16 *>(a.l.x) +
-                                                 (int64_t)(a.l.perm[p.q0 + (int)half * own + r] / a.l.x_div) * a.l.ld_x + col
-                                           : nullptr;
-            }
+            for (int i = 0; i < PAIR_ROWS / 32; ++i)
+                src[i] = slots[i] < 0 ? nullptr
+                                      : static_cast<const __nv_bfloat16 *>(a.l.x) + (int64_t)(int)(((float)slots[i] + 0.5f) * per) * a.l.ld_x + col;
+            if (t + clusters < tiles) ask(t + clusters);
             for (int k = k_lo; k < k_hi; ++k, ring.next()) {
                 if (ring.reused() && !uniform_wait(empty(ring.slot), ring.parity ^ 1u, bound, failed)) break;
                 const uint32_t to = base + (uint32_t)ring.slot * slot_bytes + w_bytes + at;

@@ -322,3 +322,40 @@ def test_two_streams_share_a_grouping(cuda_lib):
             lora.lora_expert_linear(y, x, w, meta, st, stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(y, want) for y in ys) and int(st.item()) == 0
+
+
+STALLS = [(s, r) for s in [(4, 4, 2048, 264), (300, 5, 512, 520), (5000, 3, 256, 2056)] for r in (1, 2, 3, 4, 5)] + \
+    [((200, 3, 333, 257), r) for r in (1, 2, 4)]
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("shape,role", STALLS)
+def test_stalled_warp_times_out_and_the_context_survives(cuda_lib, monkeypatch, shape, gated, role):
+    """As lora_linear's: the wait runs out, the call returns, the next one is exact."""
+    slots, N, d, n = shape
+    ids = (torch.arange(slots) * 7 % N).int()
+    meta, st = _meta(ids, N), _status()
+    y = torch.full((slots + 1, n + 8), 99.0, dtype=torch.bfloat16, device="cuda")
+    x, w = torch.ones(slots, d, dtype=torch.bfloat16, device="cuda"), torch.ones(N, 2 * n if gated else n, d, dtype=torch.bfloat16, device="cuda")
+    monkeypatch.setenv("LORA_DEBUG_STALL", str(role))
+    lora.lora_expert_linear(y[:slots, :n], x, w, meta, st, gated=gated)
+    monkeypatch.delenv("LORA_DEBUG_STALL")
+    assert int(st.item()) == lora.DEV_TIMEOUT
+    assert (y[slots] == 99).all() and (y[:, n:] == 99).all()
+    _experts_check(slots, slots, N, d, n, torch.bfloat16, gated=gated)
+
+
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 8704), (torch.bfloat16, 8701), (torch.float32, 8704)])
+def test_experts_offsets_past_32_bits(cuda_lib, dtype, d):
+    """Weights of more than 2^31 elements: the last expert's rows lie beyond."""
+    N, n, slots = 9, 28672, 40
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.zeros(N, n, d, dtype=dtype, device="cuda")
+    x, last = whole(g, (slots, d), 1).to(dtype), whole(g, (n, d), 1).to(dtype)
+    w[N - 1] = last
+    ids = torch.where(torch.arange(slots) % 3 == 0, N - 1, 0).int()
+    meta, st = _meta(ids, N), _status()
+    y = torch.full((slots, n), 7.0, dtype=dtype, device="cuda")
+    lora.lora_expert_linear(y, x, w, meta, st)
+    want = torch.where((ids == N - 1)[:, None].cuda(), x.float() @ last.float().T, torch.zeros((), device="cuda")).to(dtype)
+    assert torch.equal(y, want) and int(st.item()) == 0   # whole numbers below 2^24

@@ -259,3 +259,38 @@ def test_delta_ahead_of_the_activation(cuda_lib):
     # norms: each rounding to bf16 (delta, u, y twice, the oracle's u) is off by 2^-9 on average at most of what it rounds
     scale = y64.norm() + res.double().norm()
     assert (y.cpu().double() - y64).norm() <= 6 * 2.0 ** -8 * scale
+
+
+def test_widest(cuda_lib):
+    """LORA_MX_MAX rows of W, both types and the gate's halves of them."""
+    for dtype in DTYPES:
+        for gated in (False, True):
+            n = lora.MX_MAX // (2 if gated else 1)
+            x = torch.tensor([[1.0] * 8, [2.0] * 8], dtype=dtype, device="cuda")
+            w = (torch.arange(lora.MX_MAX, device="cuda") % 7).to(dtype)[:, None].expand(-1, 8).contiguous()
+            y = _run({"x": x, "w": w, "bias": None, "addend": None, "residual": None}, n, gated)
+            z = 8 * (torch.arange(lora.MX_MAX, device="cuda") % 7).double()
+            want = z[:n] * z[n:] if gated else z
+            assert torch.equal(y[0], want.to(dtype)) and torch.equal(y[1], ((4 if gated else 2) * want).to(dtype))
+
+
+# a few rows (k split over pairs), row tiles, many tiles a pair; rows off 16-byte steps have other roles
+STALLS = [(s, r) for s in [(1, 4096, 4096), (40, 4096, 1024), (257, 2048, 520), (3000, 512, 4104)] for r in (1, 3, 4, 5)] + \
+    [(s, r) for s in [(70, 1001, 300), (2000, 333, 3000)] for r in (1, 2, 4)]
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("shape,role", STALLS)
+def test_stalled_warp_times_out_and_the_context_survives(cuda_lib, monkeypatch, shape, gated, role):
+    """LORA_DEBUG_STALL: a warp of one role waits for what never comes.  The bounded wait runs out (a few ms), the other
+    warps stop, LORA_DEV_TIMEOUT is set, nothing beside y is written, and the call returns; the next call is exact."""
+    T, d, n = shape
+    _, o = _operands(T, T, d, n, torch.bfloat16, gated, False, True, False)
+    y = torch.full((T + 1, n + 8), 99.0, dtype=torch.bfloat16, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    monkeypatch.setenv("LORA_DEBUG_STALL", str(role))
+    lora.lora_linear(y[:T, :n], o["x"], o["w"], status, addend=o["addend"], gated=gated)
+    monkeypatch.delenv("LORA_DEBUG_STALL")
+    assert int(status.item()) == lora.DEV_TIMEOUT
+    assert (y[T] == 99).all() and (y[:, n:] == 99).all()
+    _check(T, T, d, n, torch.bfloat16, gated, addend=True)
