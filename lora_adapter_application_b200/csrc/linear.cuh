@@ -59,9 +59,9 @@ __device__ __forceinline__ void activate(int act, float *z) {
 }
 
 // ------------------------------------------------------------------ experts
-// Row tiles (rows positions each) of experts before e, for e in 0..N, to pre[0..N] in shared memory, by a whole block;
-// part: 32 words of shared memory.  Ends with the block's barrier.
-__device__ __forceinline__ void count_tiles(const int32_t *seg_start, int N, int rows, int *pre, int *part) {
+// Row tiles (rows positions each) of experts before e, for e in 0..N, to pre[0..N] in shared memory, by a whole block, and
+// seg_start to start[0..N] (may be NULL); part: 32 words of shared memory.  Ends with the block's barrier.
+__device__ __forceinline__ void count_tiles(const int32_t *seg_start, int N, int rows, int *pre, int *start, int *part) {
     const int per = (N + (int)blockDim.x - 1) / (int)blockDim.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int lo = min(N, (int)threadIdx.x * per), hi = min(N, lo + per);
     int sum = 0;
@@ -76,10 +76,14 @@ __device__ __forceinline__ void count_tiles(const int32_t *seg_start, int N, int
     __syncthreads();
     int at = up - sum;
     for (int w = 0; w < warp; ++w) at += part[w];
-    if (threadIdx.x == 0) pre[0] = 0;
+    if (threadIdx.x == 0) {
+        pre[0] = 0;
+        if (start) start[0] = seg_start[0];
+    }
     for (int e = lo; e < hi; ++e) {
         at += (seg_start[e + 1] - seg_start[e] + rows - 1) / rows;
         pre[e + 1] = at;
+        if (start) start[e + 1] = seg_start[e + 1];
     }
     __syncthreads();
 }
@@ -93,7 +97,6 @@ __device__ __forceinline__ int expert_of(const int *pre, int N, int t) {
     }
     return lo;
 }
-constexpr int MAX_EXPERTS = LORA_MAX_EXPERTS;
 
 // tmaps.cu
 int tensor_map_rows(CUtensorMap *out, const void *base, uint64_t inner, uint64_t rows, uint64_t row_stride,

@@ -41,7 +41,7 @@ __device__ __forceinline__ bool block_rows(const LinArgs &a, int tile, int rows,
         out->e = 0, out->q0 = tile * rows, out->cnt = min(rows, a.T - out->q0);
         return true;
     }
-    count_tiles(a.seg_start, a.N, rows, pre, part);
+    count_tiles(a.seg_start, a.N, rows, pre, nullptr, part);
     if (tile >= pre[a.N]) return false;
     const int e = expert_of(pre, a.N, tile);
     out->e = e;
@@ -66,7 +66,7 @@ constexpr int DOT_ROWS = 8, DOT_FEATURES = 2, DOT_WARPS = 8;
 
 template <bool GATED>
 __global__ void __launch_bounds__(32 * DOT_WARPS) linear_dot_kernel(const LinArgs a, int vec, int row_tiles) {
-    __shared__ int pre[MAX_EXPERTS + 1], part[32];
+    __shared__ int pre[LORA_MAX_EXPERTS + 1], part[32];
     pdl_next();
     pdl_wait();
     Rows r;
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(KG * (BM / TM) * (BN / TN)) linear_tile_kernel
     constexpr int GROUP = (BM / TM) * (BN / TN), THREADS = KG * GROUP, ROWS = BM + BN, TX = BN / TN, H = BN / 2, TILE_LD = TILE_K + 4;
     static_assert(TN % 2 == 0 && TX % 8 == 0 && GROUP % 32 == 0 && BM / TM % 4 == 0, "gate and up in one thread, whole warps");
     extern __shared__ __align__(16) float lin_tiles[];   // [STAGES][ROWS][TILE_LD]
-    __shared__ int pre[MAX_EXPERTS + 1], part[32];
+    __shared__ int pre[LORA_MAX_EXPERTS + 1], part[32];
     __shared__ const float *src[ROWS];   // rows of x, then of W
     pdl_next();
     pdl_wait();

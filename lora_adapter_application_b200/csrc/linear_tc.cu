@@ -37,9 +37,7 @@ template <int MODE>
 constexpr int load_warps() { return MODE == PLAIN ? 0 : MODE == GATHERED ? 4 : 8; }
 template <int MODE>
 constexpr int pair_threads() { return 32 * (2 + EPI_WARPS + load_warps<MODE>()); }
-// dynamic shared memory, all that the experts' table of 4 KB or the barriers leave: one block an SM, as its tensor memory asks for
-template <int MODE>
-constexpr size_t pair_smem() { return (MODE == PLAIN ? 226 : 221) * 1024; }
+constexpr size_t PAIR_SMEM = 226 * 1024;   // all of the shared memory: one block an SM, as its tensor memory asks for
 enum { STALL_MMA = 1, STALL_ROWS = 2, STALL_COPY = 3, STALL_SUMS = 4, STALL_COPY_FIRST = 5 };   // LORA_DEBUG_STALL
 
 struct PairArgs {
@@ -54,6 +52,7 @@ struct PairArgs {
     int S;               // pairs that split k
     int own_red;         // the partial sums' place is behind the ring
     uint32_t epi_at;     // the epilogue's, behind both
+    uint32_t table_at;   // experts: row tiles and slots before each, behind that
     int vec;             // y, addend, residual and bias in 16-byte steps
     unsigned limit;
     int stall;
@@ -146,7 +145,7 @@ __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(co
     __shared__ uint32_t tmem_sm;
     __shared__ __align__(8) uint64_t bars[4 * PAIR_STAGES + 6];
     __shared__ uint32_t stop_sm, used_sm;   // used_sm: ring uses that this block's copies have begun
-    __shared__ int pre[ROWS ? MAX_EXPERTS + 1 : 1], part[ROWS ? 32 : 1];
+    __shared__ int part[32];
     constexpr int FIRST_EPI = 2 + load_warps<MODE>();
     const bool grouped = MODE == GATHERED || (MODE == LOADED && a.l.perm);
     const int warp = __shfl_sync(FULL, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -198,9 +197,10 @@ __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(co
         tmem = __shfl_sync(FULL, tmem_sm, 0);
         if (warp == 1 && half == 1 && elect_one()) mbar_arrive_peer(map_rank(ready, first));
     }
+    int *const pre = reinterpret_cast<int *>(lin_sm + (base - smem_u32(lin_sm)) + a.table_at), *const start = pre + a.l.N + 1;
     int tiles = a.m_tiles * a.n_tiles;
     if (grouped) {
-        count_tiles(a.l.seg_start, a.l.N, a.bn, pre, part);
+        count_tiles(a.l.seg_start, a.l.N, a.bn, pre, start, part);
         tiles = a.m_tiles * pre[a.l.N];
     }
 
@@ -213,8 +213,8 @@ __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(co
             p.e = expert_of(pre, a.l.N, t / a.m_tiles);
             const int n = pre[p.e + 1] - pre[p.e], left = t - pre[p.e] * a.m_tiles;
             mi = left / n;
-            p.q0 = a.l.seg_start[p.e] + (left - mi * n) * a.bn;
-            rows = a.l.seg_start[p.e + 1];
+            p.q0 = start[p.e] + (left - mi * n) * a.bn;
+            rows = start[p.e + 1];
         } else {
             constexpr int BAND = 16;
             const int per = BAND * a.m_tiles, band = t / per, left = t - band * per, high = min(BAND, a.n_tiles - band * BAND);
@@ -623,12 +623,12 @@ int pair_fit(int dev, const int **fit) {
     int *f = table[dev & 63];
     auto kernel = linear_pair_kernel<MODE, MT, KT>;
     if (!f[0]) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pair_smem<MODE>());
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)PAIR_SMEM);
         for (int i = MAX_S - 1; i >= 0 && e == cudaSuccess; --i) {   // f[0] last: it marks the table as filled
             cudaLaunchConfig_t cfg{};
             cfg.gridDim = dim3(2u * (i + 1));
             cfg.blockDim = dim3(pair_threads<MODE>());
-            cfg.dynamicSmemBytes = pair_smem<MODE>();
+            cfg.dynamicSmemBytes = PAIR_SMEM;
             cudaLaunchAttribute attr{};
             attr.id = cudaLaunchAttributeClusterDimension;
             attr.val.clusterDim.x = 2u * (i + 1);
@@ -665,7 +665,7 @@ int consider(const LinArgs &l, bool gated, int bn, int64_t row_tiles, int64_t li
     for (int s = 1; s <= MAX_S && s <= n_k; ++s) {
         const int64_t tiles = m * row_tiles, expect = m * likely;
         if (s > 1 && tiles > fit[s - 1]) break;   // a cluster that splits k has one tile
-        if (s > 1 && bn > 32 && (size_t)own_rows(rows, s) * s * 512 * MT > pair_smem<MODE>() - 1024) continue;
+        if (s > 1 && bn > 32 && (size_t)own_rows(rows, s) * s * 512 * MT > PAIR_SMEM - 1024) continue;
         const int64_t clusters = std::min<int64_t>(tiles, fit[s - 1]);
         const int64_t rounds = (expect + clusters - 1) / clusters;
         const int64_t k_ns = (n_k + s - 1) / s * KT * step;
@@ -680,15 +680,17 @@ int launch_pair(PairArgs &a, const PairPlan &plan, cudaStream_t st) {
     a.bn = plan.bn, a.S = plan.S;
     a.up = a.gated ? a.l.d_out : 256;
     a.m_tiles = m_tiles_of(a.l, a.gated, MT);
-        a.own_red = plan.S > 1 && plan.bn <= 32;
+    a.own_red = plan.S > 1 && plan.bn <= 32;
     a.n_k = (a.l.d_in + 64 * KT - 1) / (64 * KT);
     a.vec = mx_vec(a.l.y, a.l.ld_y, a.l.d_out, 2) && (!a.l.addend || mx_vec(a.l.addend, a.l.ld_a, a.l.d_out, 2)) &&
             (!a.l.residual || mx_vec(a.l.residual, a.l.ld_r, a.l.d_out, 2)) && (!a.l.bias || mx_aligned(a.l.bias, 16));
     const size_t slot = (16384u * MT + 64u * (size_t)plan.bn) * KT, red = a.own_red ? (size_t)own_rows(plan.bn, plan.S) * 512 * MT * plan.S : 0;
-    a.stages = (int)std::min<size_t>(PAIR_STAGES, (pair_smem<MODE>() - 1024 - EPI_WARPS * 1024 * MT - red) / slot);
+    const size_t table = a.l.perm ? 8 * (size_t)(a.l.N + 1) : 0;
+    a.stages = (int)std::min<size_t>(PAIR_STAGES, (PAIR_SMEM - 1024 - EPI_WARPS * 1024 * MT - table - red) / slot);
     a.epi_at = (uint32_t)(a.stages * slot + red);
+    a.table_at = a.epi_at + EPI_WARPS * 1024 * MT;
     return launch_after(linear_pair_kernel<MODE, MT, KT>, dim3((unsigned)(plan.clusters * 2 * plan.S)), pair_threads<MODE>(),
-                        pair_smem<MODE>(), 2u * plan.S, st, a);
+                        PAIR_SMEM, 2u * plan.S, st, a);
 }
 
 template <int MODE>
@@ -715,10 +717,6 @@ int launch_plan(PairArgs &a, const PairPlan &p, cudaStream_t st) {
 }
 
 int round32(int64_t n) { return (int)((n + 31) / 32 * 32); }
-
-}  // namespace
-
-namespace {
 
 // Rows of x and W in the 16-byte steps that TMA and 16-byte copies take.
 bool whole_steps(const LinArgs &a, int64_t x_rows) {
