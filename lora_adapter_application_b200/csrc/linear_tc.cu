@@ -14,7 +14,7 @@
 // read the accumulators (lane = feature, column = row of x), apply the epilogue and store.  Experts (GATHERED): four more
 // warps copy the group's rows of x, wherever they lie, with cp.async into the same swizzle, 16 bytes a lane (gather4
 // copies of four rows x 128 bytes would be 32 a stage; a TMA copy costs its warp 40-60 ns); they count on the block's own
-// barrier, and warp 1 of the second block passes the word on to the first.
+// barrier, from which one more warp of each block passes the word on to the first one's warp 1.
 #include "linear.cuh"
 #include "pipe.cuh"
 
@@ -36,7 +36,7 @@ constexpr int EPI_WARPS = 8;
 template <int MODE>
 constexpr int load_warps() { return MODE == PLAIN ? 0 : MODE == GATHERED ? 4 : 8; }
 template <int MODE>
-constexpr int pair_threads() { return 32 * (2 + EPI_WARPS + load_warps<MODE>()); }
+constexpr int pair_threads() { return 32 * (2 + EPI_WARPS + load_warps<MODE>() + (MODE == GATHERED)); }
 constexpr size_t PAIR_SMEM = 226 * 1024;   // all of the shared memory: one block an SM, as its tensor memory asks for
 enum { STALL_MMA = 1, STALL_ROWS = 2, STALL_COPY = 3, STALL_SUMS = 4, STALL_COPY_FIRST = 5 };   // LORA_DEBUG_STALL
 
@@ -138,9 +138,19 @@ __device__ __forceinline__ uint4 shfl4(const uint4 &v, int from) {
                       __shfl_sync(FULL, v.w, from));
 }
 
+// uniform_wait for two barriers at once: each costs 100 clocks where it is complete already
+__device__ __forceinline__ bool uniform_wait2(uint32_t a, uint32_t b, unsigned parity, const Bound &w, bool &failed) {
+    for (unsigned it = 0; it < w.limit; ++it) {
+        const bool x = mbar_try<false>(a, parity), y = mbar_try<false>(b, parity);
+        if (__all_sync(FULL, x && y)) return true;
+        if (__any_sync(FULL, stopped(w.stop))) break;
+    }
+    failed = true;
+    return false;
+}
+
 template <int MODE, int MT, int KT>
 __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(const __grid_constant__ PairArgs a) {
-    constexpr bool ROWS = MODE != PLAIN;   // x comes by warps
     extern __shared__ __align__(1024) unsigned char lin_sm[];
     __shared__ uint32_t tmem_sm;
     __shared__ __align__(8) uint64_t bars[4 * PAIR_STAGES + 6];
@@ -158,8 +168,8 @@ __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(co
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     auto full = [&](int s) { return bar(s); };                       // the first block's counts both blocks' TMA bytes
     auto empty = [&](int s) { return bar(PAIR_STAGES + s); };
-    auto rows_in = [&](int s) { return bar(2 * PAIR_STAGES + s); };      // this block's gathered rows
-    auto peer_rows = [&](int s) { return bar(3 * PAIR_STAGES + s); };    // the first block's: the second's have landed too
+    auto rows_in = [&](int s) { return bar(2 * PAIR_STAGES + s); };       // this block's gathered rows
+    auto rows_ready = [&](int s) { return bar(3 * PAIR_STAGES + s); };    // the first block's: both blocks' rows (W's too, LOADED)
     auto acc_full = [&](int b) { return bar(4 * PAIR_STAGES + b); };
     auto acc_empty = [&](int b) { return bar(4 * PAIR_STAGES + 2 + b); };   // the first block's: eight warps of each block
     const uint32_t ready = bar(4 * PAIR_STAGES + 5);   // the first block's: the second has its tensor memory
@@ -169,8 +179,10 @@ __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(co
 
     if (warp == 0) {
         for (int i = lane; i < 4 * PAIR_STAGES + 6; i += 32) {
-            const bool rows = i >= 2 * PAIR_STAGES && i < 3 * PAIR_STAGES, drained = i >= 4 * PAIR_STAGES + 2 && i < 4 * PAIR_STAGES + 4;
-            mbar_init(bar(i), rows ? (MODE == GATHERED ? 32 : 1) * max(1, load_warps<MODE>()) : drained ? 2 * EPI_WARPS : 1);
+            const int kind = i / PAIR_STAGES;   // 2: rows_in, 3: rows_ready
+            const bool drained = i >= 4 * PAIR_STAGES + 2 && i < 4 * PAIR_STAGES + 4;
+            mbar_init(bar(i), kind == 2 ? 32 * max(1, load_warps<MODE>()) : kind == 3 ? (MODE == LOADED ? 2 * load_warps<MODE>() : 2)
+                                                                          : drained ? 2 * EPI_WARPS : 1);
         }
         if (lane == 0) {
             stop_sm = 0, used_sm = 0;
@@ -190,7 +202,8 @@ __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(co
     pdl_wait();   // all warps: none of the bounded waits below runs while the kernel before this one does
     asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
     uint32_t tmem = 0;
-    if (warp == 1 || warp >= FIRST_EPI) {
+    const bool sums = warp >= FIRST_EPI && warp < FIRST_EPI + EPI_WARPS;   // the warps of the epilogue
+    if (warp == 1 || sums) {
         tc_fence_before();
         asm volatile("bar.sync 1, %0;\n" ::"n"(32 * (1 + EPI_WARPS)) : "memory");
         tc_fence_after();
@@ -265,15 +278,12 @@ __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(co
                 const uint32_t d = tmem + (uint32_t)(b * MT * a.bn), idesc = pair_idesc(p.n);
                 for (int k = k_lo; k < k_hi; ++k, ring.next()) {
                     const int s = ring.slot;
-                    if (MODE != LOADED && !uniform_wait(full(s), ring.parity, bound, failed)) break;
-                    if (ROWS) {
-                        if (!uniform_wait(rows_in(s), ring.parity, bound, failed) || !uniform_wait(peer_rows(s), ring.parity, bound, failed))
-                            break;
-                    }
+                    if (!(MODE == GATHERED ? uniform_wait2(full(s), rows_ready(s), ring.parity, bound, failed)
+                                           : uniform_wait(MODE == PLAIN ? full(s) : rows_ready(s), ring.parity, bound, failed)))
+                        break;
                     tc_fence_after();
                     const uint32_t slot = base + (uint32_t)s * slot_bytes;
                     if (elect_one()) {
-                        if (MODE == GATHERED) fence_proxy_async();   // rows came by cp.async (generic proxy), the MMA reads them as operands
 #pragma unroll
                         for (int x = 0; x < KT; ++x) {
                             const uint64_t dx = desc_sw128(slot + w_bytes + x_bytes * x);
@@ -290,17 +300,19 @@ __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(co
                 }
                 if (elect_one()) tc_commit_pair(acc_full(b), first);
             }
-        } else if (ROWS) {
-            Ring ring(a.stages);
-            for (int t = cluster; t < tiles && !failed; t += clusters)
-                for (int k = k_lo; k < k_hi; ++k, ring.next()) {
-                    if (!uniform_wait(rows_in(ring.slot), ring.parity, bound, failed)) break;
-                    if (elect_one()) {
-                        if (MODE == GATHERED) fence_proxy_async();
-                        mbar_arrive_peer(map_rank(peer_rows(ring.slot), first));
-                    }
-                }
         }
+    } else if (MODE == GATHERED && warp == FIRST_EPI + EPI_WARPS) {
+        // Rows that came by cp.async (generic proxy) are made visible to the MMA, which reads them as operands; the word goes to the
+        // first block's warp 1 from here, for which a fence of its own each step was too much.
+        Ring ring(a.stages);
+        for (int t = cluster; t < tiles && !failed; t += clusters)
+            for (int k = k_lo; k < k_hi; ++k, ring.next()) {
+                if (!uniform_wait(rows_in(ring.slot), ring.parity, bound, failed)) break;
+                if (elect_one()) {
+                    fence_proxy_async();
+                    mbar_arrive_peer(map_rank(rows_ready(ring.slot), first));
+                }
+            }
     } else if (MODE == GATHERED && warp >= 2 && warp < FIRST_EPI) {
         // Lane l of warp w copies columns 8 (l % 8) .. of rows 16 i + 4 (w - 2) + l / 8 of this block's half.  Rows past the
         // group's last are not read: what the slot holds there only enters columns of the accumulator that no one stores.
@@ -402,10 +414,10 @@ __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(co
                     }
                 fence_proxy_async();   // the MMA reads what these stores wrote
                 __syncwarp();
-                if (elect_one()) mbar_arrive(rows_in(ring.slot));
+                if (elect_one()) mbar_arrive_peer(map_rank(rows_ready(ring.slot), first));
             }
         }
-    } else if (warp >= FIRST_EPI) {
+    } else if (sums) {
         // A warp reads 32 lanes of tensor memory: features f, a row of x in each column.  Through shared memory of its own, eight
         // rows at a time, a thread gets eight columns of one row, four neighbours the warp's 32: one 16-byte access of each
         // operand and of y where there were eight of two bytes, each with its address.  (As they lie in tensor memory: 256 rows
@@ -578,7 +590,7 @@ __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(co
     // ---------------------------------------------------------------- teardown
     __syncwarp();
     leave<true>(bound, failed, first);
-    if (S > 1 && warp < FIRST_EPI && cluster < tiles) {   // the barriers of the exchange, for the warps that take no part in it
+    if (S > 1 && !sums && cluster < tiles) {   // the barriers of the exchange, for the warps that take no part in it
         if (!a.own_red) cluster_sync_all();
         cluster_sync_all();
     }
