@@ -87,15 +87,14 @@ __device__ __forceinline__ void count_tiles(const int32_t *seg_start, int N, int
     }
     __syncthreads();
 }
-// The expert of row tile t: the last e with pre[e] <= t (t < pre[N]).
-__device__ __forceinline__ int expert_of(const int *pre, int N, int t) {
-    int lo = 0, hi = N;   // pre[lo] <= t < pre[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (pre[mid] <= t) lo = mid;
-        else hi = mid;
+// The expert of row tile t: the last e with pre[e] <= t (t < pre[N]), from e on (pre[e] <= t), by a whole warp: 32 to a look.
+__device__ __forceinline__ int expert_of(const int *pre, int N, int t, int e = 0) {
+    const int lane = threadIdx.x & 31;
+    for (;;) {
+        const unsigned before = __ballot_sync(FULL, e + 1 + lane <= N && pre[e + 1 + lane] <= t);
+        e += __popc(before);
+        if (before != FULL) return e;
     }
-    return lo;
 }
 
 // tmaps.cu

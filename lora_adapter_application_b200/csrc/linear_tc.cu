@@ -219,13 +219,14 @@ __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(co
 
     // Tiles run along x first: pairs at work at the same time share W's rows (and, in bands of 16 tiles of x, few enough
     // rows of x to find both in L2).
+    int e_from = 0;   // a warp's tiles go up, and their experts
     auto place = [&](int t) {
         Tile p;
         int mi, rows;
         if (grouped) {
-            p.e = expert_of(pre, a.l.N, t / a.m_tiles);
+            p.e = e_from = expert_of(pre, a.l.N, (int)((unsigned)t / (unsigned)a.m_tiles), e_from);
             const int n = pre[p.e + 1] - pre[p.e], left = t - pre[p.e] * a.m_tiles;
-            mi = left / n;
+            mi = (int)((unsigned)left / (unsigned)n);
             p.q0 = start[p.e] + (left - mi * n) * a.bn;
             rows = start[p.e + 1];
         } else {
