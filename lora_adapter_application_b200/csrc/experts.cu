@@ -13,7 +13,8 @@ namespace {
 // do, 0 for those that cannot be chosen.  A pick is one warp reduction in hardware for bf16 logits, whose 16 bits share a
 // key with the expert's complement (the largest key is the first expert's of the largest logit), two for fp32: the largest
 // key, and the first expert that holds it.  The weights come from the picks' logits, so that ids depend on comparisons
-// alone.  Bound: latency (1 token), then the picks' instructions (8192 x 256 bf16, 8 of them: KERNEL_US).
+// alone.  Bound: latency (1 token: 2.2 us), then instructions, of which a pick costs about 35 (8192 x 256 bf16, 8 picks: 9.2 us,
+// issue slots 60 % busy; fp32 11.3).
 constexpr int ROUTE_WARPS = 4;
 
 __device__ __forceinline__ uint32_t order_key(float l) {
@@ -117,7 +118,8 @@ int launch_route(int32_t *ids, float *weights, const void *logits, int64_t ld, i
 // -------------------------------------------------------------------- sum
 // A warp takes 256 columns of a few tokens, eight a lane (VEC: 16-byte accesses; else 32 columns apart), and adds the slots'
 // rows in slot order, fp32, one rounding.  The tokens' ids and weights come in one load of the warp, ahead of all; four
-// rows' loads are in flight at a time.  Bound: HBM.
+// rows' loads are in flight at a time.  Bound: HBM (8192 x 4 x 4096 with a residual 64.9 us, 95 % of the measured copy rate;
+// with a block for each token 79.5).
 constexpr int SUM_WARPS = 4, SUM_TOKENS = 4;
 
 template <typename E, bool VEC>

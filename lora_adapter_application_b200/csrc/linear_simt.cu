@@ -2,9 +2,11 @@
 // arithmetic units: fp32 products, no tf32; any stride and alignment.
 //
 //   few rows    a warp takes two features (gated: one of each half) x eight rows, its lanes split k: W is read once for
-//               eight rows, bound by HBM
-//   many rows   a block takes a tile of rows x features, 8 x 8 or 4 x 4 sums a thread, both operands through shared memory;
-//               bound by the arithmetic units (128 fused multiply-adds a clock and SM)
+//               eight rows, bound by HBM (1 x 14336 x 4096 38.3 us = 6.1 TB/s; 1 x 4096 x 4096 14.2)
+//   many rows   a block takes a tile of rows x features, 8 x 4 or 4 x 4 sums a thread, both operands through shared memory;
+//               bound by the arithmetic units, at 60 % of their 128 multiply-adds a clock and SM (4096^3 3.2 ms = 43 TFLOP/s,
+//               where torch's matrix product takes 2.4), few tiles by latency (333 x 1003 x 777 35 us, with rows in
+//               16-byte steps 29)
 #include "linear.cuh"
 #include "ptx.cuh"
 
@@ -271,7 +273,7 @@ int launch_as(const LinArgs &a, int sms, cudaStream_t st) {
         const int tiles = row_tiles(DOT_ROWS);   // at most 3072 of them, and 65536 blocks of features
         return launch_after(linear_dot_kernel<GATED>, dim3(tiles * ((a.d_out + cols - 1) / cols)), 32 * DOT_WARPS, 0, 0, st, a, vec, tiles);
     }
-    // the largest tile that gives every SM one
+    // the largest tile that gives every SM one (64 x 4096 x 14336: 296 us on 64 x 64, 384 on 32 x 64)
     auto tiles = [&](int bm, int bn) { return (int64_t)row_tiles(bm) * ((a.n_w + bn - 1) / bn); };
     if (per_group > 64 && tiles(128, 64) >= sms) return launch_tile<GATED, 128, 64, 8, 4, 1, 32, 3>(a, vec, row_tiles(128), st);
     if (per_group > 32 && tiles(64, 64) >= sms) return launch_tile<GATED, 64, 64, 8, 4, 2, 32, 3>(a, vec, row_tiles(64), st);

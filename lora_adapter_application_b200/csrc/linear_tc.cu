@@ -4,17 +4,29 @@
 // W's rows are the MMA's M side: a pair of blocks (cta_group::2) takes 256 features, each block loading its own 128; the
 // rows of x are the N side, any multiple of 32 up to 256, each block loading half.  So a decode batch reads W once and
 // computes no more than it must, a group of an expert's rows wastes at most 31 of a tile, and many rows get 256 x 256
-// tiles, 64 bytes a clock and SM of operands at full rate.  MT = 2: two such feature blocks on one x tile: the gate's and
-// the up projection's columns of a gated product, which then meet in one thread, or twice the features.
+// or 512 x 128 tiles (MT = 2: two feature blocks on one x tile: the gate's and the up projection's columns of a gated product,
+// which then meet in one thread, or twice the features), 64 to 80 bytes of operands a clock and SM at the tensor cores' full rate.
 //
 // One persistent kernel for all sizes.  Tile t of cluster c: t = c, c + clusters, ....  Few tiles: a cluster is S pairs that
 // split k, each cluster has one tile, and its blocks add their sums, in rank order, through distributed shared memory.
 //
 // Warp 0 copies W's boxes (and x's, plain product) by TMA; warp 1 of the first block of a pair issues the MMAs; eight warps
-// read the accumulators (lane = feature, column = row of x), apply the epilogue and store.  Experts (GATHERED): four more
-// warps copy the group's rows of x, wherever they lie, with cp.async into the same swizzle, 16 bytes a lane (gather4
-// copies of four rows x 128 bytes would be 32 a stage; a TMA copy costs its warp 40-60 ns); they count on the block's own
-// barrier, from which one more warp of each block passes the word on to the first one's warp 1.
+// read the accumulators (lane = feature, column = row of x), apply the epilogue and store, while the next tile's products go
+// into the other accumulator.  Experts (GATHERED): four more warps copy the group's rows of x, wherever they lie, with
+// cp.async into the same swizzle, 16 bytes a lane (gather4 copies of four rows x 128 bytes would be 32 a stage; a TMA copy
+// costs its warp 40-60 ns); they count on the block's own barrier, from which one more warp of each block passes the word
+// on to the first one's warp 1.
+//
+// Bound.  Few rows: HBM behind about 4 us that any call takes (1 x 4096 x 4096 9.4 us; 16 x 8192 x 28672 73.6 us = 6.4 TB/s;
+// 8 experts of 4096 x 2 x 14336, 64 tokens, 290 us = 6.5 TB/s, 99 % of the measured copy rate).  Many rows: the tensor cores
+// (8192 x 4096 x 2 x 14336 1200 us = 1600 TFLOP/s in a short burst, 1420 at the power cap; the issuing warp waits for no
+// operands: 513 clocks a step of 512).  Between, 100 to 1000 rows: the operands' way into shared memory, about 64 bytes a
+// clock and SM, and the exchange (257 x 14336 x 4096 34.7 us, its floor 19.7).  Many small experts (8192 tokens, 4 of 64, 2048 x
+// 2 x 1024: 240 us): 630 clocks a step where dense rows take 513, at 1.35 GHz under the power cap.
+//
+// Measured and dropped: 16-bit accesses of y and the operands straight from tensor memory's layout (see the epilogue); one accumulator
+// of 512 x 256 (8192 x 4096 x 2 x 14336 1380 us); W prefetched to L2 eight steps ahead (experts 262 -> 268, decode 291 -> 430);
+// x in a deeper ring of its own (experts: no gain).
 #include "linear.cuh"
 #include "pipe.cuh"
 
@@ -357,7 +369,8 @@ __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(co
         // Rows at any (even) address: eight lanes read the aligned 16-byte pieces around 64 columns of a row, a ninth piece comes
         // from a load that a warp makes once for all its rows, and each lane shifts two neighbouring pieces into the 16 bytes
         // that the operand's swizzle wants.  Pieces that hold no column of the row are not read.  Loads go out ahead of the
-        // wait for the slot; a slot's 32 KB in flight bound it.
+        // wait for the slot; a slot's 32 KB in flight bound it, about 1 us a step (8192 x 4095 x 4096 717 us = 383 TFLOP/s, where 4096
+        // columns take 196).
         constexpr int W_IT = 4 * MT, X_IT = PAIR_ROWS / MT / 2 / 32, ITS = W_IT + X_IT, EXTRA = (ITS + 7) / 8;
         const int lw = warp - 2, lr = lane >> 3, c = lane & 7;   // rows 4 (lw + 8 i) + lr of W's, then of x's
         Ring ring(a.stages);
@@ -660,10 +673,14 @@ int pair_fit(int dev, const int **fit) {
 
 int m_tiles_of(const LinArgs &l, bool gated, int mt) { return (l.d_out + (gated ? 256 : 256 * mt) - 1) / (gated ? 256 : 256 * mt); }
 
-// Two 64-column steps to a ring slot while three slots fit.
+// Two 64-column steps to a ring slot while three slots fit: half the waits (257 x 14336 x 4096, 96-row tiles: 55.3 -> 50.1 us).
 bool two_steps(int mt, int bn) { return mt == 1 ? bn <= 160 : bn <= 32; }
 
-// The best split of k for tiles of bn rows; row_tiles: as many as there may be, likely: as many as are expected.
+// The best split of k for tiles of bn rows; row_tiles: as many as there may be, likely: as many as are expected.  The times
+// are those of the cases below, whose plan was the best of all within 7 % (us; MT, rows of a tile, S): 1 x 4096 x 4096 9.3 (1, 32, 3), S = 2
+// 10.0; 64 x 4096 x 4096 10.8 (1, 32, 2); 128 x 14336 x 4096 26.9 (1, 128, 3), S = 1 50; 257 x 14336 x 4096 34.7 (1, 160, 2), S = 1 58,
+// (1, 96, 1) 42.6; 512 x 14336 x 4096 49.4 (1, 256, 2); 1024 x 4096 x 4096 29.3 (1, 256, 1); 4096 x 4096 x 4096 97 (2, 128, 1),
+// (1, 256, 1) 100.  8 % off: 512 x 4096 x 4096 21.0 for 18.9 (1, 128, 1), 1024 x 14336 x 4096 93 for 85 (1, 256, 1).
 template <int MODE, int MT, int KT>
 int consider(const LinArgs &l, bool gated, int bn, int64_t row_tiles, int64_t likely, int dev, PairPlan *best) {
     const int *fit = nullptr;

@@ -5,9 +5,10 @@ Whole inputs: x and W hold whole numbers (bias and addend halves), so that every
 in any order: z is exact, whatever the kernel's order.  Then y is off by its activation's arithmetic and the one rounding
 (finfo(dtype).eps / 2 of y):
     none, relu        nothing more
-    silu, gelu_tanh   z / (1 + e^-u).  e^-u: bf16 results use __expf, 2 + 1.16 |u| units of 2^-23 (CUDA's bound),
-                      fp32 ones expf, 2; u itself 4 roundings, which e^-u multiplies by |u|: 4 |u| units of 2^-24;
-                      sum, quotient (__fdividef 2 units) and the rest 5 units: (9 + 3.2 |u|) 2^-23
+    silu, gelu_tanh   z / (1 + e^-u).  e^-u: bf16 results use ex2.approx of -u log2 e (2 units of 2^-23, and two roundings of
+                      the argument, |u| 2^-23 together: less than 2 + 1.16 |u| units), fp32 ones expf, 2; u itself 4
+                      roundings, which e^-u multiplies by |u|: 4 |u| units of 2^-24; sum, reciprocal or quotient (1 to 2
+                      units) and the rest 5 units: (9 + 3.2 |u|) 2^-23
     gelu              z erfc(v) / 2, v = -z / sqrt 2 rounded twice; erfc changes by at most (2 v^2 + 2) of a relative change
                       of v: (2 v^2 + 2) units; erfcf 4 units (CUDA's bound), two products: (8 + 2 v^2) 2^-23 = (8 + z^2) 2^-23
     gated             one product more, residual one sum more: 2^-24 each of their results

@@ -359,3 +359,14 @@ def test_experts_offsets_past_32_bits(cuda_lib, dtype, d):
     lora.lora_expert_linear(y, x, w, meta, st)
     want = torch.where((ids == N - 1)[:, None].cuda(), x.float() @ last.float().T, torch.zeros((), device="cuda")).to(dtype)
     assert torch.equal(y, want) and int(st.item()) == 0   # whole numbers below 2^24
+
+
+@pytest.mark.parametrize("dtype,d", [(torch.bfloat16, 64), (torch.bfloat16, 33), (torch.float32, 64)])
+def test_experts_most_slots_and_experts(cuda_lib, dtype, d):
+    _experts_check(3, lora.MAX_ROWS, lora.MAX_EXPERTS, d, 72, dtype, "skewed", x_div=8)
+
+
+def test_run_case(cuda_lib):
+    from lora_adapter_application_b200 import run_case
+    assert run_case.main(["decode_qproj", "--base", "bf16", "--experts", "8", "--reps", "2"]) == 0
+    assert run_case.main(["tiny", "--base", "bf16", "--experts", "3", "--reps", "1"]) == 0

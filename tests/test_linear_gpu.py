@@ -92,14 +92,18 @@ def test_random_values(cuda_lib, T, d, n, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("T", [1, 40, 300])
-def test_in_place(cuda_lib, T, dtype):
-    """y over the residual, over the addend."""
-    o64, o = _operands(5, T, 512, 264, dtype, False, True, True, True)
+@pytest.mark.parametrize("T,d,n", [(1, 512, 264), (40, 512, 264), (300, 512, 264), (2500, 512, 2056), (40, 333, 257), (700, 333, 600)])
+def test_in_place(cuda_lib, T, d, n, dtype):
+    """y over the residual, over the addend; a gated y over the residual."""
+    o64, o = _operands(5, T, d, n, dtype, False, True, True, True)
     want, tol = dense64(**o64, act=lora.ACT_GELU, dtype=dtype)
     for name in ("residual", "addend"):
         y = o[name].clone()
-        assert_close(_run({**o, name: y}, 264, False, lora.ACT_GELU, y=y), want, tol, name)
+        assert_close(_run({**o, name: y}, n, False, lora.ACT_GELU, y=y), want, tol, name)
+    o64, o = _operands(6, T, d, n, dtype, True, False, True, True)
+    want, tol = dense64(**o64, act=lora.ACT_SILU, gated=True, dtype=dtype)
+    y = o["residual"].clone()
+    assert_close(_run({**o, "residual": y}, n, True, lora.ACT_SILU, y=y), want, tol, "gated")
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
