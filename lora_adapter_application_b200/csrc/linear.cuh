@@ -34,6 +34,26 @@ __device__ __forceinline__ float over_one_plus_exp(float z, float u) {   // z / 
     asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(1.f + e));
     return z * r;
 }
+// z Phi(z) = z erfc(-z / sqrt 2) / 2.  For a = |z| / sqrt 2: erfc(a) = t e^(-a^2 + g(t)), t = 1 / (1 + a / 2), with g a polynomial of degree 9
+// fitted to ln(erfc(a) e^(a^2) / t) over a in [0, 15] (minimax, in 64 bits: off by 6.3e-8), times log2 e here; in all within
+// (8 + z^2) 2^-23 of the value, z^2 from the rounding of the exponent.  A third of the instructions of erfcf: 4126 x 1024 x 13536 with this activation 201 -> 139 us.
+__device__ __forceinline__ float gelu_fast(float z) {
+    float t, e;
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(t) : "f"(fmaf(fabsf(z), 0.35355339059327376f, 1.f)));
+    float g = 0.23579010367393494f;
+    g = fmaf(g, t, -1.1268246173858643f);
+    g = fmaf(g, t, 2.006770372390747f);
+    g = fmaf(g, t, -1.4504882097244263f);
+    g = fmaf(g, t, 0.24917496740818024f);
+    g = fmaf(g, t, -0.189505934715271f);
+    g = fmaf(g, t, 0.11389805376529694f);
+    g = fmaf(g, t, 0.5447050333023071f);
+    g = fmaf(g, t, 1.4422062635421753f);
+    g = fmaf(g, t, -1.8257261514663696f);
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(e) : "f"(fmaf(-0.72134752044448170f * z, z, g)));
+    const float h = 0.5f * fminf(z, 1e30f) * (t * e);   // the smaller of the two parts (0 where z is infinite)
+    return z < 0.f ? h : z - h;
+}
 template <bool FAST, int N>
 __device__ __forceinline__ void activate(int act, float *z) {
     switch (act) {
@@ -43,7 +63,7 @@ __device__ __forceinline__ void activate(int act, float *z) {
             break;
         case LORA_ACT_GELU:
 #pragma unroll
-            for (int i = 0; i < N; ++i) z[i] = 0.5f * z[i] * erfcf(-0.70710678118654752f * z[i]);
+            for (int i = 0; i < N; ++i) z[i] = FAST ? gelu_fast(z[i]) : 0.5f * z[i] * erfcf(-0.70710678118654752f * z[i]);
             break;
         case LORA_ACT_GELU_TANH:   // (1 + tanh u) / 2 = 1 / (1 + e^-2u), u = sqrt(2 / pi) (z + 0.044715 z^3)
 #pragma unroll

@@ -45,6 +45,7 @@ constexpr int MAX_S = 4;          // most pairs that split k: clusters of eight 
 // (rows off 16-byte steps, with or without experts).
 enum { PLAIN = 0, GATHERED = 1, LOADED = 2 };
 constexpr int EPI_WARPS = 8;
+constexpr uint32_t EPI_BYTES = 2048;   // of shared memory a warp of the epilogue
 template <int MODE>
 constexpr int load_warps() { return MODE == PLAIN ? 0 : MODE == GATHERED ? 4 : 8; }
 template <int MODE>
@@ -433,13 +434,13 @@ __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(co
         }
     } else if (sums) {
         // A warp reads 32 lanes of tensor memory: features f, a row of x in each column.  Through shared memory of its own, eight
-        // rows at a time, a thread gets eight columns of one row, four neighbours the warp's 32: one 16-byte access of each
+        // or 16 rows at a time, a thread gets eight columns of one row, four neighbours the warp's 32: one 16-byte access of each
         // operand and of y where there were eight of two bytes, each with its address.  (As they lie in tensor memory: 256 rows
         // 5.5 us for 256 features, and a chunk's operands, loaded one after the other, up to 0.5 us a row.)
         const int q = warp & 3, f = 32 * q + lane;
         const int side = warp >= FIRST_EPI + 4;             // which of the two warps of these lanes
         const int l_row = lane >> 2, l_col = 32 * q + 8 * (lane & 3);   // this thread's row of eight and columns
-        const uint32_t buf = base + a.epi_at + (uint32_t)(warp - FIRST_EPI) * (1024u * MT);
+        const uint32_t buf = base + a.epi_at + (uint32_t)(warp - FIRST_EPI) * EPI_BYTES;
         const LinArgs &l = a.l;
         __nv_bfloat16 *const y = static_cast<__nv_bfloat16 *>(l.y);
         const __nv_bfloat16 *const add = static_cast<const __nv_bfloat16 *>(l.addend);
@@ -531,21 +532,28 @@ __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(co
                     for (int u = 0; u < MT; ++u) tc_ld16(acc + (uint32_t)(u * a.bn + c), v[u]);
                     tc_wait_ld();
                     if (c + 16 >= c_hi) drained();
+                    // 16 rows of one feature block at a time, or eight of two
 #pragma unroll
-                    for (int h = 0; h < 16; h += 8)
+                    for (int h = 0; h < 16; h += 16 / MT)
                         if (c + h < c_hi) {
                             __syncwarp();
 #pragma unroll
                             for (int u = 0; u < MT; ++u)
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) sts32(buf + 1024u * u + 128u * j + 4u * lane, __float_as_uint(v[u][h + j]));
+                                for (int j = 0; j < 16 / MT; ++j) sts32(buf + 1024u * u + 128u * j + 4u * lane, __float_as_uint(v[u][h + j]));
                             __syncwarp();
-                            float z[MT][8];
+                            float z[2 / MT][MT][8];
 #pragma unroll
-                            for (int u = 0; u < MT; ++u) load_row(z[u], buf + 1024u * u + 128u * (uint32_t)l_row + 32u * (lane & 3));
-                            const Operands<MT> now = o[h / 8];
-                            if (c + h + 16 < c_hi) fetch(o[h / 8], c + h + 16 + l_row);
-                            finish(z, now, c + h + l_row < c_hi);
+                            for (int g = 0; g < 2 / MT; ++g)
+#pragma unroll
+                                for (int u = 0; u < MT; ++u) load_row(z[g][u], buf + 1024u * (g + u) + 128u * (uint32_t)l_row + 32u * (lane & 3));
+#pragma unroll
+                            for (int g = 0; g < 2 / MT; ++g) {
+                                const int at = h / 8 + g;   // eight rows from c + 8 at
+                                const Operands<MT> now = o[at];
+                                if (c + 8 * at + 16 < c_hi) fetch(o[at], c + 8 * at + 16 + l_row);
+                                finish(z[g], now, c + 8 * at + l_row < c_hi);
+                            }
                         }
                 }
                 if (c_lo >= c_hi) drained();
@@ -716,9 +724,10 @@ int launch_pair(PairArgs &a, const PairPlan &plan, cudaStream_t st) {
             (!a.l.residual || mx_vec(a.l.residual, a.l.ld_r, a.l.d_out, 2)) && (!a.l.bias || mx_aligned(a.l.bias, 16));
     const size_t slot = (16384u * MT + 64u * (size_t)plan.bn) * KT, red = a.own_red ? (size_t)own_rows(plan.bn, plan.S) * 512 * MT * plan.S : 0;
     const size_t table = a.l.perm ? 8 * (size_t)(a.l.N + 1) : 0;
-    a.stages = (int)std::min<size_t>(PAIR_STAGES, (PAIR_SMEM - 1024 - EPI_WARPS * 1024 * MT - table - red) / slot);
+    const size_t epi = plan.S > 1 ? 0 : EPI_WARPS * EPI_BYTES;   // sums of an exchange lie as the epilogue wants them
+    a.stages = (int)std::min<size_t>(PAIR_STAGES, (PAIR_SMEM - 1024 - epi - table - red) / slot);
     a.epi_at = (uint32_t)(a.stages * slot + red);
-    a.table_at = a.epi_at + EPI_WARPS * 1024 * MT;
+    a.table_at = (uint32_t)(a.epi_at + epi);
     return launch_after(linear_pair_kernel<MODE, MT, KT>, dim3((unsigned)(plan.clusters * 2 * plan.S)), pair_threads<MODE>(),
                         PAIR_SMEM, 2u * plan.S, st, a);
 }

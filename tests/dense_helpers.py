@@ -10,7 +10,9 @@ in any order: z is exact, whatever the kernel's order.  Then y is off by its act
                       roundings, which e^-u multiplies by |u|: 4 |u| units of 2^-24; sum, reciprocal or quotient (1 to 2
                       units) and the rest 5 units: (9 + 3.2 |u|) 2^-23
     gelu              z erfc(v) / 2, v = -z / sqrt 2 rounded twice; erfc changes by at most (2 v^2 + 2) of a relative change
-                      of v: (2 v^2 + 2) units; erfcf 4 units (CUDA's bound), two products: (8 + 2 v^2) 2^-23 = (8 + z^2) 2^-23
+                      of v: (2 v^2 + 2) units; erfcf 4 units (CUDA's bound), two products: (8 + 2 v^2) 2^-23 = (8 + z^2) 2^-23.
+                      bf16 results: the exponent -z^2 / 2 rounded twice, z^2 / 2 units of 2^-24 each, exponential and reciprocal 2
+                      each, the fit 1, three products: within the same
     gated             one product more, residual one sum more: 2^-24 each of their results
 and, where fp32 cannot hold e^-u or a quotient (below 2^-126), 2^-120.
 Any inputs, no activation: fp32 accumulation of K exact products in any order is off by at most K 2^-23 sum |x w| (2^-23: a

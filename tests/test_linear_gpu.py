@@ -158,6 +158,22 @@ def test_activations_far_out(cuda_lib, dtype, act):
     tol = want.abs() * (torch.finfo(dtype).eps / 2 + (9 + 4 * u + u * u) * 2.0 ** -23) + 2.0 ** -120
     for row in y.cpu():
         assert_close(row, want, tol)
+    ends = torch.tensor([math.inf, -math.inf, math.nan, 0] * 4, dtype=dtype)
+    y = _run({"x": x, "w": w, "bias": ends.cuda(), "addend": None, "residual": None}, 16, False, act).cpu()
+    assert (y[:, 0::4] == math.inf).all() and torch.isnan(y[:, 1::4]).all() and torch.isnan(y[:, 2::4]).all() and (y[:, 3::4] == 0).all()
+
+
+@pytest.mark.parametrize("act", [lora.ACT_SILU, lora.ACT_GELU, lora.ACT_GELU_TANH])
+def test_activations_of_every_bf16(cuda_lib, act):
+    """All finite bf16 z in [-14, 60], from the bias."""
+    z = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    z = z[torch.isfinite(z) & (z >= -14) & (z <= 60)]
+    n = z.numel() // 8 * 8
+    z = z[:n].cuda()
+    x, w = torch.zeros(2, 8, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, 8, dtype=torch.bfloat16, device="cuda")
+    y = _run({"x": x, "w": w, "bias": z, "addend": None, "residual": None}, n, False, act)
+    want, tol = dense64(x.double(), w.double(), bias=z.double(), act=act)
+    assert_close(y, want, tol)
 
 
 def act_of(z, act):
