@@ -535,11 +535,12 @@ LORA_API int lora_mx_linear(void *y, int64_t ld_y, const lora_mx *x, const lora_
  *     y[i][c] = act(z[i][c]) + residual[i][c]                             n_w = d_out
  *     y[i][c] = act(z[i][c]) * z[i][d_out + c] + residual[i][c]           gated: n_w = 2 d_out
  * with fp32 sums in a fixed order and one rounding into y.  The adapters' delta comes in as the addend, ahead of the
- * activation (lora_add_linear into zeros), or as the residual, behind it.  act, z >= 0 or not, by its formula:
+ * activation (lora_add_linear into zeros), or as the residual, behind it.
  *     LORA_ACT_NONE z;  _SILU z / (1 + e^-z);  _GELU z erfc(-z / sqrt 2) / 2;
  *     _GELU_TANH z / (1 + e^-2u), u = sqrt(2 / pi) (z + 0.044715 z^3);  _RELU 0 below 0, else z
- * (-infinity gives NaN in all but NONE and RELU).  bf16 rows in steps of 16 bytes run on the tensor cores, others and
- * fp32 on the ordinary units, with fp32 products.
+ * (NaN stays NaN; -infinity gives NaN in all but NONE and RELU).  bf16 data runs on the tensor cores, fastest where rows
+ * of x and w, and of y and the epilogue's operands, lie in steps of 16 bytes; fp32 data on the ordinary units, with fp32
+ * products.
  */
 typedef enum { LORA_ACT_NONE = 0, LORA_ACT_SILU = 1, LORA_ACT_GELU = 2, LORA_ACT_GELU_TANH = 3, LORA_ACT_RELU = 4 } lora_act;
 
