@@ -19,14 +19,15 @@
 //
 // Bound.  Few rows: HBM behind about 4 us that any call takes (1 x 4096 x 4096 9.4 us; 16 x 8192 x 28672 73.6 us = 6.4 TB/s;
 // 8 experts of 4096 x 2 x 14336, 64 tokens, 290 us = 6.5 TB/s, 99 % of the measured copy rate).  Many rows: the tensor cores
-// (8192 x 4096 x 2 x 14336 1200 us = 1600 TFLOP/s in a short burst, 1420 at the power cap; the issuing warp waits for no
+// (8192 x 4096 x 2 x 14336 1190 us = 1620 TFLOP/s in a short burst, 1417 at the power cap; the issuing warp waits for no
 // operands: 513 clocks a step of 512).  Between, 100 to 1000 rows: the operands' way into shared memory, about 64 bytes a
-// clock and SM, and the exchange (257 x 14336 x 4096 34.7 us, its floor 19.7).  Many small experts (8192 tokens, 4 of 64, 2048 x
+// clock and SM, and the exchange (257 x 14336 x 4096 34.7 us, its floor 19.7).  Many rows, few columns: the epilogue's latencies
+// (4126 x 128 x 13536 72 us, 1.6 TB/s).  Many small experts (8192 tokens, 4 of 64, 2048 x
 // 2 x 1024: 240 us): 630 clocks a step where dense rows take 513, at 1.35 GHz under the power cap.
 //
 // Measured and dropped: 16-bit accesses of y and the operands straight from tensor memory's layout (see the epilogue); one accumulator
 // of 512 x 256 (8192 x 4096 x 2 x 14336 1380 us); W prefetched to L2 eight steps ahead (experts 262 -> 268, decode 291 -> 430);
-// x in a deeper ring of its own (experts: no gain).
+// x in a deeper ring of its own (experts: no gain); the next 16 columns of tensor memory asked for ahead (4126 x 128 x 13536 72 -> 76).
 #include "linear.cuh"
 #include "pipe.cuh"
 
@@ -436,7 +437,8 @@ __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(co
         // A warp reads 32 lanes of tensor memory: features f, a row of x in each column.  Through shared memory of its own, eight
         // or 16 rows at a time, a thread gets eight columns of one row, four neighbours the warp's 32: one 16-byte access of each
         // operand and of y where there were eight of two bytes, each with its address.  (As they lie in tensor memory: 256 rows
-        // 5.5 us for 256 features, and a chunk's operands, loaded one after the other, up to 0.5 us a row.)
+        // 5.5 us for 256 features, and a chunk's operands, loaded one after the other, up to 0.5 us a row; 8192 x 1024 x 4096
+        // with a residual: eight rows at a time 110 us, 16 79.)
         const int q = warp & 3, f = 32 * q + lane;
         const int side = warp >= FIRST_EPI + 4;             // which of the two warps of these lanes
         const int l_row = lane >> 2, l_col = 32 * q + 8 * (lane & 3);   // this thread's row of eight and columns
