@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -650,7 +651,7 @@ def _call_on(index, stream, fn, *args):
         st = torch._C._cuda_getCurrentRawStream(index)
     else:
         st = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:   # torch.cuda.current_device(), past its look for a started CUDA: a tensor is there
         rc = fn(*args, st)
     else:
         with torch.cuda.device(index):
@@ -737,37 +738,56 @@ def lora_mx_linear(y, x, w, status, stream=None):
 
 
 # ---------------------------------------------------------------- dense base, experts
+# Small calls cost what their checks cost: each property of a tensor is asked for once.
 def _operand(t, what, n, d, index, dtype):
     """(address, row stride) of an operand that must be [n, d] of x's dtype on CUDA device `index`."""
-    if not isinstance(t, torch.Tensor) or t.shape != (n, d) or t.dtype is not dtype:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != (n, d):
         raise LoraError(f"{what} must be [{n}, {d}] of x's dtype {dtype}")
-    _, _, ld = _matrix(t, what)
+    ld, one = t.stride()
+    if one != 1 and d > 1:
+        raise LoraError(f"{what} must be 2-D with unit column stride")
+    if n <= 1:
+        ld = d
+    elif ld < d:
+        raise LoraError(f"{what}'s rows overlap")
     if t.get_device() != index:
         raise LoraError(f"{what} must be on cuda:{index}")
     return t.data_ptr(), ld
 
 
+def _flat(t, what, shape, dtype, index):
+    """The address of a contiguous tensor of this shape and dtype on CUDA device `index`."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise LoraError(f"{what} must be contiguous {list(shape)} of {dtype}")
+    if t.get_device() != index:
+        raise LoraError(f"{what} must be on cuda:{index}")
+    return t.data_ptr()
+
+
+_EPILOGUE = struct.Struct("@PPqPqii")   # lora_epilogue's fields, as bytes (a ctypes struct takes a microsecond to make)
+assert _EPILOGUE.size == ctypes.sizeof(lora_epilogue)
+
+
 def _epilogue(T, n_w, n, index, dtype, bias, bias_shape, addend, residual, act, gated):
-    """(address, owner) of the call's lora_epilogue."""
+    """The call's lora_epilogue."""
     if act not in (ACT_NONE, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU):
         raise LoraError("act is one of ACT_NONE, ACT_SILU, ACT_GELU, ACT_GELU_TANH, ACT_RELU")
-    ep = lora_epilogue(None, None, 0, None, 0, act, 1 if gated else 0)
+    pb = pa = la = pr = lr = 0
     if bias is not None:
-        if not isinstance(bias, torch.Tensor) or bias.shape != bias_shape or bias.dtype is not dtype or \
-                not bias.is_contiguous():
-            raise LoraError(f"bias must be contiguous {list(bias_shape)} of x's dtype")
-        ep.bias = _cuda_on(bias, "bias", index)
+        pb = _flat(bias, "bias", bias_shape, dtype, index)
     if addend is not None:
-        ep.addend, ep.ld_addend = _operand(addend, "addend", T, n_w, index, dtype)
+        pa, la = _operand(addend, "addend", T, n_w, index, dtype)
     if residual is not None:
-        ep.residual, ep.ld_residual = _operand(residual, "residual", T, n, index, dtype)
-    return ctypes.addressof(ep), ep
+        pr, lr = _operand(residual, "residual", T, n, index, dtype)
+    return _EPILOGUE.pack(pb, pa, la, pr, lr, act, 1 if gated else 0)
 
 
 def _status_on(status, index):
-    if not isinstance(status, torch.Tensor) or status.dtype != torch.int32 or status.numel() < 1:
+    if not isinstance(status, torch.Tensor) or status.dtype is not torch.int32 or status.numel() < 1:
         raise LoraError("status must be an int32 tensor")
-    return _cuda_on(status, "status", index)
+    if status.get_device() != index:
+        raise LoraError(f"status must be on cuda:{index}")
+    return status.data_ptr()
 
 
 def lora_linear(y, x, w, status, bias=None, addend=None, residual=None, act=ACT_NONE, gated=False, stream=None):
@@ -778,18 +798,22 @@ def lora_linear(y, x, w, status, bias=None, addend=None, residual=None, act=ACT_
     n_w, dw, ld_w = _matrix(w, "w")
     if T > MAX_ROWS or d > MX_MAX or n_w > MX_MAX or d < 1 or n_w < 1:
         raise LoraError(f"x has at most {MAX_ROWS} rows, x and w 1 to {MX_MAX} columns, w 1 to {MX_MAX} rows")
-    if dw != d or w.dtype is not x.dtype or (gated and n_w & 1):
+    dtype = x.dtype
+    if dw != d or w.dtype is not dtype or (gated and n_w & 1):
         raise LoraError(f"w must be [n, {d}] of x's dtype, n even where gated")
+    index = x.get_device()
     if not x.is_cuda:
         raise LoraError("x must be a CUDA tensor")
-    code, index, dtype = _dtype_of(x), x.get_device(), x.dtype
+    code = _CODES.get(dtype)
+    if code is None:
+        code = _dtype_of(x)
     n = n_w // 2 if gated else n_w
     py, ld_y = _operand(y, "y", T, n, index, dtype)
-    at = own = None
+    ep = None
     if bias is not None or addend is not None or residual is not None or act or gated:
-        at, own = _epilogue(T, n_w, n, index, dtype, bias, (n_w,), addend, residual, act, gated)
+        ep = _epilogue(T, n_w, n, index, dtype, bias, (n_w,), addend, residual, act, gated)
     _call_on(index, stream, (_lib or load()).lora_linear, py, ld_y, x.data_ptr(), ld_x, _cuda_on(w, "w", index), ld_w, T, d,
-             n, at, code, _status_on(status, index))
+             n, ep, code, _status_on(status, index))
 
 
 def lora_expert_linear(y, x, w, meta: Meta, status, x_div=1, bias=None, addend=None, residual=None, act=ACT_NONE,
@@ -798,32 +822,31 @@ def lora_expert_linear(y, x, w, meta: Meta, status, x_div=1, bias=None, addend=N
     [N, n (gated: 2n), d] and bias[e] of bias [N, n (2n)]; meta: lora_build_segments of the slots' expert ids (T =
     slots).  Rows of slots without an expert are left as they were."""
     R, d, ld_x = _matrix(x, "x")
-    if not isinstance(w, torch.Tensor) or w.dim() != 3 or not w.is_contiguous() or w.dtype is not x.dtype or \
-            w.shape[0] != meta.N or w.shape[2] != d or (gated and w.shape[1] & 1):
-        raise LoraError(f"w must be contiguous [{meta.N}, n, {d}] of x's dtype, n even where gated")
-    n_w = w.shape[1]
-    if R > MX_MAX or d > MX_MAX or n_w > MX_MAX or d < 1 or n_w < 1 or meta.N > MAX_EXPERTS:
+    dtype, slots, N = x.dtype, meta.T, meta.N
+    if not isinstance(w, torch.Tensor) or w.dim() != 3 or not w.is_contiguous() or w.dtype is not dtype:
+        raise LoraError(f"w must be contiguous [{N}, n, {d}] of x's dtype, n even where gated")
+    wn, n_w, dw = w.shape
+    if wn != N or dw != d or (gated and n_w & 1):
+        raise LoraError(f"w must be contiguous [{N}, n, {d}] of x's dtype, n even where gated")
+    if R > MX_MAX or d > MX_MAX or n_w > MX_MAX or d < 1 or n_w < 1 or N > MAX_EXPERTS:
         raise LoraError(f"at most {MX_MAX} rows of x, 1 to {MX_MAX} columns and rows of w, {MAX_EXPERTS} experts")
-    if not 1 <= x_div <= MAX_ROWS or R * x_div < meta.T:
+    if not 1 <= x_div <= MAX_ROWS or R * x_div < slots:
         raise LoraError("x must hold a row for every slot: ceil(slots / x_div)")
+    index = x.get_device()
     if not x.is_cuda:
         raise LoraError("x must be a CUDA tensor")
-    code, index, dtype = _dtype_of(x), x.get_device(), x.dtype
+    code = _CODES.get(dtype)
+    if code is None:
+        code = _dtype_of(x)
     if meta.perm.get_device() != index:
         raise LoraError(f"meta must be on cuda:{index}")
     n = n_w // 2 if gated else n_w
-    py, ld_y = _operand(y, "y", meta.T, n, index, dtype)
-    at = own = None
+    py, ld_y = _operand(y, "y", slots, n, index, dtype)
+    ep = None
     if bias is not None or addend is not None or residual is not None or act or gated:
-        at, own = _epilogue(meta.T, n_w, n, index, dtype, bias, (meta.N, n_w), addend, residual, act, gated)
+        ep = _epilogue(slots, n_w, n, index, dtype, bias, (N, n_w), addend, residual, act, gated)
     _call_on(index, stream, (_lib or load()).lora_expert_linear, py, ld_y, x.data_ptr(), ld_x, R, x_div,
-             _cuda_on(w, "w", index), d, n, ctypes.byref(meta.c), at, code, _status_on(status, index))
-
-
-def _choices(t, what, T, k, dtype, index):
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_contiguous() or t.numel() != T * k:
-        raise LoraError(f"{what} must be contiguous [{T}, {k}] of {dtype}")
-    return _cuda_on(t, what, index)
+             _cuda_on(w, "w", index), d, n, ctypes.byref(meta.c), ep, code, _status_on(status, index))
 
 
 def lora_expert_route(ids, weights, logits, score=SCORE_SOFTMAX, renormalize=True, scale=1.0, stream=None):
@@ -831,18 +854,19 @@ def lora_expert_route(ids, weights, logits, score=SCORE_SOFTMAX, renormalize=Tru
     lowest expert, and weights fp32 [T, k]: softmax over all experts or sigmoid, over the token's sum where
     renormalize, times scale.  -infinity and NaN close an expert; id -1 and weight 0 where fewer than k are open."""
     T, n, ld = _matrix(logits, "logits")
-    if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or ids.shape[0] != T:
+    shape = ids.shape if isinstance(ids, torch.Tensor) else ()
+    if len(shape) != 2 or shape[0] != T:
         raise LoraError(f"ids must be [{T}, k]")
-    k = ids.shape[1]
+    k = shape[1]
     if T > MAX_ROWS or not 1 <= n <= MAX_EXPERTS or not 1 <= k <= min(n, MAX_TOPK):
         raise LoraError(f"at most {MAX_ROWS} tokens, {MAX_EXPERTS} experts, k of 1 to {MAX_TOPK} and at most the experts")
     if score not in (SCORE_SOFTMAX, SCORE_SIGMOID):
         raise LoraError("score is SCORE_SOFTMAX or SCORE_SIGMOID")
+    index = logits.get_device()
     if not logits.is_cuda:
         raise LoraError("logits must be a CUDA tensor")
-    index = logits.get_device()
-    _call_on(index, stream, (_lib or load()).lora_expert_route, _choices(ids, "ids", T, k, torch.int32, index),
-             _choices(weights, "weights", T, k, torch.float32, index), logits.data_ptr(), ld, T, n, k, score,
+    _call_on(index, stream, (_lib or load()).lora_expert_route, _flat(ids, "ids", shape, torch.int32, index),
+             _flat(weights, "weights", shape, torch.float32, index), logits.data_ptr(), ld, T, n, k, score,
              1 if renormalize else 0, float(scale), _dtype_of(logits))
 
 
@@ -850,16 +874,18 @@ def lora_expert_sum(y, x, ids, weights, n_experts, residual=None, stream=None):
     """y [T, d] = residual + the weighted rows of each token's k slots: x [T k, d], ids int32 and weights fp32 [T, k];
     slots whose id is outside [0, n_experts) are left out.  y may be residual."""
     T, d, ld_y = _matrix(y, "y")
-    if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or ids.shape[0] != T:
+    shape = ids.shape if isinstance(ids, torch.Tensor) else ()
+    if len(shape) != 2 or shape[0] != T:
         raise LoraError(f"ids must be [{T}, k]")
-    k = ids.shape[1]
+    k = shape[1]
     if T > MAX_ROWS or not 1 <= d <= MX_MAX or not 1 <= k <= MAX_TOPK or not 1 <= n_experts <= MAX_EXPERTS:
         raise LoraError(f"at most {MAX_ROWS} tokens, 1 to {MX_MAX} columns, {MAX_TOPK} slots a token, {MAX_EXPERTS} experts")
+    index = y.get_device()
     if not y.is_cuda:
         raise LoraError("y must be a CUDA tensor")
-    code, index, dtype = _dtype_of(y), y.get_device(), y.dtype
+    code, dtype = _dtype_of(y), y.dtype
     px, ld_x = _operand(x, "x", T * k, d, index, dtype)
     pr, ld_r = (None, 0) if residual is None else _operand(residual, "residual", T, d, index, dtype)
     _call_on(index, stream, (_lib or load()).lora_expert_sum, y.data_ptr(), ld_y, px, ld_x,
-             _choices(ids, "ids", T, k, torch.int32, index), _choices(weights, "weights", T, k, torch.float32, index),
+             _flat(ids, "ids", shape, torch.int32, index), _flat(weights, "weights", shape, torch.float32, index),
              n_experts, T, k, d, pr, ld_r, code)
