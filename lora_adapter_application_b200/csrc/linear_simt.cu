@@ -270,7 +270,7 @@ int launch_as(const LinArgs &a, int sms, cudaStream_t st) {
     const int per_group = a.perm ? (a.T + a.N - 1) / a.N : a.T;
     if (per_group <= 2 * DOT_ROWS) {
         const int cols = DOT_WARPS * DOT_FEATURES / (GATED ? 2 : 1);
-        const int tiles = row_tiles(DOT_ROWS);   // at most 3072 of them, and 65536 blocks of features
+        const int tiles = row_tiles(DOT_ROWS);   // a few thousand of them at most, and 65536 blocks of features
         return launch_after(linear_dot_kernel<GATED>, dim3(tiles * ((a.d_out + cols - 1) / cols)), 32 * DOT_WARPS, 0, 0, st, a, vec, tiles);
     }
     // the largest tile that gives every SM one (64 x 4096 x 14336: 296 us on 64 x 64, 384 on 32 x 64)
