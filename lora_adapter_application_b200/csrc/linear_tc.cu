@@ -67,7 +67,7 @@ struct PairArgs {
     int own_red;         // the partial sums' place is behind the ring
     uint32_t epi_at;     // the epilogue's, behind both
     uint32_t table_at;   // experts: row tiles and slots before each, behind that
-    int vec;             // y, addend, residual and bias in 16-byte steps
+    int step;            // elements of an access to y, addend, residual and bias: 8, 2 or 1
     unsigned limit;
     int stall;
 };
@@ -102,24 +102,33 @@ struct Operands {
     uint4 add[MT], res[MT];
     int64_t row;
 };
-// n (0 to 8) elements at p; vec: 16-byte steps, n is 0 or 8
-__device__ __forceinline__ uint4 load_cols(const __nv_bfloat16 *p, int n, bool vec) {
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (vec) {
-        if (n > 0) u = *reinterpret_cast<const uint4 *>(p);
-    } else {
-        uint32_t w[8];
+// n (0 to 8) elements at p; step: elements of an access, 8, 2 or 1, of which n is a multiple
+__device__ __forceinline__ uint4 load_cols(const __nv_bfloat16 *p, int n, int step) {
+    if (step == 8) return n > 0 ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
+    uint32_t w[4];
+    if (step == 2) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = i < n ? __bfloat16_as_ushort(p[i]) : 0u;
-        u = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
-    }
-    return u;
-}
-__device__ __forceinline__ void store_cols(__nv_bfloat16 *p, const uint4 &u, int n, bool vec) {
-    if (vec) {
-        if (n > 0) *reinterpret_cast<uint4 *>(p) = u;
+        for (int i = 0; i < 4; ++i) w[i] = 2 * i < n ? *reinterpret_cast<const uint32_t *>(p + 2 * i) : 0u;
     } else {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint32_t h[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[i] = i < n ? __bfloat16_as_ushort(p[i]) : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = h[2 * i] | h[2 * i + 1] << 16;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store_cols(__nv_bfloat16 *p, const uint4 &u, int n, int step) {
+    if (step == 8) {
+        if (n > 0) *reinterpret_cast<uint4 *>(p) = u;
+        return;
+    }
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if (step == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (2 * i < n) *reinterpret_cast<uint32_t *>(p + 2 * i) = w[i];
+    } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i < n) p[i] = __ushort_as_bfloat16((unsigned short)(w[i >> 1] >> (16 * (i & 1))));
@@ -448,7 +457,7 @@ __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(co
         const __nv_bfloat16 *const add = static_cast<const __nv_bfloat16 *>(l.addend);
         const __nv_bfloat16 *const res = static_cast<const __nv_bfloat16 *>(l.residual);
         const __nv_bfloat16 *const bias = static_cast<const __nv_bfloat16 *>(l.bias);
-        const bool vec = a.vec;
+        const int step = a.step;
         int n = 0;
         for (int t = cluster; t < tiles && !failed; t += clusters, ++n) {
             const Tile p = place(t);
@@ -459,18 +468,18 @@ __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(co
             uint4 bz[MT];
 #pragma unroll
             for (int u = 0; u < MT; ++u)
-                bz[u] = bias ? load_cols(bias + (int64_t)p.e * l.n_w + m + u * a.up, u ? n1 : n0, vec) : make_uint4(0, 0, 0, 0);
+                bz[u] = bias ? load_cols(bias + (int64_t)p.e * l.n_w + m + u * a.up, u ? n1 : n0, step) : make_uint4(0, 0, 0, 0);
 
             auto fetch = [&](Operands<MT> &o, int r) {   // for tile row r (past the last: the last one again)
                 const int at = p.q0 + min(r, p.cnt - 1);
                 o.row = grouped ? l.perm[at] : at;
                 if (add) {
-                    o.add[0] = load_cols(add + o.row * l.ld_a + m, n0, vec);
-                    if (MT == 2) o.add[MT - 1] = load_cols(add + o.row * l.ld_a + m + a.up, n1, vec);
+                    o.add[0] = load_cols(add + o.row * l.ld_a + m, n0, step);
+                    if (MT == 2) o.add[MT - 1] = load_cols(add + o.row * l.ld_a + m + a.up, n1, step);
                 }
                 if (res) {
-                    o.res[0] = load_cols(res + o.row * l.ld_r + m, n0, vec);
-                    if (MT == 2 && !a.gated) o.res[MT - 1] = load_cols(res + o.row * l.ld_r + m + a.up, n1, vec);
+                    o.res[0] = load_cols(res + o.row * l.ld_r + m, n0, step);
+                    if (MT == 2 && !a.gated) o.res[MT - 1] = load_cols(res + o.row * l.ld_r + m + a.up, n1, step);
                 }
             };
             auto plus = [](float *z, const uint4 &u) {
@@ -496,12 +505,12 @@ __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(co
                         activate<true, 8>(l.act, z[MT - 1]);
                         if (res) plus(z[MT - 1], o.res[MT - 1]);
                         raw_round(z[MT - 1], out);
-                        if (there) store_cols(to + a.up, out, n1, vec);
+                        if (there) store_cols(to + a.up, out, n1, step);
                     }
                 }
                 if (res) plus(z[0], o.res[0]);
                 raw_round(z[0], out);
-                if (there) store_cols(to, out, n0, vec);
+                if (there) store_cols(to, out, n0, step);
             };
             // eight floats of a row of 128 bytes (buf) or 512 (partial sums); odd rows take their halves the other way round, so
             // that eight threads meet no bank twice
@@ -722,8 +731,11 @@ int launch_pair(PairArgs &a, const PairPlan &plan, cudaStream_t st) {
     a.m_tiles = m_tiles_of(a.l, a.gated, MT);
     a.own_red = plan.S > 1 && plan.bn <= 32;
     a.n_k = (a.l.d_in + 64 * KT - 1) / (64 * KT);
-    a.vec = mx_vec(a.l.y, a.l.ld_y, a.l.d_out, 2) && (!a.l.addend || mx_vec(a.l.addend, a.l.ld_a, a.l.d_out, 2)) &&
-            (!a.l.residual || mx_vec(a.l.residual, a.l.ld_r, a.l.d_out, 2)) && (!a.l.bias || mx_aligned(a.l.bias, 16));
+    a.step = a.l.d_out % 8 == 0 ? 8 : a.l.d_out % 2 == 0 ? 2 : 1;
+    auto allow = [&](const void *p, int64_t ld) {   // rows of ld elements at p
+        while (p && (!mx_aligned(p, 2 * a.step) || ld % a.step)) a.step = a.step == 8 ? 2 : 1;
+    };
+    allow(a.l.y, a.l.ld_y), allow(a.l.addend, a.l.ld_a), allow(a.l.residual, a.l.ld_r), allow(a.l.bias, 0);
     const size_t slot = (16384u * MT + 64u * (size_t)plan.bn) * KT, red = a.own_red ? (size_t)own_rows(plan.bn, plan.S) * 512 * MT * plan.S : 0;
     const size_t table = a.l.perm ? 8 * (size_t)(a.l.N + 1) : 0;
     const size_t epi = plan.S > 1 ? 0 : EPI_WARPS * EPI_BYTES;   // sums of an exchange lie as the epilogue wants them
