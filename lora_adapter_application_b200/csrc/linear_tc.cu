@@ -102,13 +102,23 @@ struct Operands {
     uint4 add[MT], res[MT];
     int64_t row;
 };
-// n (0 to 8) elements at p; step: elements of an access, 8, 2 or 1, of which n is a multiple
+// n (0 to 8) elements at p; step: elements of an access, 8, 2 or 1, of which n is a multiple.  At step 1 eight elements
+// go as words all the same: four, or three between two halves where p is off a word.
+__device__ __forceinline__ bool off_word(const void *p) { return reinterpret_cast<uintptr_t>(p) & 2; }
 __device__ __forceinline__ uint4 load_cols(const __nv_bfloat16 *p, int n, int step) {
     if (step == 8) return n > 0 ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
     uint32_t w[4];
-    if (step == 2) {
+    if (step == 2 || (n == 8 && !off_word(p))) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = 2 * i < n ? *reinterpret_cast<const uint32_t *>(p + 2 * i) : 0u;
+    } else if (n == 8) {
+        uint32_t m[5];
+        m[0] = (uint32_t)__bfloat16_as_ushort(p[0]) << 16;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) m[i + 1] = *reinterpret_cast<const uint32_t *>(p + 1 + 2 * i);
+        m[4] = __bfloat16_as_ushort(p[7]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(m[i], m[i + 1], 16);
     } else {
         uint32_t h[8];
 #pragma unroll
@@ -124,10 +134,15 @@ __device__ __forceinline__ void store_cols(__nv_bfloat16 *p, const uint4 &u, int
         return;
     }
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    if (step == 2) {
+    if (step == 2 || (n == 8 && !off_word(p))) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (2 * i < n) *reinterpret_cast<uint32_t *>(p + 2 * i) = w[i];
+    } else if (n == 8) {
+        p[0] = __ushort_as_bfloat16((unsigned short)w[0]);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) *reinterpret_cast<uint32_t *>(p + 1 + 2 * i) = __funnelshift_r(w[i], w[i + 1], 16);
+        p[7] = __ushort_as_bfloat16((unsigned short)(w[3] >> 16));
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
