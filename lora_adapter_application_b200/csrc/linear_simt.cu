@@ -145,8 +145,8 @@ __device__ __forceinline__ float sum2(uint64_t v) {
     return __uint_as_float((uint32_t)v) + __uint_as_float((uint32_t)(v >> 32));
 }
 
-template <bool GATED, int BM, int BN, int TM, int TN, int KG, int TILE_K, int STAGES>
-__global__ void __launch_bounds__(KG * (BM / TM) * (BN / TN)) linear_tile_kernel(const LinArgs a, int vec) {
+template <bool GATED, int BM, int BN, int TM, int TN, int KG, int TILE_K, int STAGES, int BLOCKS>
+__global__ void __launch_bounds__(KG * (BM / TM) * (BN / TN), BLOCKS) linear_tile_kernel(const LinArgs a, int vec) {
     constexpr int GROUP = (BM / TM) * (BN / TN), THREADS = KG * GROUP, ROWS = BM + BN, TX = BN / TN, H = BN / 2, TILE_LD = TILE_K + 4;
     static_assert(TN % 2 == 0 && TX % 8 == 0 && GROUP % 32 == 0 && BM / TM % 4 == 0, "gate and up in one thread, whole warps");
     extern __shared__ __align__(16) float lin_tiles[];   // [STAGES][ROWS][TILE_LD]
@@ -252,11 +252,11 @@ __global__ void __launch_bounds__(KG * (BM / TM) * (BN / TN)) linear_tile_kernel
     }
 }
 
-template <bool GATED, int BM, int BN, int TM, int TN, int KG, int TILE_K, int STAGES>
+template <bool GATED, int BM, int BN, int TM, int TN, int KG, int TILE_K, int STAGES, int BLOCKS>
 int launch_tile(const LinArgs &a, int vec, int row_tiles, cudaStream_t st) {
     constexpr int COLS = GATED ? BN / 2 : BN;
     constexpr size_t SMEM = (size_t)STAGES * (BM + BN) * (TILE_K + 4) * sizeof(float);
-    auto kernel = linear_tile_kernel<GATED, BM, BN, TM, TN, KG, TILE_K, STAGES>;
+    auto kernel = linear_tile_kernel<GATED, BM, BN, TM, TN, KG, TILE_K, STAGES, BLOCKS>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM);
     if (e != cudaSuccess) return cuda_rc(e);
     return launch_after(kernel, dim3(row_tiles, (a.d_out + COLS - 1) / COLS), KG * (BM / TM) * (BN / TN), SMEM, 0, st, a, vec);
@@ -273,11 +273,13 @@ int launch_as(const LinArgs &a, int sms, cudaStream_t st) {
         const int tiles = row_tiles(DOT_ROWS);   // a few thousand of them at most, and 65536 blocks of features
         return launch_after(linear_dot_kernel<GATED>, dim3(tiles * ((a.d_out + cols - 1) / cols)), 32 * DOT_WARPS, 0, 0, st, a, vec, tiles);
     }
-    // the largest tile that gives every SM one (64 x 4096 x 14336: 296 us on 64 x 64, 384 on 32 x 64)
+    // the largest tile that gives every SM one (64 x 4096 x 14336: 263 us on 64 x 64, 384 on 32 x 64).
+    // Two blocks of 64 x 64 share an SM, for the four registers that this spills: its 224 tiles are one wave and a half
+    // (295 us with one block); two of 128 x 64 gain nothing (512 x 4096 x 4096: 484 and 487 us).
     auto tiles = [&](int bm, int bn) { return (int64_t)row_tiles(bm) * ((a.n_w + bn - 1) / bn); };
-    if (per_group > 64 && tiles(128, 64) >= sms) return launch_tile<GATED, 128, 64, 8, 4, 1, 32, 3>(a, vec, row_tiles(128), st);
-    if (per_group > 32 && tiles(64, 64) >= sms) return launch_tile<GATED, 64, 64, 8, 4, 2, 32, 3>(a, vec, row_tiles(64), st);
-    return launch_tile<GATED, 32, 64, 4, 4, 4, 64, 3>(a, vec, row_tiles(32), st);
+    if (per_group > 64 && tiles(128, 64) >= sms) return launch_tile<GATED, 128, 64, 8, 4, 1, 32, 3, 1>(a, vec, row_tiles(128), st);
+    if (per_group > 32 && tiles(64, 64) >= sms) return launch_tile<GATED, 64, 64, 8, 4, 2, 32, 3, 2>(a, vec, row_tiles(64), st);
+    return launch_tile<GATED, 32, 64, 4, 4, 4, 64, 3, 1>(a, vec, row_tiles(32), st);
 }
 
 }  // namespace
