@@ -274,10 +274,10 @@ int launch_as(const LinArgs &a, int sms, cudaStream_t st) {
         return launch_after(linear_dot_kernel<GATED>, dim3(tiles * ((a.d_out + cols - 1) / cols)), 32 * DOT_WARPS, 0, 0, st, a, vec, tiles);
     }
     // the largest tile that gives every SM one (64 x 4096 x 14336: 263 us on 64 x 64, 384 on 32 x 64).
-    // Two blocks of 64 x 64 share an SM, for the four registers that this spills: its 224 tiles are one wave and a half
-    // (295 us with one block); two of 128 x 64 gain nothing (512 x 4096 x 4096: 484 and 487 us).
+    // Two blocks of 256 threads share an SM, for the four registers that this spills: with one, 64 x 4096 x 14336, a
+    // wave and a half of tiles, takes 295 us, and 512 x 4096 x 4096 508 instead of 487.
     auto tiles = [&](int bm, int bn) { return (int64_t)row_tiles(bm) * ((a.n_w + bn - 1) / bn); };
-    if (per_group > 64 && tiles(128, 64) >= sms) return launch_tile<GATED, 128, 64, 8, 4, 1, 32, 3, 1>(a, vec, row_tiles(128), st);
+    if (per_group > 64 && tiles(128, 64) >= sms) return launch_tile<GATED, 128, 64, 8, 4, 1, 32, 3, 2>(a, vec, row_tiles(128), st);
     if (per_group > 32 && tiles(64, 64) >= sms) return launch_tile<GATED, 64, 64, 8, 4, 2, 32, 3, 2>(a, vec, row_tiles(64), st);
     return launch_tile<GATED, 32, 64, 4, 4, 4, 64, 3, 1>(a, vec, row_tiles(32), st);
 }
