@@ -112,7 +112,8 @@ typedef enum {
     LORA_ERR_DTYPE = -2,      /* unknown element type */
     LORA_ERR_SHAPE = -3,      /* a size or stride is out of range or inconsistent */
     LORA_ERR_RANK = -4,       /* r_max outside [1, LORA_MAX_RANK] */
-    LORA_ERR_ALIGN = -5,      /* a microscaled matrix off its alignment (other data takes a slower path) */
+    LORA_ERR_ALIGN = -5,      /* a microscaled matrix off its alignment (other data takes a slower path); an address
+                                 off its elements' size, in lora_linear and the lora_expert_* calls */
     LORA_ERR_WORKSPACE = -6,  /* scratch or workspace smaller than required */
     LORA_ERR_CAPACITY = -7,   /* a tile-list capacity below lora_meta_capacity() */
     LORA_ERR_CUDA = -8        /* a CUDA launch failed (cudaGetLastError) */

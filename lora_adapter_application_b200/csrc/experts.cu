@@ -201,6 +201,7 @@ int lora_expert_route(int32_t *ids, float *weights, const void *logits, int64_t 
         return LORA_ERR_SHAPE;
     if (T == 0) return LORA_OK;
     if (!ids || !weights || !logits) return LORA_ERR_NULL;
+    if (!mx_aligned(ids, 4) || !mx_aligned(weights, 4) || !mx_aligned(logits, dtype == LORA_BF16 ? 2 : 4)) return LORA_ERR_ALIGN;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const int sigmoid = score == LORA_SCORE_SIGMOID, renorm = renormalize != 0;
     return dtype == LORA_BF16 ? launch_route<__nv_bfloat16>(ids, weights, logits, ld, T, n_experts, k, sigmoid, renorm, scale, st)
@@ -217,6 +218,9 @@ int lora_expert_sum(void *y, int64_t ld_y, const void *x, int64_t ld_x, const in
         return LORA_ERR_SHAPE;
     if (T == 0) return LORA_OK;
     if (!y || !x || !ids || !weights) return LORA_ERR_NULL;
+    const uintptr_t es = dtype == LORA_BF16 ? 2 : 4;
+    if (!mx_aligned(y, es) || !mx_aligned(x, es) || !mx_aligned(residual, es) || !mx_aligned(ids, 4) || !mx_aligned(weights, 4))
+        return LORA_ERR_ALIGN;
     if (y == x || (y == residual && ld_y != ld_r)) return LORA_ERR_SHAPE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return dtype == LORA_BF16 ? launch_sum<__nv_bfloat16>(y, ld_y, x, ld_x, ids, weights, n_experts, T, k, d, residual, ld_r, st)

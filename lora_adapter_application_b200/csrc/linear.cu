@@ -21,6 +21,11 @@ int check_dense(LinArgs &a, const lora_epilogue *ep, lora_dtype dtype) {
     if (!a.status) return LORA_ERR_NULL;
     if (a.T == 0) return LORA_OK;
     if (!a.y || !a.x || !a.w) return LORA_ERR_NULL;
+    const uintptr_t es = dtype == LORA_BF16 ? 2 : 4;
+    for (const void *p : {static_cast<const void *>(a.y), a.x, a.w, a.bias, a.addend, a.residual})
+        if (!mx_aligned(p, es)) return LORA_ERR_ALIGN;   // no access of an element reaches those
+    for (const int32_t *p : {static_cast<const int32_t *>(a.status), a.perm, a.seg_start})
+        if (!mx_aligned(p, 4)) return LORA_ERR_ALIGN;
     // in place over the residual, or over the addend where its columns are y's
     if (a.y == a.x || (a.y == a.residual && a.ld_y != a.ld_r) || (a.y == a.addend && (ep->gated || a.ld_y != a.ld_a)))
         return LORA_ERR_SHAPE;

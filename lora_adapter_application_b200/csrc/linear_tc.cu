@@ -748,7 +748,7 @@ int launch_pair(PairArgs &a, const PairPlan &plan, cudaStream_t st) {
     a.n_k = (a.l.d_in + 64 * KT - 1) / (64 * KT);
     a.step = a.l.d_out % 8 == 0 ? 8 : a.l.d_out % 2 == 0 ? 2 : 1;
     auto allow = [&](const void *p, int64_t ld) {   // rows of ld elements at p
-        while (p && (!mx_aligned(p, 2 * a.step) || ld % a.step)) a.step = a.step == 8 ? 2 : 1;
+        while (p && a.step > 1 && (!mx_aligned(p, 2 * a.step) || ld % a.step)) a.step = a.step == 8 ? 2 : 1;
     };
     allow(a.l.y, a.l.ld_y), allow(a.l.addend, a.l.ld_a), allow(a.l.residual, a.l.ld_r), allow(a.l.bias, 0);
     const size_t slot = (16384u * MT + 64u * (size_t)plan.bn) * KT, red = a.own_red ? (size_t)own_rows(plan.bn, plan.S) * 512 * MT * plan.S : 0;

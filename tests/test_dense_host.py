@@ -148,3 +148,38 @@ def test_sizes_past_the_limits_are_refused(lib):
             lora.lora_expert_linear(e(8, n), e(R_, d), e(3, n, d), m, st)
     with pytest.raises(LoraError, match="every slot"):
         lora.lora_expert_linear(e(8, 8), e(8, 8), e(3, 8, 8), m, st, x_div=big + 1)
+
+
+# ------------------------------------------------------------------- addresses off their elements' size
+ALIGN = -5
+
+
+@pytest.mark.parametrize("dt,off", [(0, 1), (1, 1), (1, 2), (1, 3)])
+def test_addresses_off_their_elements_are_refused(lib, dt, off):
+    """Odd addresses of bf16 data, and fp32 data, ids, weights and a status off four bytes: no kernel can read those."""
+    ep = {}
+
+    def linear(y=P, x=Q, w=R, st=P):
+        return lib.lora_linear(y, 96, x, 64, w, 64, 4, 64, 96, _ref(ep.get("e")), dt, st, None)
+
+    def experts(y=P, x=Q, w=R, st=P, **meta):
+        m = _meta(**meta)
+        return lib.lora_expert_linear(y, 96, x, 64, 4, 2, w, 64, 96, ctypes.byref(m), _ref(ep.get("e")), dt, st, None)
+    for call in (linear, experts):
+        for over in (dict(y=P + off), dict(x=Q + off), dict(w=R + off), dict(st=P + 2)):
+            assert call(**over) == ALIGN, (call.__name__, over)
+        for over in (dict(bias=R + off), dict(addend=R + off, ld_addend=96), dict(residual=R + off, ld_residual=96)):
+            ep["e"] = _ep(**over)
+            assert call() == ALIGN, (call.__name__, over)
+        ep.clear()
+    assert experts(perm=P + 2) == ALIGN and experts(seg_start=P + 2) == ALIGN
+
+    def route(ids=P, w=Q, logits=R):
+        return lib.lora_expert_route(ids, w, logits, 64, 4, 64, 8, 0, 1, 1.0, dt, None)
+    for over in (dict(ids=P + off), dict(w=Q + off), dict(logits=R + off)):
+        assert route(**over) == ALIGN, over
+
+    def total(y=P, x=Q, ids=R, w=R, r=None):
+        return lib.lora_expert_sum(y, 64, x, 64, ids, w, 8, 4, 2, 64, r, 64, dt, None)
+    for over in (dict(y=P + off), dict(x=Q + off), dict(ids=R + off), dict(w=R + off), dict(r=R + off)):
+        assert total(**over) == ALIGN, over
