@@ -603,8 +603,8 @@ LORA_API int lora_expert_linear(void *y, int64_t ld_y, const void *x, int64_t ld
 
 /*
  * y[t][c] = residual[t][c] + sum_{j < k} weights[t][j] * x[t * k + j][c] for t < T, c < d, over the slots whose id is in
- * [0, n_experts) (the rows of the others are not read), fp32 in slot order, one rounding.  residual may be NULL, or y
- * itself of the same stride; y overlaps nothing else.
+ * [0, n_experts) (the rows of the others are not read): fp32, the slots in order, then the residual, one rounding.
+ * residual may be NULL, or y itself of the same stride; y overlaps nothing else.
  */
 LORA_API int lora_expert_sum(void *y, int64_t ld_y, const void *x, int64_t ld_x, const int32_t *ids,
                              const float *weights, int32_t n_experts, int32_t T, int32_t k, int32_t d,

@@ -117,8 +117,9 @@ int launch_route(int32_t *ids, float *weights, const void *logits, int64_t ld, i
 
 // -------------------------------------------------------------------- sum
 // A warp takes 256 columns of a few tokens, eight a lane (VEC: 16-byte accesses; else 32 columns apart), and adds the slots'
-// rows in slot order, fp32, one rounding.  The tokens' ids and weights come in one load of the warp, ahead of all; four
-// rows' loads are in flight at a time.  Bound: HBM (8192 x 4 x 4096 with a residual 64.9 us, 95 % of the measured copy rate;
+// rows in slot order, then the residual, fp32, one rounding: ahead of the rows a residual, larger than they are, would have
+// every sum rounded at its size (33 x 8 x 2048 in fp32, four times a row: 7.0e-8 off the value for 2.6e-8).  The tokens' ids and weights come in one load of the warp, ahead of all; four
+// rows' loads are in flight at a time.  Bound: HBM (8192 x 4 x 4096 with a residual 64.4 us, 95 % of the measured copy rate;
 // with a block for each token 79.5).
 constexpr int SUM_WARPS = 4, SUM_TOKENS = 4;
 
@@ -139,15 +140,8 @@ __global__ void __launch_bounds__(32 * SUM_WARPS) sum_kernel(E *y, int64_t ld_y,
     const float my_w = lane < here * k ? weights[t0 * k + lane] : 0.f;
     for (int i = 0; i < here; ++i) {
         const int64_t t = t0 + i;
-        float acc[8], v[8];
-        if (res) {
-            Raw u;
-            load8<VEC>(res + t * ld_r, c0, d, lane, u);
-            raw_values(u, acc);
-        } else {
-#pragma unroll
-            for (int c = 0; c < 8; ++c) acc[c] = 0.f;
-        }
+        float acc[8] = {}, v[8];
+        Raw r;
         for (int j = 0; j < k; j += 4) {
             Raw u[4];
             float w[4];
@@ -161,6 +155,8 @@ __global__ void __launch_bounds__(32 * SUM_WARPS) sum_kernel(E *y, int64_t ld_y,
                 // the rows of slots without an expert hold nothing of use: not read
                 if (there[s]) load8<VEC>(x + (t * k + j + s) * ld_x, c0, d, lane, u[s]);
             }
+            // beside the last rows; behind them where halves are packed two to a register, which each waits for its load
+            if (VEC && res && j + 4 >= k) load8<VEC>(res + t * ld_r, c0, d, lane, r);
 #pragma unroll
             for (int s = 0; s < 4; ++s)
                 if (there[s]) {
@@ -168,6 +164,12 @@ __global__ void __launch_bounds__(32 * SUM_WARPS) sum_kernel(E *y, int64_t ld_y,
 #pragma unroll
                     for (int c = 0; c < 8; ++c) acc[c] = fmaf(w[s], v[c], acc[c]);
                 }
+        }
+        if (res) {
+            if (!VEC) load8<VEC>(res + t * ld_r, c0, d, lane, r);
+            raw_values(r, v);
+#pragma unroll
+            for (int c = 0; c < 8; ++c) acc[c] += v[c];
         }
         Raw u;
         raw_round(acc, u);

@@ -370,3 +370,15 @@ def test_run_case(cuda_lib):
     from lora_adapter_application_b200 import run_case
     assert run_case.main(["decode_qproj", "--base", "bf16", "--experts", "8", "--reps", "2"]) == 0
     assert run_case.main(["tiny", "--base", "bf16", "--experts", "3", "--reps", "1"]) == 0
+
+
+# ------------------------------------------------------------------------ sum: order
+@pytest.mark.parametrize("T", [3, 4099])
+@pytest.mark.parametrize("d", [264, 259])
+def test_sum_adds_the_residual_last(cuda_lib, T, d):
+    """Eight halves and 2^24: 2^24 + 4, where adding them to 2^24 one by one leaves it as it is (0.5 is a quarter of its last place)."""
+    k = 8
+    x, w = torch.ones(T * k, d, device="cuda"), torch.full((T, k), 0.5, device="cuda")
+    y = torch.full((T, d), 2.0 ** 24, device="cuda")
+    lora.lora_expert_sum(y, x, torch.zeros(T, k, dtype=torch.int32, device="cuda"), w, 1, residual=y)
+    assert (y == 2.0 ** 24 + 4).all()
