@@ -651,7 +651,7 @@ def _call_on(index, stream, fn, *args):
         st = torch._C._cuda_getCurrentRawStream(index)
     else:
         st = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch._C._cuda_getDevice() == index:   # torch.cuda.current_device(), past its look for a started CUDA: a tensor is there
+    if torch.cuda.current_device() == index:
         rc = fn(*args, st)
     else:
         with torch.cuda.device(index):

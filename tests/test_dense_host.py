@@ -183,3 +183,13 @@ def test_addresses_off_their_elements_are_refused(lib, dt, off):
         return lib.lora_expert_sum(y, 64, x, 64, ids, w, 8, 4, 2, 64, r, 64, dt, None)
     for over in (dict(y=P + off), dict(x=Q + off), dict(ids=R + off), dict(w=R + off), dict(r=R + off)):
         assert total(**over) == ALIGN, over
+
+
+def test_current_device_is_asked_for_in_public(lib, monkeypatch):
+    """The helper behind every call goes by torch.cuda.current_device(): the call is made at once where it is the operands'."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    got = []
+    lora._call_on(3, 17, lambda *a: got.append(a) or 0, "a", "b")
+    assert got == [("a", "b", 17)]
+    with pytest.raises(LoraError):
+        lora._call_on(3, 17, lambda *a: SHAPE)
