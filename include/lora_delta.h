@@ -535,7 +535,8 @@ LORA_API int lora_mx_linear(void *y, int64_t ld_y, const lora_mx *x, const lora_
  *     z[i][o] = sum_j x[i][j] w[o][j] + bias[o] + addend[i][o]            fp32, o < n_w
  *     y[i][c] = act(z[i][c]) + residual[i][c]                             n_w = d_out
  *     y[i][c] = act(z[i][c]) * z[i][d_out + c] + residual[i][c]           gated: n_w = 2 d_out
- * with fp32 sums in a fixed order and one rounding into y.  The adapters' delta comes in as the addend, ahead of the
+ * with fp32 sums and one rounding into y.  The order of the sums follows from the call's sizes and layout: equal calls give equal
+ * bits, and a row's last bits may differ between batches of different T.  The adapters' delta comes in as the addend, ahead of the
  * activation (lora_add_linear into zeros), or as the residual, behind it.
  *     LORA_ACT_NONE z;  _SILU z / (1 + e^-z);  _GELU z erfc(-z / sqrt 2) / 2;
  *     _GELU_TANH z / (1 + e^-2u), u = sqrt(2 / pi) (z + 0.044715 z^3);  _RELU 0 below 0, else z
