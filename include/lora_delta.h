@@ -542,7 +542,8 @@ LORA_API int lora_mx_linear(void *y, int64_t ld_y, const lora_mx *x, const lora_
  *     _GELU_TANH z / (1 + e^-2u), u = sqrt(2 / pi) (z + 0.044715 z^3);  _RELU 0 below 0, else z
  * (NaN stays NaN; -infinity gives NaN in all but NONE and RELU).  bf16 data runs on the tensor cores, fastest where rows
  * of x and w, and of y and the epilogue's operands, lie in steps of 16 bytes; fp32 data on the ordinary units, with fp32
- * products.
+ * products.  Rows of bf16 x and w off such steps are read in aligned pieces of 16 bytes, all that hold a part of a row: up to
+ * 14 bytes ahead of a row and behind it are read too, and dropped, whatever they hold and whoever writes them meanwhile.
  */
 typedef enum { LORA_ACT_NONE = 0, LORA_ACT_SILU = 1, LORA_ACT_GELU = 2, LORA_ACT_GELU_TANH = 3, LORA_ACT_RELU = 4 } lora_act;
 

@@ -394,9 +394,11 @@ __global__ void __launch_bounds__(pair_threads<MODE>(), 1) linear_pair_kernel(co
     } else if (MODE == LOADED && warp >= 2 && warp < FIRST_EPI) {
         // Rows at any (even) address: eight lanes read the aligned 16-byte pieces around 64 columns of a row, a ninth piece comes
         // from a load that a warp makes once for all its rows, and each lane shifts two neighbouring pieces into the 16 bytes
-        // that the operand's swizzle wants.  Pieces that hold no column of the row are not read.  Loads go out ahead of the
-        // wait for the slot; a slot's 32 KB in flight bound it, about 1 us a step (8192 x 4095 x 4096 717 us = 383 TFLOP/s, where 4096
-        // columns take 196).
+        // that the operand's swizzle wants.  Pieces that hold no column of the row are not read; of those at a row's ends up to
+        // 14 bytes are not the row's.  They share 16 aligned bytes, so a page, with bytes that are, and are dropped.  (By halves
+        // where a row ends: 64 x 4095 x 28672 162 -> 179 us, 33 x 129 x 2 x 4099 10.7 -> 19.3; only where x or w ends: 171, 18.6.)
+        // Loads go out ahead of the wait for the slot; a slot's 32 KB in flight bound it, about 1 us a step (8192 x 4095 x 4096
+        // 717 us = 383 TFLOP/s, where 4096 columns take 196).
         constexpr int W_IT = 4 * MT, X_IT = PAIR_ROWS / MT / 2 / 32, ITS = W_IT + X_IT, EXTRA = (ITS + 7) / 8;
         const int lw = warp - 2, lr = lane >> 3, c = lane & 7;   // rows 4 (lw + 8 i) + lr of W's, then of x's
         Ring ring(a.stages);

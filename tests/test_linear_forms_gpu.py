@@ -1,10 +1,47 @@
-"""lora_linear: equal calls."""
+"""lora_linear and lora_expert_linear over rows off 16-byte steps, at every offset of a row in its 16 bytes and with row ends in every
+part of them (all around the rows lies NaN, none of which may reach a sum); calls repeated."""
+import math
+
 import pytest
 import torch
 
 import lora_adapter_application_b200 as lora
+from dense_helpers import whole
 
 pytestmark = pytest.mark.gpu
+
+
+def _rows(t, off, pad):
+    """t's rows in bf16 from element `off` of a buffer of NaN, `pad` elements apart."""
+    rows, d = t.shape
+    buf = torch.full((off + rows * (d + pad) + 8,), math.nan, dtype=torch.bfloat16, device="cuda")
+    v = buf[off:off + rows * (d + pad)].view(rows, d + pad)[:, :d]
+    v.copy_(t)
+    return v
+
+
+@pytest.mark.parametrize("grouped", [False, True])
+@pytest.mark.parametrize("T", [1, 3, 150])
+@pytest.mark.parametrize("d", [1, 2, 7, 9, 15, 17, 57, 63, 65, 71, 73, 127, 129, 135, 137, 193, 201, 263])
+def test_rows_at_every_offset(cuda_lib, T, d, grouped):
+    n, N = 10, 2
+    g = torch.Generator(device="cuda").manual_seed(d)
+    x, w = whole(g, (T, d), 2), whole(g, (N, n, d), 2)
+    ids = (torch.arange(T) % N).int()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    meta = lora.Meta(T, N, min_run=0)
+    lora.lora_build_segments(ids.cuda(), meta, status)
+    want = torch.einsum("td,tnd->tn", x, w[ids.cuda().long()] if grouped else w[:1].expand(T, n, d)).bfloat16()   # exact in any order
+    for off in range(8):
+        for pad in (0, 1, 2, 6):
+            y = torch.full((T, n), 7.0, dtype=torch.bfloat16, device="cuda")
+            xs, ws = _rows(x, off, pad), _rows(w.view(N * n, d), (3 * off + 1) % 8, 0 if grouped else pad)
+            if grouped:
+                lora.lora_expert_linear(y, xs, ws.view(N, n, d), meta, status)
+            else:
+                lora.lora_linear(y, xs, ws[:n], status)
+            assert torch.equal(y, want), (off, pad)
+    assert int(status.item()) == 0
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
