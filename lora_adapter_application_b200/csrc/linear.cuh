@@ -24,8 +24,11 @@ struct LinArgs {
 // ------------------------------------------------------------------ epilogue
 // silu and both gelus as quotients or products without cancellation: z / (1 + e^-z) and z erfc(-z / sqrt 2) / 2 keep their
 // relative accuracy where z is far below 0, which z (1 + erf) / 2 and z (1 + tanh) / 2 lose.
-// FAST (results rounded to bf16): the approximate base-2 exponential and reciprocal, about 2^-20 relative at |z| <= 20, far below
-// bf16's 2^-9; for fp32 results the accurate functions.
+// FAST (results rounded to bf16, off by up to 2^-8 of themselves): the approximate base-2 exponential and reciprocal; for fp32
+// results the accurate functions.  The exponential multiplies its argument's rounding by the argument u (silu: u = z), so both
+// are within (9 + 3.2 |u|) 2^-23 of the value.  With exponential and reciprocal rounded exactly, silu is off by 2^-19.9 at worst
+// for |z| <= 20, the tanh form of gelu by as much up to |z| = 3, then by more, where the value goes to 0: 2^-15.8 at z = -9.8
+// (a value of 1e-35).
 template <bool FAST>
 __device__ __forceinline__ float over_one_plus_exp(float z, float u) {   // z / (1 + e^-u)
     if (!FAST) return z / (1.f + expf(-u));
@@ -34,9 +37,12 @@ __device__ __forceinline__ float over_one_plus_exp(float z, float u) {   // z / 
     asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(1.f + e));
     return z * r;
 }
-// z Phi(z) = z erfc(-z / sqrt 2) / 2.  For a = |z| / sqrt 2: erfc(a) = t e^(-a^2 + g(t)), t = 1 / (1 + a / 2), with g a polynomial of degree 9
-// fitted to ln(erfc(a) e^(a^2) / t) over a in [0, 15] (minimax, in 64 bits: off by 6.3e-8), times log2 e here; in all within
-// (8 + z^2) 2^-23 of the value, z^2 from the rounding of the exponent.  A third of the instructions of erfcf: 4126 x 1024 x 13536 with this activation 201 -> 139 us.
+// z Phi(z) = z erfc(-z / sqrt 2) / 2.  For a = |z| / sqrt 2: erfc(a) = t e^(-a^2 + g(t)), t = 1 / (1 + a / 2), the form of Press
+// et al., Numerical Recipes (error function, Chebyshev fit).  g is a polynomial of degree 9 of our own: least squares to
+// ln(erfc(a) e^(a^2) / t) in 64 bits on the 4000 Chebyshev nodes of t in [2/17, 1] (a in [0, 15]), weights of the squares started
+// at 1 and 200 times multiplied by each node's error (Lawson's iteration), which leaves the largest error smallest: 6.3e-8; then
+// in powers of t, times log2 e, rounded to fp32: 1.9e-7 (1.6 units of 2^-23, at a = 0.04).  In all within (8 + z^2) 2^-23 of the
+// value, z^2 from the rounding of the exponent.  A third of the instructions of erfcf: 4126 x 1024 x 13536 with this activation 201 -> 140 us.
 __device__ __forceinline__ float gelu_fast(float z) {
     float t, e;
     asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(t) : "f"(fmaf(fabsf(z), 0.35355339059327376f, 1.f)));

@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(32 * DOT_WARPS) linear_dot_kernel(const LinArg
 
 // --------------------------------------------------------------- many rows
 // BM rows x BN features of W (gated: BN / 2 of each half), TM x TN sums a thread, KG groups of threads that take a part of each
-// k tile each (where tiles are few: more warps on an SM) and add their sums at the end, in order; k in tiles of 32 that cp.async brings into
+// k tile each (where tiles are few: more warps on an SM) and add their sums at the end, in order; k in tiles of TILE_K that cp.async brings into
 // a ring of STAGES: 16 bytes a copy, or 4 where rows are off 16-byte steps.  Rows lie TILE_K + 4 floats apart: a thread reads four
 // k of a row at once, eight neighbours eight rows of W in eight different bank groups.  A thread's features are BN / TN
 // apart, so a gated tile's gate and up sums of a column meet in one thread, and neighbours store neighbouring columns.
@@ -268,12 +268,17 @@ int launch_as(const LinArgs &a, int sms, cudaStream_t st) {
     // row tiles that a grouping may have: whole ones, and a last one for each expert that has rows
     auto row_tiles = [&](int rows) { return a.perm ? a.T / rows + std::min(a.N, a.T) : (a.T + rows - 1) / rows; };
     const int per_group = a.perm ? (a.T + a.N - 1) / a.N : a.T;
+    // Few rows a group, by the mean, which is what the host knows (us, few-row kernel / 32 x 64 tiles): 8 x 4096 x 4096 50 / 90, 16 76 / 87,
+    // 32 127 / 87; over wide outputs the tiles win earlier, 12 x 4096 x 14336 160 / 176, 16 211 / 173.  The mean counts experts
+    // without rows: of 1024 experts (512 -> 256) 8192 slots spread evenly take 777 / 432, with 90 % of them in four 697 / 350.
     if (per_group <= 2 * DOT_ROWS) {
         const int cols = DOT_WARPS * DOT_FEATURES / (GATED ? 2 : 1);
         const int tiles = row_tiles(DOT_ROWS);   // a few thousand of them at most, and 65536 blocks of features
         return launch_after(linear_dot_kernel<GATED>, dim3(tiles * ((a.d_out + cols - 1) / cols)), 32 * DOT_WARPS, 0, 0, st, a, vec, tiles);
     }
-    // the largest tile that gives every SM one (64 x 4096 x 14336: 263 us on 64 x 64, 384 on 32 x 64).
+    // the largest tile that gives every SM one (us on 32 x 64 / 64 x 64 / 128 x 64: 64 x 4096 x 4096 87 / 149 / 278, 64 x 4096 x 9472
+    // 172 / 149 / 321, 64 x 4096 x 14336 341 / 264 / 533, 128 x 4096 x 4096 172 / 227 / 273, 256 x 4096 x 4096 341 / 263 / 420,
+    // 512 x 4096 x 4096 597 / 508 / 490, 1024 x 2048 x 2048 317 / 263 / 251, 333 x 1003 x 777 35 / 70 / 94).
     // Two blocks of 256 threads share an SM, for the four registers that this spills: with one, 64 x 4096 x 14336, a
     // wave and a half of tiles, takes 295 us, and 512 x 4096 x 4096 508 instead of 487.
     auto tiles = [&](int bm, int bn) { return (int64_t)row_tiles(bm) * ((a.n_w + bn - 1) / bn); };

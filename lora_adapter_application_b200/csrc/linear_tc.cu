@@ -22,7 +22,7 @@
 // (8192 x 4096 x 2 x 14336 1190 us = 1620 TFLOP/s in a short burst, 1417 at the power cap; the issuing warp waits for no
 // operands: 513 clocks a step of 512).  Between, 100 to 1000 rows: the operands' way into shared memory, about 64 bytes a
 // clock and SM, and the exchange (257 x 14336 x 4096 34.7 us, its floor 19.7).  Many rows, few columns: the epilogue's latencies
-// (4126 x 128 x 13536 72 us, 1.6 TB/s).  Many small experts (8192 tokens, 4 of 64, 2048 x
+// (4126 x 128 x 13536 74 us, 1.6 TB/s).  Many small experts (8192 tokens, 4 of 64, 2048 x
 // 2 x 1024: 240 us): 630 clocks a step where dense rows take 513, at 1.35 GHz under the power cap.
 //
 // Measured and dropped: 16-bit accesses of y and the operands straight from tensor memory's layout (see the epilogue); one accumulator
@@ -723,7 +723,9 @@ int consider(const LinArgs &l, bool gated, int bn, int64_t row_tiles, int64_t li
     const int rc = pair_fit<MODE, MT, KT>(dev, &fit);
     if (rc != LORA_OK) return rc;
     const int64_t m = m_tiles_of(l, gated, MT), n_k = (l.d_in + 64 * KT - 1) / (64 * KT);
-    // a 64-column step: its products, its copies into shared memory, or what a step takes at least (ns)
+    // a 64-column step: its products, its copies into shared memory, or what a step takes at least (ns); rows off 16-byte steps: 1000
+    // whatever the tile, which chose the best plan of all at 8192 x 4095 x 4096, 2048 x 2047 x 2 x 2048, 257 x 14335 x 4096, 700 x 1001 x 600, 64 x
+    // 4095 x 28672 and 64 x 4095 x 2 x 4096, but (2, 32, 4), 42 us, for (1, 32, 3), 28, at 1 x 4095 x 4096
     const int64_t step = std::max<int64_t>({(int64_t)MT * bn * 8 / 7, (16384 * MT + 64 * bn) / 112, MODE == LOADED ? 1000 : 90});
     const int64_t sums = 500 + 25 * bn * MT;   // a tile's epilogue, beside the next tile's products
     const int64_t hbm = ((int64_t)std::min<int64_t>(l.N, likely) * l.n_w * l.d_in + (int64_t)l.T * (l.d_in + l.d_out)) * 2 / 6400;
