@@ -120,7 +120,7 @@ int launch_route(int32_t *ids, float *weights, const void *logits, int64_t ld, i
 // rows in slot order, then the residual, fp32, one rounding: ahead of the rows a residual, larger than they are, would have
 // every sum rounded at its size (33 x 8 x 2048 in fp32, four times a row: 7.0e-8 off the value for 2.6e-8).  The tokens' ids
 // and weights come in one load of the warp, ahead of all; four rows' loads are in flight at a time.  Bound: HBM (8192 x 4 x
-// 4096 with a residual 64.4 us, 95 % of the measured copy rate; with a block for each token 68.0).
+// 4096 with a residual 64.1 us, 96 % of the measured copy rate; with a block for each token 68.0).
 constexpr int SUM_WARPS = 4, SUM_TOKENS = 4;
 
 template <typename E, bool VEC>
@@ -140,7 +140,9 @@ __global__ void __launch_bounds__(32 * SUM_WARPS) sum_kernel(E *y, int64_t ld_y,
     const float my_w = lane < here * k ? weights[t0 * k + lane] : 0.f;
     for (int i = 0; i < here; ++i) {
         const int64_t t = t0 + i;
-        float acc[8] = {}, v[8];
+        float acc[8], v[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[c] = -0.f;   // -0: added to a residual of -0 it leaves it so
         Raw r;
         for (int j = 0; j < k; j += 4) {
             Raw u[4];
@@ -168,9 +170,12 @@ __global__ void __launch_bounds__(32 * SUM_WARPS) sum_kernel(E *y, int64_t ld_y,
         if (res) {
             if (!VEC) load8<VEC>(res + t * ld_r, c0, d, lane, r);
             raw_values(r, v);
+        } else {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) acc[c] += v[c];
+            for (int c = 0; c < 8; ++c) v[c] = 0.f;
         }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[c] += v[c];
         Raw u;
         raw_round(acc, u);
         store8<VEC>(y + t * ld_y, c0, d, lane, u);
@@ -183,7 +188,8 @@ int launch_sum(void *y, int64_t ld_y, const void *x, int64_t ld_x, const int32_t
     const bool vec = mx_vec(x, ld_x, d, sizeof(E)) && mx_vec(y, ld_y, d, sizeof(E)) && (!res || mx_vec(res, ld_r, d, sizeof(E)));
     // several tokens a warp only where many: a block of one token lives mostly for the latency of its ids (us, one / several, bf16:
     // 1024 x 4 x 4096 10.2 / 10.9, 4096 34.0 / 33.2, 8192 68.0 / 63.7; 1024 x 2 x 512 2.2 / 3.9, 16384 19.1 / 15.3; not worth it at
-    // eight slots, 4096 x 8 x 2048 27.8 / 30.9, 16384 99 / 102; fp32 within 3 % from 4096 on, but for 8192 x 2 x 512 13.0 / 13.8)
+    // eight slots, 4096 x 8 x 2048 27.8 / 30.9, 16384 99 / 102; fp32 within 3 % from 4096 on, at 512
+    // columns 4096 x 2 6.8 / 7.2, 8192 13.0 / 13.8, 16384 25.0 / 23.8)
     const int tokens = T >= 4096 ? std::max(1, std::min(SUM_TOKENS, 32 / k)) : 1;
     const dim3 grid((unsigned)((T + tokens - 1) / tokens), (unsigned)((d + 256 * SUM_WARPS - 1) / (256 * SUM_WARPS)));
     return launch_after(vec ? sum_kernel<E, true> : sum_kernel<E, false>, grid, 32 * SUM_WARPS, 0, 0, st, static_cast<E *>(y), ld_y,

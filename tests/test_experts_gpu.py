@@ -382,3 +382,18 @@ def test_sum_adds_the_residual_last(cuda_lib, T, d):
     y = torch.full((T, d), 2.0 ** 24, device="cuda")
     lora.lora_expert_sum(y, x, torch.zeros(T, k, dtype=torch.int32, device="cuda"), w, 1, residual=y)
     assert (y == 2.0 ** 24 + 4).all()
+
+
+@pytest.mark.parametrize("T", [3, 4099])
+@pytest.mark.parametrize("d", [264, 259])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_sum_leaves_tokens_without_experts_bit_for_bit(cuda_lib, T, d, dtype):
+    """A residual of -0 stays -0 where no slot adds to it; without a residual the sum of nothing is 0."""
+    k = 3
+    ids = torch.where(torch.arange(T) % 2 == 0, -1, 0).int()[:, None].expand(T, k).contiguous().cuda()
+    x, w = torch.ones(T * k, d, dtype=dtype, device="cuda"), torch.zeros(T, k, device="cuda")
+    y = torch.full((T, d), -0.0, dtype=dtype, device="cuda")
+    lora.lora_expert_sum(y, x, ids, w, 1, residual=y)
+    assert torch.equal(torch.signbit(y), (ids[:, :1] < 0).expand(T, d)) and (y == 0).all()   # 0 * 1 + -0 = 0
+    lora.lora_expert_sum(y, x, ids, w, 1)
+    assert not torch.signbit(y).any() and (y == 0).all()
